@@ -1,0 +1,477 @@
+// Products of many tokens with packed 3-bit matrices, their input gradients and
+// the gated feed-forward block.
+//
+//   y[m][n]  = sum_k x[m][k] w[n][k]          (q3_gemm)
+//   dx[m][k] = sum_n dy[m][n] w[n][k]         (q3_gemm_backward)
+//   h[m][i]  = act(x . w[i]) * (x . w[I + i]) (q3_glu)
+//
+// Up to 64 tokens a product is bound by the packed weights, and q3_linear.hip's
+// kernels read them once.  For more tokens it is bound by the matrix cores, and
+// dequantising inside the product would repeat the vector work for every block
+// of tokens; so the matrix is widened once, exactly, to bf16 in the caller's
+// workspace (for the gradient: transposed) and all three run on one kernel:
+// C = A B^T with both operands bf16 and contiguous along the summed axis.
+#include "q3_act.h"
+#include "q3_device.h"
+#include "q3_internal.h"
+
+namespace q3 {
+namespace {
+
+// ---- widening -----------------------------------------------------------------
+
+// One wave per (16-row tile, 512-k step): lane l holds row l%16 and groups
+// 4*(l/16)..+3, as the planes are laid out, and writes its 128 weights.
+// out [n][gp*32]; groups past G are written as zeros.
+__global__ __launch_bounds__(256) void widen_kernel(PlaneView w, uint16_t* __restrict__ out, int64_t units, int steps) {
+  const int lane = threadIdx.x & 63;
+  const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (unit >= units) return;
+  const int i = lane & 15, kb = lane >> 4;
+  const int64_t tile = unit / steps;
+  const uint32_t s = (uint32_t)(unit - tile * steps);
+  const uint32_t gp = (uint32_t)((w.groups + 3) & ~3);
+  const uint32_t q = step_quads(s, gp);
+  const int64_t row = tile * 16 + i;
+  if ((uint32_t)kb >= q || row >= w.n) return;
+  const uint8_t* c = w.code + tile * (int64_t)(192u * gp) + 3072u * s;
+  u32x4 d[3];
+#pragma unroll
+  for (int j = 0; j < 3; ++j) d[j] = *reinterpret_cast<const u32x4*>(c + 16u * (16u * (q * j + kb) + i));
+  const uint32_t sc = *reinterpret_cast<const uint32_t*>(w.scale + tile * (int64_t)(16u * gp) + 256u * s +
+                                                         4u * (16u * kb + i));
+  const u32x2 cb = *reinterpret_cast<const u32x2*>(w.cb + row * 8);
+  uint16_t* o = out + row * (int64_t)(gp * 32u) + s * 512u + kb * 128u;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    bf16x2 v[16];
+    dequant_group_bf16(d[0][t], d[1][t], d[2][t], (sc >> (8 * t)) & 255u, cb.x, cb.y, v);
+    const bool real = (int)(s * 16u + kb * 4u + t) < w.groups;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      u32x4 u;
+#pragma unroll
+      for (int f = 0; f < 4; ++f) u[f] = real ? __builtin_bit_cast(uint32_t, v[4 * e + f]) : 0u;
+      *reinterpret_cast<u32x4*>(o + 32 * t + 8 * e) = u;
+    }
+  }
+}
+
+// Transposed: out [k][np], np = n padded to 64 with zeros.  A block takes 64
+// rows (a tile per wave) and one 512-k step, a group of each quad at a time
+// through LDS.
+__global__ __launch_bounds__(256) void widen_t_kernel(PlaneView w, uint16_t* __restrict__ out, int64_t np) {
+  constexpr int kPad = 72;   // 64 rows and 16 bytes against bank conflicts
+  __shared__ uint16_t buf[128 * kPad];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int i = lane & 15, kb = lane >> 4;
+  const uint32_t s = blockIdx.y;
+  const int64_t tile = (int64_t)blockIdx.x * 4 + wave;
+  const uint32_t gp = (uint32_t)((w.groups + 3) & ~3);
+  const uint32_t q = step_quads(s, gp);
+  const int64_t row = tile * 16 + i;
+  const bool ok = (uint32_t)kb < q && row < w.n;
+  u32x4 d[3] = {};
+  uint32_t sc = 0;
+  u32x2 cb = {0u, 0u};
+  if (ok) {
+    const uint8_t* c = w.code + tile * (int64_t)(192u * gp) + 3072u * s;
+#pragma unroll
+    for (int j = 0; j < 3; ++j) d[j] = *reinterpret_cast<const u32x4*>(c + 16u * (16u * (q * j + kb) + i));
+    sc = *reinterpret_cast<const uint32_t*>(w.scale + tile * (int64_t)(16u * gp) + 256u * s + 4u * (16u * kb + i));
+    cb = *reinterpret_cast<const u32x2*>(w.cb + row * 8);
+  }
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    bf16x2 v[16];
+    dequant_group_bf16(d[0][t], d[1][t], d[2][t], (sc >> (8 * t)) & 255u, cb.x, cb.y, v);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const uint32_t u = ok ? __builtin_bit_cast(uint32_t, v[e]) : 0u;
+      buf[(kb * 32 + 2 * e) * kPad + wave * 16 + i] = (uint16_t)u;
+      buf[(kb * 32 + 2 * e + 1) * kPad + wave * 16 + i] = (uint16_t)(u >> 16);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int at = c * 256 + threadIdx.x, r = at >> 3, p = at & 7;   // k row r of the 128, 8 columns
+      const int64_t k = (int64_t)s * 512 + (r >> 5) * 128 + t * 32 + (r & 31);
+      if (k < (int64_t)w.groups * 32)
+        *reinterpret_cast<u32x4*>(out + k * np + (int64_t)blockIdx.x * 64 + 8 * p) =
+            *reinterpret_cast<const u32x4*>(&buf[r * kPad + 8 * p]);
+    }
+    __syncthreads();
+  }
+}
+
+// dy rows padded with zeros to np columns (only when n % 8 leaves a 16-byte
+// piece half filled with what the caller keeps behind the row).
+__global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* __restrict__ src, int64_t ld, int64_t n,
+                                                       uint16_t* __restrict__ dst, int64_t np) {
+  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (c < np) dst[(int64_t)blockIdx.y * np + c] = c < n ? src[(int64_t)blockIdx.y * ld + c] : 0;
+}
+
+// ---- C = A B^T ------------------------------------------------------------------
+
+enum Epilogue : int { kStoreF32 = 0, kGlu = 1 };
+
+struct GemmArgs {
+  const uint16_t* a;   // [m][lda], a multiple of 8 columns valid
+  int64_t lda;
+  const uint16_t* b;   // [rows][ldb]
+  int64_t ldb;
+  int64_t m, n;        // outputs (kGlu: n = I, b holds 2I rows)
+  int64_t k;           // summed columns of a (k % 8 == 0); b is zero from there to the next multiple of 64
+  float* c;
+  int64_t ldc;
+  int vec;             // c rows 16-byte aligned
+  // kGlu
+  uint16_t* h;
+  int64_t ldh;
+  float* pre;
+  int64_t ld_pre;
+  int act;
+  int tiles_m, tiles_n;
+};
+
+// One wave's 1 KB from memory to LDS: lane l's 16 bytes at voff + soff land at
+// dst + 16 l (dst is wave-uniform).
+__device__ __forceinline__ void load_lds16(rsrc_t r, uint8_t* dst, uint32_t voff, uint32_t soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, voff, soff, 0, 0);
+}
+
+// Block of WM x WN waves on a BM x BN tile (tokens x weight rows), 64 of the
+// summed axis at a time through two LDS buffers filled by direct-to-LDS loads.
+// A buffer row is 128 bytes in 8 chunks of 16; row r keeps chunk c at position
+// c ^ (r & 7) (the loads permute which chunk a lane fetches), so the 16 rows a
+// fragment read touches fall on distinct banks.  Weights are the MFMA's A
+// operand: a lane then holds four consecutive weight rows of one token, which
+// leave in one store.
+// kGlu: the 16 TN weight rows of a wave are 8 TN gate rows and the 8 TN up
+// rows of the same outputs, so the product is formed in registers.
+template <int BM, int BN, int WM, int WN, int kEpi>
+__global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
+  constexpr int kW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
+  constexpr uint32_t kABytes = BM * 128, kBuf = (BM + BN) * 128;
+  constexpr int kOut = kEpi == kGlu ? BN / 2 : BN;   // outputs per tile
+  extern __shared__ __align__(16) uint8_t lds[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+
+  // Tiles go to the 8 XCDs in contiguous runs (blocks are dealt round robin),
+  // and inside a run in columns of up to 8 token tiles, so the blocks that
+  // share an L2 share operand tiles.
+  const int total = g.tiles_m * g.tiles_n;
+  const int id = blockIdx.x, xcd = id & 7, per = total >> 3, rem = total & 7;
+  const int t = xcd * per + (xcd < rem ? xcd : rem) + (id >> 3);
+  const int gsize = 8 * g.tiles_n, grp = t / gsize, in = t - grp * gsize;
+  const int gm = g.tiles_m - grp * 8 < 8 ? g.tiles_m - grp * 8 : 8;
+  const int64_t m0 = (int64_t)(grp * 8 + in % gm) * BM;
+  const int64_t n0 = (int64_t)(in / gm) * kOut;
+
+  const int64_t rows_a = g.m - m0 < BM ? g.m - m0 : BM;
+  const rsrc_t ra = make_rsrc(g.a + m0 * g.lda, (uint32_t)(((rows_a - 1) * g.lda + g.k) * 2));
+  const int r8 = lane >> 3, chunk = (lane & 7) ^ r8;
+  const uint32_t lda2 = (uint32_t)g.lda * 2u, ldb2 = (uint32_t)g.ldb * 2u;
+  const uint32_t va = (uint32_t)r8 * lda2, vb = (uint32_t)r8 * ldb2 + 16u * chunk;
+  // Weight rows of the tile in runs of 8: first row of run j (wave-uniform).
+  auto b_row = [&](int j) -> int64_t {
+    if constexpr (kEpi == kGlu) {
+      constexpr int kHalf = 8 * TN;   // outputs per wave
+      const int wcol = 8 * j / (16 * TN), o = 8 * j % (16 * TN);
+      return n0 + wcol * kHalf + (o < kHalf ? o : g.n + o - kHalf);
+    } else {
+      return n0 + 8 * j;
+    }
+  };
+  constexpr int kLoadsA = BM / 8 / kW, kLoadsB = BN / 8 / kW;
+  static_assert(BM % (8 * kW) == 0 && BN % (8 * kW) == 0, "whole loads per wave");
+  const uint16_t* pb[kLoadsB];
+  uint32_t vbl[kLoadsB];
+#pragma unroll
+  for (int q = 0; q < kLoadsB; ++q) {
+    const int64_t row = b_row(wave * kLoadsB + q);
+    const int64_t end = kEpi == kGlu ? (row < g.n ? g.n : 2 * g.n) : g.n;
+    pb[q] = g.b + row * g.ldb;
+    vbl[q] = row + r8 < end && (kEpi != kGlu || row < 2 * g.n) ? vb : kOob;
+  }
+  uint32_t val[kLoadsA];
+#pragma unroll
+  for (int q = 0; q < kLoadsA; ++q)
+    val[q] = m0 + 8 * (wave * kLoadsA + q) + r8 < g.m ? va : kOob;
+
+  auto load = [&](int s, uint32_t buf) {
+    // Chunks past k (only in the last step) read the row's first chunk of the
+    // step instead: finite values that meet b's zeros.
+    const uint32_t ca = 64 * (int64_t)s + 8 * chunk < g.k ? 16u * chunk : 0u;
+#pragma unroll
+    for (int q = 0; q < kLoadsA; ++q) {
+      const uint32_t row8 = (uint32_t)(wave * kLoadsA + q) * 8u;
+      load_lds16(ra, lds + buf + row8 * 128u, val[q] + ca, row8 * lda2 + 128u * (uint32_t)s);
+    }
+#pragma unroll
+    for (int q = 0; q < kLoadsB; ++q) {
+      const uint32_t row8 = (uint32_t)(wave * kLoadsB + q) * 8u;
+      load_lds16(make_rsrc(pb[q], 8u * ldb2), lds + buf + kABytes + row8 * 128u, vbl[q], 128u * (uint32_t)s);
+    }
+  };
+
+  f32x4 acc[TN][TM];
+#pragma unroll
+  for (int n = 0; n < TN; ++n)
+#pragma unroll
+    for (int m = 0; m < TM; ++m) acc[n][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // Fragment address: row lane%16 of a 16-row tile, chunk lane/16 (+4 for the
+  // second half of the step), swizzled.
+  const uint32_t frag = (uint32_t)(lane & 15) * 128u + (((uint32_t)lane >> 4) ^ ((uint32_t)lane & 7u)) * 16u;
+  const uint32_t fa = (uint32_t)(wm * TM * 16) * 128u + frag;
+  const uint32_t fb = kABytes + (uint32_t)(wn * TN * 16) * 128u + frag;
+  const int steps = (int)((g.k + 63) / 64);
+  if (steps > 0) load(0, 0u);
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  uint32_t buf = 0;
+  for (int s = 0; s < steps; ++s) {
+    if (s + 1 < steps) load(s + 1, kBuf - buf);
+#pragma unroll
+    for (uint32_t half = 0; half < 2; ++half) {
+      bf16x8 wv[TN], xv[TM];
+#pragma unroll
+      for (int n = 0; n < TN; ++n)
+        wv[n] = *reinterpret_cast<const bf16x8*>(lds + buf + ((fb + n * 2048u) ^ (64u * half)));
+#pragma unroll
+      for (int m = 0; m < TM; ++m)
+        xv[m] = *reinterpret_cast<const bf16x8*>(lds + buf + ((fa + m * 2048u) ^ (64u * half)));
+#pragma unroll
+      for (int n = 0; n < TN; ++n)
+#pragma unroll
+        for (int m = 0; m < TM; ++m)
+          acc[n][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[n], xv[m], acc[n][m], 0, 0, 0);
+    }
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    buf = kBuf - buf;
+  }
+
+  // Lane l holds weight rows 4*(l/16)..+3 of each tile for token l%16.
+#pragma unroll
+  for (int m = 0; m < TM; ++m) {
+    const int64_t token = m0 + (wm * TM + m) * 16 + (lane & 15);
+    if (token >= g.m) continue;
+    if constexpr (kEpi == kGlu) {
+      constexpr int kHalfT = TN / 2;
+#pragma unroll
+      for (int n = 0; n < kHalfT; ++n) {
+        const int64_t i = n0 + wn * 8 * TN + n * 16 + 4 * (lane >> 4);
+        if (i >= g.n) continue;   // n is a multiple of 32
+        const f32x4 ga = acc[n][m], up = acc[n + kHalfT][m];
+        float h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = act_value(g.act, ga[e]) * up[e];
+        const bf16x2 h0 = {static_cast<__bf16>(h[0]), static_cast<__bf16>(h[1])};
+        const bf16x2 h1 = {static_cast<__bf16>(h[2]), static_cast<__bf16>(h[3])};
+        *reinterpret_cast<u32x2*>(g.h + token * g.ldh + i) =
+            u32x2{__builtin_bit_cast(uint32_t, h0), __builtin_bit_cast(uint32_t, h1)};
+        if (g.pre) {
+          *reinterpret_cast<f32x4*>(g.pre + token * g.ld_pre + i) = ga;
+          float* pu = g.pre + token * g.ld_pre + g.n + i;   // n % 32 == 0 keeps the alignment
+          *reinterpret_cast<f32x4*>(pu) = up;
+        }
+      }
+    } else {
+      float* c = g.c + token * g.ldc;
+#pragma unroll
+      for (int n = 0; n < TN; ++n) {
+        const int64_t i = n0 + (wn * TN + n) * 16 + 4 * (lane >> 4);
+        if (g.vec && i + 3 < g.n) {
+          *reinterpret_cast<f32x4*>(c + i) = acc[n][m];
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (i + e < g.n) c[i + e] = acc[n][m][e];
+        }
+      }
+    }
+  }
+}
+
+template <int BM, int BN, int WM, int WN, int kEpi>
+hipError_t launch_gemm_one(GemmArgs g, hipStream_t s) {
+  constexpr int kOut = kEpi == kGlu ? BN / 2 : BN;
+  constexpr size_t shm = 2 * (BM + BN) * 128;
+  static LdsAllowance seen;
+  const hipError_t e =
+      allow_dynamic_lds(reinterpret_cast<const void*>(gemm_kernel<BM, BN, WM, WN, kEpi>), shm, seen);
+  if (e != hipSuccess) return e;
+  const int64_t tm = (g.m + BM - 1) / BM, tn = (g.n + kOut - 1) / kOut;
+  if (tm * tn > 0x7FFFFFFF) return hipErrorInvalidValue;
+  g.tiles_m = (int)tm;
+  g.tiles_n = (int)tn;
+  hipLaunchKernelGGL((gemm_kernel<BM, BN, WM, WN, kEpi>), dim3((unsigned)(tm * tn)), dim3(64 * WM * WN), shm, s, g);
+  return hipGetLastError();
+}
+
+template <int kEpi>
+hipError_t launch_gemm_pick(const GemmArgs& g, hipStream_t s) {
+  const int64_t cols = kEpi == kGlu ? 2 * g.n : g.n;
+  const int64_t big = ((g.m + 255) / 256) * ((cols + 255) / 256);
+  if (big >= 192) return launch_gemm_one<256, 256, 2, 4, kEpi>(g, s);
+  return launch_gemm_one<128, 128, 2, 2, kEpi>(g, s);
+}
+
+int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
+int64_t padded_k(int64_t k) { return (k + 127) / 128 * 128; }
+int64_t padded_n(int64_t n) { return (n + 63) / 64 * 64; }
+constexpr int64_t kSmallM = 64;
+
+hipError_t launch_widen(const PlaneView& w, uint16_t* out, hipStream_t s) {
+  const uint32_t gp = (uint32_t)((w.groups + 3) & ~3);
+  const int steps = (int)((gp + 15) / 16);
+  const int64_t units = (w.n + 15) / 16 * steps;
+  hipLaunchKernelGGL(widen_kernel, dim3((unsigned)((units + 3) / 4)), dim3(256), 0, s, w, out, units, steps);
+  return hipGetLastError();
+}
+
+// The gradient of the gated pre-activations, four outputs per thread.
+__global__ __launch_bounds__(256) void glu_back_kernel(const float* __restrict__ pre, int64_t ld_pre,
+                                                       const float* __restrict__ dh, int64_t ld_dh, int act,
+                                                       int64_t quads, int64_t inter, uint16_t* __restrict__ dpre,
+                                                       int64_t ld_dpre) {
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (e >= quads) return;
+  const int64_t per = inter / 4, row = e / per, i = 4 * (e - row * per);
+  const f32x4 ga = *reinterpret_cast<const f32x4*>(pre + row * ld_pre + i);
+  const f32x4 up = *reinterpret_cast<const f32x4*>(pre + row * ld_pre + inter + i);
+  const f32x4 d = *reinterpret_cast<const f32x4*>(dh + row * ld_dh + i);
+  uint32_t og[2], ou[2];
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    float g2[2], u2[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      float a, da;
+      act_both(act, ga[2 * p + q], a, da);
+      g2[q] = d[2 * p + q] * up[2 * p + q] * da;
+      u2[q] = d[2 * p + q] * a;
+    }
+    const bf16x2 gb = {static_cast<__bf16>(g2[0]), static_cast<__bf16>(g2[1])};
+    const bf16x2 ub = {static_cast<__bf16>(u2[0]), static_cast<__bf16>(u2[1])};
+    og[p] = __builtin_bit_cast(uint32_t, gb);
+    ou[p] = __builtin_bit_cast(uint32_t, ub);
+  }
+  *reinterpret_cast<u32x2*>(dpre + row * ld_dpre + i) = u32x2{og[0], og[1]};
+  *reinterpret_cast<u32x2*>(dpre + row * ld_dpre + inter + i) = u32x2{ou[0], ou[1]};
+}
+
+}  // namespace
+
+int64_t gemm_workspace_bytes(int64_t n, int64_t k, int64_t m) {
+  if (m <= kSmallM) return gemm_small_m_workspace_bytes(n, k, m);
+  return align256(n * padded_k(k) * 2);
+}
+
+hipError_t launch_gemm(const PlaneView& w, const uint16_t* x, int64_t m, int64_t ldx, float* y, int64_t ldy, void* ws,
+                       hipStream_t s) {
+  const int64_t k = (int64_t)w.groups * 32;
+  if (w.n == 0) return hipSuccess;
+  if (m <= kSmallM)
+    return launch_gemm_small_m(w, x, m, ldx, y, ldy, ws, ws ? gemm_workspace_bytes(w.n, k, m) : 0, s);
+  uint16_t* wide = static_cast<uint16_t*>(ws);
+  const hipError_t e = launch_widen(w, wide, s);
+  if (e != hipSuccess) return e;
+  GemmArgs g{};
+  g.a = x;
+  g.lda = ldx;
+  g.b = wide;
+  g.ldb = padded_k(k);
+  g.m = m;
+  g.n = w.n;
+  g.k = k;
+  g.c = y;
+  g.ldc = ldy;
+  g.vec = (uintptr_t)y % 16 == 0 && ldy % 4 == 0;
+  return launch_gemm_pick<kStoreF32>(g, s);
+}
+
+int64_t gemm_backward_workspace_bytes(int64_t n, int64_t k, int64_t m) {
+  return align256(k * padded_n(n) * 2) + (n % 8 ? align256(m * padded_n(n) * 2) : 0);
+}
+
+hipError_t launch_gemm_backward(const PlaneView& w, const uint16_t* dy, int64_t m, int64_t ld_dy, float* dx,
+                                int64_t ld_dx, void* ws, hipStream_t s) {
+  const int64_t k = (int64_t)w.groups * 32, np = padded_n(w.n);
+  uint16_t* wide = static_cast<uint16_t*>(ws);
+  if (w.n > 0) {
+    const int steps = (int)(((w.groups + 3) / 4 + 3) / 4);
+    hipLaunchKernelGGL(widen_t_kernel, dim3((unsigned)(np / 64), (unsigned)steps), dim3(256), 0, s, w, wide, np);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  GemmArgs g{};
+  g.a = dy;
+  g.lda = ld_dy;
+  g.k = w.n;
+  if (w.n % 8) {
+    uint16_t* padded = wide + align256(k * np * 2) / 2;
+    for (int64_t r = 0; r < m; r += 65535) {   // grid rows of one launch
+      const int64_t rows = m - r < 65535 ? m - r : 65535;
+      hipLaunchKernelGGL(pad_rows_kernel, dim3((unsigned)((np + 255) / 256), (unsigned)rows), dim3(256), 0, s,
+                         dy + r * ld_dy, ld_dy, w.n, padded + r * np, np);
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    g.a = padded;
+    g.lda = np;
+    g.k = np;
+  }
+  g.b = wide;
+  g.ldb = np;
+  g.m = m;
+  g.n = k;
+  g.c = dx;
+  g.ldc = ld_dx;
+  g.vec = (uintptr_t)dx % 16 == 0 && ld_dx % 4 == 0;
+  return launch_gemm_pick<kStoreF32>(g, s);
+}
+
+int64_t glu_workspace_bytes(int64_t n_gu, int64_t k, int64_t m) {
+  return m <= kSmallM ? 0 : align256(n_gu * padded_k(k) * 2);
+}
+
+hipError_t launch_glu(const PlaneView& gate_up, const uint16_t* x, int64_t m, int64_t ldx, int32_t act, uint16_t* h,
+                      int64_t ldh, float* pre, int64_t ld_pre, void* ws, hipStream_t s) {
+  if (gate_up.n == 0) return hipSuccess;
+  if (m <= kSmallM) return launch_glu_small_m(gate_up, x, m, ldx, act, h, ldh, pre, ld_pre, s);
+  uint16_t* wide = static_cast<uint16_t*>(ws);
+  const hipError_t e = launch_widen(gate_up, wide, s);
+  if (e != hipSuccess) return e;
+  GemmArgs g{};
+  g.a = x;
+  g.lda = ldx;
+  g.b = wide;
+  g.ldb = padded_k((int64_t)gate_up.groups * 32);
+  g.m = m;
+  g.n = gate_up.n / 2;
+  g.k = (int64_t)gate_up.groups * 32;
+  g.h = h;
+  g.ldh = ldh;
+  g.pre = pre;
+  g.ld_pre = ld_pre;
+  g.act = act;
+  return launch_gemm_pick<kGlu>(g, s);
+}
+
+hipError_t launch_glu_backward(const float* pre, int64_t ld_pre, const float* dh, int64_t ld_dh, int32_t act,
+                               int64_t m, int64_t inter, uint16_t* dpre, int64_t ld_dpre, hipStream_t s) {
+  const int64_t quads = m * (inter / 4), blocks = (quads + 255) / 256;
+  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (quads == 0) return hipSuccess;
+  hipLaunchKernelGGL(glu_back_kernel, dim3((unsigned)blocks), dim3(256), 0, s, pre, ld_pre, dh, ld_dh, act, quads,
+                     inter, dpre, ld_dpre);
+  return hipGetLastError();
+}
+
+}  // namespace q3

@@ -108,6 +108,92 @@ hipError_t launch_moe_mlp(const ExpertView& gu, const ExpertView& dn, const uint
                           const int32_t* ids, int32_t t, int32_t topk, const float* logits, int64_t ld_logits,
                           uint16_t* h, float* part, int64_t ldp, float* out, int64_t ldo, hipStream_t s);
 
+// Residual norms (q3_norm.hip).  `vec`: every row starts on four elements and
+// n % 4 == 0.  Null pointers as in the C ABI.
+struct NormArgs {
+  const float* y;
+  int64_t ldy;
+  const float* post_w;
+  const float* gate;
+  int64_t ld_gate;   // 0: one row for all tokens
+  float scale, eps;
+  const void* r;
+  int64_t ldr;
+  void* r_out;
+  int64_t ldr_out;
+  const float* pre_w;
+  uint16_t* x;
+  int64_t ldx;
+  int64_t m;
+  int n;
+};
+hipError_t launch_residual_norm(const NormArgs& a, int32_t r_type, bool vec, hipStream_t s);
+
+// part_*: one row of n floats per group, added in group order by a second
+// launch into dpre, dpost and dgate_row (null: not wanted).
+struct NormBackArgs {
+  const float* y;
+  int64_t ldy;
+  const float* post_w;
+  const float* gate;
+  int64_t ld_gate;
+  float scale, eps;
+  const void* r;
+  int64_t ldr;
+  const float* pre_w;
+  const float* dx;
+  int64_t ld_dx;
+  const void* dr_out;
+  int64_t ld_dr_out;
+  void* dr;
+  int64_t ld_dr;
+  uint16_t* dy;
+  int64_t ld_dy;
+  float* dgate;
+  int64_t ld_dgate;
+  float* part_pre;
+  float* part_post;
+  float* part_gate;
+  int64_t groups;
+  int64_t m;
+  int n;
+};
+int64_t norm_back_groups(int64_t m, int n);
+hipError_t launch_residual_norm_back(const NormBackArgs& a, int32_t r_type, bool vec, float* dpre, float* dpost,
+                                     float* dgate_row, hipStream_t s);
+
+// Sampling (q3_sample.hip).
+struct SampleArgs {
+  const float* logits;
+  int64_t ld;
+  int m, n;
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  const float* u;
+  int32_t* tokens;
+  float* logprobs;
+};
+int64_t sample_workspace_bytes(int64_t m, int64_t n);
+hipError_t launch_sample(const SampleArgs& a, void* ws, hipStream_t s);
+
+// Gated feed-forward block and products of many tokens (q3_gemm.hip).
+int64_t gemm_workspace_bytes(int64_t n, int64_t k, int64_t m);
+hipError_t launch_gemm(const PlaneView& w, const uint16_t* x, int64_t m, int64_t ldx, float* y, int64_t ldy, void* ws,
+                       hipStream_t s);
+int64_t gemm_backward_workspace_bytes(int64_t n, int64_t k, int64_t m);
+hipError_t launch_gemm_backward(const PlaneView& w, const uint16_t* dy, int64_t m, int64_t ld_dy, float* dx,
+                                int64_t ld_dx, void* ws, hipStream_t s);
+int64_t glu_workspace_bytes(int64_t n_gu, int64_t k, int64_t m);
+hipError_t launch_glu(const PlaneView& gate_up, const uint16_t* x, int64_t m, int64_t ldx, int32_t act, uint16_t* h,
+                      int64_t ldh, float* pre, int64_t ld_pre, void* ws, hipStream_t s);
+hipError_t launch_glu_backward(const float* pre, int64_t ld_pre, const float* dh, int64_t ld_dh, int32_t act,
+                               int64_t m, int64_t inter, uint16_t* dpre, int64_t ld_dpre, hipStream_t s);
+// The dense gated product of up to 64 tokens, straight from the packed planes (q3_linear.hip).
+hipError_t launch_glu_small_m(const PlaneView& gate_up, const uint16_t* x, int64_t m, int64_t ldx, int32_t act,
+                              uint16_t* h, int64_t ldh, float* pre, int64_t ld_pre, hipStream_t s);
+
 // Dynamic LDS above 64 KB must be allowed per kernel on each device.  One
 // LdsAllowance per kernel (a zero-initialised static) remembers, per device,
 // the largest size already allowed, so later launches cost one atomic load.

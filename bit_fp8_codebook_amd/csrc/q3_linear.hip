@@ -45,6 +45,7 @@
 #include <atomic>
 #include <type_traits>
 
+#include "q3_act.h"
 #include "q3_device.h"
 #include "q3_internal.h"
 
@@ -76,7 +77,11 @@ enum Grouping : int {
   kDownTerms = 3,     // as kExperts with each pair's activation given as two bf16 rows (high
                       // and low term): the block adds the two products and stores one output
                       // row per pair
+  kDenseGlu = 4,      // every token against a gate/up matrix [gate I rows; up I rows]: a wave takes
+                      // gate tile q and up tile q and writes h = act(g) * u in bf16 (and g and u)
 };
+// Token/expert pairs from routing ids, rather than all tokens.
+constexpr bool routed(int grouping) { return grouping != kDense && grouping != kDenseGlu; }
 
 struct KArgs {
   const uint8_t* code;
@@ -101,9 +106,13 @@ struct KArgs {
   int slice_cap;   // expert passes in full-K mode: token rows the LDS staging holds (<= 16, even)
   int num_experts;
   // kSwiGLU: tiles in the gate half; output terms h[2*pair + term][I]
+  // (kDenseGlu: h[token][I]; pre, if not null, [token][g I; u I])
   int half_tiles;
   uint16_t* h;
   int64_t ldh;
+  int act;
+  float* pre;
+  int64_t ld_pre;
   // kDownTerms: per-pair outputs
   float* part;
   int64_t ldp;
@@ -362,6 +371,24 @@ __device__ __forceinline__ void stage_chunks(rsrc_t r, int count, uint8_t* lds, 
   }
 }
 
+// Four gated outputs i..i+3 of one token (kDenseGlu): h rounded once to bf16,
+// and the pre-activations where the caller keeps them.  I is a multiple of 32,
+// so the four are all inside.
+__device__ __forceinline__ void store_glu(const KArgs& a, int64_t token, int64_t i, f32x4 g, f32x4 u) {
+  float h[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) h[e] = act_value(a.act, g[e]) * u[e];
+  const bf16x2 h0 = {static_cast<__bf16>(h[0]), static_cast<__bf16>(h[1])};
+  const bf16x2 h1 = {static_cast<__bf16>(h[2]), static_cast<__bf16>(h[3])};
+  *reinterpret_cast<u32x2*>(a.h + token * a.ldh + i) =
+      u32x2{__builtin_bit_cast(uint32_t, h0), __builtin_bit_cast(uint32_t, h1)};
+  if (a.pre) {
+    float* p = a.pre + token * a.ld_pre + i;
+    *reinterpret_cast<f32x4*>(p) = g;
+    *reinterpret_cast<f32x4*>(p + 16 * (int64_t)a.half_tiles) = u;
+  }
+}
+
 // Waves per SIMD the register budget is held to (128 registers per lane for 4,
 // 256 for 2): a decode launch wants every wave resident at once.
 template <int NT, int R, bool kDot>
@@ -388,6 +415,7 @@ __device__ __forceinline__ uint32_t wave_or32(uint32_t v) {
 template <int NT, int R, int kW, int kGrouped, int kMode, bool kDot, int kBits>
 __global__ __launch_bounds__(64 * kW) __attribute__((amdgpu_waves_per_eu(min_waves_per_eu<NT, R, kDot>())))
 void linear_kernel(KArgs a) {
+  constexpr bool kRouted = routed(kGrouped);
   constexpr int kWd = kBits == 2 ? 2 : 3;          // code words per group
   constexpr uint32_t kCbBytes = kBits == 2 ? 4 : 8;   // codebook bytes per row
   constexpr int kThreads = 64 * kW;
@@ -396,7 +424,7 @@ void linear_kernel(KArgs a) {
   // Expert passes: each wave keeps its own copy of the block's (token, slot)
   // pairs, written and read by that wave alone, so no block barrier stands
   // between the ids and the first loads.
-  __shared__ int pairs_w[kGrouped ? kW : 1][64];
+  __shared__ int pairs_w[kRouted ? kW : 1][64];
 
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -410,7 +438,7 @@ void linear_kernel(KArgs a) {
 
   // ---- which expert / tokens -------------------------------------------------
   int expert = 0, npairs = 0;
-  if (kGrouped) {
+  if (kRouted) {
     // Every wave reads the round's ids and finds its block's expert and pairs
     // itself, so the planes' addresses and the first loads need no barrier.
     const int id = lane < a.pairs_total ? a.ids[lane] : -1;
@@ -429,7 +457,7 @@ void linear_kernel(KArgs a) {
     expert = __builtin_amdgcn_readfirstlane(e);
     const bool match = expert >= 0 && id == expert;
     const unsigned long long mask = __ballot(match);
-    if (match) pairs_w[kGrouped ? wave : 0][__popcll(mask & ((1ull << lane) - 1ull))] = lane;
+    if (match) pairs_w[kRouted ? wave : 0][__popcll(mask & ((1ull << lane) - 1ull))] = lane;
     npairs = __popcll(mask);
     // Order this wave's writes of its pairs before its reads of them.
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -437,8 +465,8 @@ void linear_kernel(KArgs a) {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     if (npairs == 0) return;   // not picked this round: no weight byte is read
   }
-  const int* const pairs = pairs_w[kGrouped ? wave : 0];
-  const int total_tokens = kGrouped == kDownTerms ? 2 * npairs : (kGrouped ? npairs : a.m);
+  const int* const pairs = pairs_w[kRouted ? wave : 0];
+  const int total_tokens = kGrouped == kDownTerms ? 2 * npairs : (kRouted ? npairs : a.m);
 
   const int G = a.G;
   const uint32_t gp = (uint32_t)((G + 3) & ~3);
@@ -448,7 +476,7 @@ void linear_kernel(KArgs a) {
   int64_t tix[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    if constexpr (kGrouped == kSwiGLU) {
+    if constexpr (kGrouped == kSwiGLU || kGrouped == kDenseGlu) {
       const int64_t q = (int64_t)blockIdx.x * rb + rg;
       tix[r] = q < a.half_tiles ? q + r * a.half_tiles : tiles;
     } else {
@@ -488,16 +516,16 @@ void linear_kernel(KArgs a) {
   // Tokens per slice: the matrix-core width, or for the expert passes in
   // full-K mode the rows their LDS was sized for (an expert meets each token at
   // most once per round, so one slice normally covers it).
-  const int cap = kGrouped && kMode == kShared ? a.slice_cap : kSlice;
+  const int cap = kRouted && kMode == kShared ? a.slice_cap : kSlice;
   for (int slice = 0; slice < total_tokens; slice += cap) {
     const int cnt = total_tokens - slice < cap ? total_tokens - slice : cap;
     // Token slot j of this slice -> its x row and y row.
     auto xrow = [&](int j) -> int {
       if (kGrouped == kDownTerms) return 2 * pairs[(slice + j) >> 1] + ((slice + j) & 1);
-      if (kGrouped) return a.x_by_slot ? pairs[slice + j] : pairs[slice + j] / a.topk;
+      if (kRouted) return a.x_by_slot ? pairs[slice + j] : pairs[slice + j] / a.topk;
       return slice + j;
     };
-    auto yrow = [&](int j) -> int { return kGrouped ? pairs[slice + j] : slice + j; };
+    auto yrow = [&](int j) -> int { return kRouted ? pairs[slice + j] : slice + j; };
     f32x4 acc[R][kDot ? 1 : NT];
     float dacc[R][kDot ? NT : 1];
 #pragma unroll
@@ -733,6 +761,12 @@ void linear_kernel(KArgs a) {
             *reinterpret_cast<u32x2*>(hr + a.ldh) = u32x2{lo[0], lo[1]};
           }
         }
+      } else if constexpr (kGrouped == kDenseGlu) {
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+          const int j = 16 * c + i;
+          if (j < cnt && tix[0] < a.half_tiles) store_glu(a, slice + j, tix[0] * 16 + 4 * kb, acc[0][c], acc[1][c]);
+        }
       } else if constexpr (kGrouped == kDownTerms) {
         // Token columns 2p and 2p+1 are the two terms of pair p: add the
         // neighbouring column, then the even lanes store the pair's outputs.
@@ -799,9 +833,11 @@ constexpr int kWideMinNT = 2;
 #endif
 constexpr int kWideWaves = 4;
 
-template <int NT, int R>
+// kGlu (R = 2): the wave's two row tiles are gate tile q and up tile q.
+template <int NT, int R, bool kGlu>
 __global__ __launch_bounds__(64 * kWideWaves) __attribute__((amdgpu_waves_per_eu(1)))
 void wide_kernel(KArgs a) {
+  static_assert(!kGlu || R == 2, "one gate and one up tile");
   constexpr int kW = kWideWaves, kSlice = 16 * NT;
   constexpr uint32_t rstride = 1024u + kRowPad;
   constexpr uint32_t buf_bytes = (uint32_t)kSlice * rstride;
@@ -815,6 +851,7 @@ void wide_kernel(KArgs a) {
   const uint32_t gp = (uint32_t)a.G;   // a multiple of 16 here
   const int64_t tiles = (a.n + 15) / 16;
   const int64_t tile0 = ((int64_t)blockIdx.x * kW + wave) * R;
+  const int64_t pair = (int64_t)blockIdx.x * kW + wave;   // kGlu
   Planes p;
   p.code = make_rsrc(a.code, (uint32_t)(tiles * 192 * gp));
   p.scale = make_rsrc(a.scale, (uint32_t)(tiles * 16 * gp));
@@ -828,7 +865,7 @@ void wide_kernel(KArgs a) {
   RowTile rt[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int64_t T = tile0 + r;
+    const int64_t T = !kGlu ? tile0 + r : (pair < a.half_tiles ? pair + r * (int64_t)a.half_tiles : tiles);
     const bool tile_ok = T < tiles;
     rt[r].vcode = tile_ok ? (uint32_t)T * (192u * gp) + 16u * lane : kOob;
     rt[r].vscale = tile_ok ? (uint32_t)T * (16u * gp) + 4u * lane : kOob;
@@ -911,6 +948,10 @@ void wide_kernel(KArgs a) {
     for (int c = 0; c < NT; ++c) {
       const int j = 16 * c + i;
       if (j < cnt) {
+        if constexpr (kGlu) {
+          if (pair < a.half_tiles) store_glu(a, slice + j, pair * 16 + 4 * kb, acc[0][c], acc[1][c]);
+          continue;
+        }
         float* yr = ybase + (int64_t)(slice + j) * a.ldy;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -1199,16 +1240,16 @@ hipError_t launch_one(const KArgs& a, size_t shm, unsigned grid_y, unsigned grid
   return hipGetLastError();
 }
 
-template <int NT, int R>
+template <int NT, int R, bool kGlu = false>
 hipError_t launch_wide(const KArgs& a, unsigned splits, hipStream_t s) {
   constexpr int kRowsPerBlock = R * kWideWaves;
   const size_t shm = stream_bytes(16 * NT);
   static LdsAllowance seen;
-  const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(wide_kernel<NT, R>), shm, seen);
+  const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(wide_kernel<NT, R, kGlu>), shm, seen);
   if (e != hipSuccess) return e;
   const int64_t tiles = (a.n + 15) / 16;
   const dim3 grid((unsigned)((tiles + kRowsPerBlock - 1) / kRowsPerBlock), 1, splits);
-  hipLaunchKernelGGL((wide_kernel<NT, R>), grid, dim3(64 * kWideWaves), shm, s, a);
+  hipLaunchKernelGGL((wide_kernel<NT, R, kGlu>), grid, dim3(64 * kWideWaves), shm, s, a);
   return hipGetLastError();
 }
 
@@ -1551,6 +1592,58 @@ hipError_t launch_gemm_small_m(const PlaneView& w, const uint16_t* x, int64_t m,
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();
+}
+
+namespace {
+
+// The gated product of NT column tiles.  Activations that fit are staged whole,
+// K split over the waves of a block until about 2048 waves share the launch;
+// on whole steps two or more column tiles take the wide kernel with one gate
+// and one up tile per wave; the rest streams through 4-wave blocks.
+template <int NT>
+hipError_t launch_glu_nt(KArgs a, hipStream_t s) {
+  const size_t fk = full_k_bytes(a.m, a.G);
+  const int steps = (((a.G + 3) & ~3) + 15) / 16;
+  if (fk <= (size_t)kFullKBudget) {
+    int sk = 1;
+    while (sk < 8 && sk * 2 <= steps && (int64_t)a.half_tiles * sk < 2048) sk *= 2;
+    a.sk = sk;
+    const int w = sk > 4 ? 8 : 4;
+    size_t shm = fk;
+    if (sk > 1) {
+      const size_t red = reduce_bytes(4 * NT, 2, w);
+      if (shm < red) shm = red;
+    }
+    if (w == 8) return launch_one<NT, 2, 8, kDenseGlu, kShared, false, 3>(a, shm, 1, 1, s);
+    return launch_one<NT, 2, 4, kDenseGlu, kShared, false, 3>(a, shm, 1, 1, s);
+  }
+  a.sk = 1;
+  if constexpr (NT >= kWideMinNT) {
+    if (a.G % 16 == 0) return launch_wide<NT, 2, true>(a, 1, s);
+  }
+  return launch_one<NT, 2, 4, kDenseGlu, kStream, false, 3>(a, stream_bytes(16 * NT), 1, 1, s);
+}
+
+}  // namespace
+
+hipError_t launch_glu_small_m(const PlaneView& gate_up, const uint16_t* x, int64_t m, int64_t ldx, int32_t act,
+                              uint16_t* h, int64_t ldh, float* pre, int64_t ld_pre, hipStream_t s) {
+  if (gate_up.n == 0) return hipSuccess;
+  KArgs a = base_args(gate_up);
+  a.x = x;
+  a.ldx = ldx;
+  a.x_rows = m;
+  a.m = (int)m;
+  a.half_tiles = (int)(gate_up.n / 32);
+  a.h = h;
+  a.ldh = ldh;
+  a.act = act;
+  a.pre = pre;
+  a.ld_pre = ld_pre;
+  if (m <= 16) return launch_glu_nt<1>(a, s);
+  if (m <= 32) return launch_glu_nt<2>(a, s);
+  if (m <= 48) return launch_glu_nt<3>(a, s);
+  return launch_glu_nt<4>(a, s);
 }
 
 hipError_t launch_head2_scores(const PlaneView& w, const uint16_t* x, int64_t m, int64_t ldx, float* y, int64_t ldy,
