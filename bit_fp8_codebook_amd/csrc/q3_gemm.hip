@@ -21,39 +21,65 @@ namespace {
 // ---- widening -----------------------------------------------------------------
 
 // One wave per (16-row tile, 512-k step): lane l holds row l%16 and groups
-// 4*(l/16)..+3, as the planes are laid out, and writes its 128 weights.
-// out [n][gp*32]; groups past G are written as zeros.
+// 4*(l/16)..+3, as the planes are laid out.  Two of its groups at a time go
+// through LDS, so that 8 lanes store 128 consecutive bytes of a row (stored
+// straight from the lanes that dequantise, 16 bytes every 256, 22016 x 4096
+// took 103 us).  out [n][gp*32]; groups past G are written as zeros.
+constexpr uint32_t kWidenSlot = 128 + 16;   // a lane's two groups, padded against bank conflicts
 __global__ __launch_bounds__(256) void widen_kernel(PlaneView w, uint16_t* __restrict__ out, int64_t units, int steps) {
+  __shared__ __align__(16) uint8_t stage[4][64 * kWidenSlot];
   const int lane = threadIdx.x & 63;
   const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (unit >= units) return;
+  if (unit >= units) return;   // whole waves; the block has no barriers
+  uint8_t* st = stage[threadIdx.x >> 6];
   const int i = lane & 15, kb = lane >> 4;
   const int64_t tile = unit / steps;
   const uint32_t s = (uint32_t)(unit - tile * steps);
   const uint32_t gp = (uint32_t)((w.groups + 3) & ~3);
   const uint32_t q = step_quads(s, gp);
   const int64_t row = tile * 16 + i;
-  if ((uint32_t)kb >= q || row >= w.n) return;
-  const uint8_t* c = w.code + tile * (int64_t)(192u * gp) + 3072u * s;
-  u32x4 d[3];
+  u32x4 d[3] = {};
+  uint32_t sc = 0;
+  u32x2 cb = {0u, 0u};
+  if ((uint32_t)kb < q && row < w.n) {
+    const uint8_t* c = w.code + tile * (int64_t)(192u * gp) + 3072u * s;
 #pragma unroll
-  for (int j = 0; j < 3; ++j) d[j] = *reinterpret_cast<const u32x4*>(c + 16u * (16u * (q * j + kb) + i));
-  const uint32_t sc = *reinterpret_cast<const uint32_t*>(w.scale + tile * (int64_t)(16u * gp) + 256u * s +
-                                                         4u * (16u * kb + i));
-  const u32x2 cb = *reinterpret_cast<const u32x2*>(w.cb + row * 8);
-  uint16_t* o = out + row * (int64_t)(gp * 32u) + s * 512u + kb * 128u;
+    for (int j = 0; j < 3; ++j) d[j] = *reinterpret_cast<const u32x4*>(c + 16u * (16u * (q * j + kb) + i));
+    sc = *reinterpret_cast<const uint32_t*>(w.scale + tile * (int64_t)(16u * gp) + 256u * s + 4u * (16u * kb + i));
+    cb = *reinterpret_cast<const u32x2*>(w.cb + row * 8);
+  }
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    bf16x2 v[16];
-    dequant_group_bf16(d[0][t], d[1][t], d[2][t], (sc >> (8 * t)) & 255u, cb.x, cb.y, v);
-    const bool real = (int)(s * 16u + kb * 4u + t) < w.groups;
+  for (int half = 0; half < 2; ++half) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      u32x4 u;
+    for (int g = 0; g < 2; ++g) {
+      const int t = 2 * half + g;
+      bf16x2 v[16];
+      dequant_group_bf16(d[0][t], d[1][t], d[2][t], (sc >> (8 * t)) & 255u, cb.x, cb.y, v);
+      const bool real = (int)(s * 16u + kb * 4u + t) < w.groups;
 #pragma unroll
-      for (int f = 0; f < 4; ++f) u[f] = real ? __builtin_bit_cast(uint32_t, v[4 * e + f]) : 0u;
-      *reinterpret_cast<u32x4*>(o + 32 * t + 8 * e) = u;
+      for (int e = 0; e < 4; ++e) {
+        u32x4 u;
+#pragma unroll
+        for (int f = 0; f < 4; ++f) u[f] = real ? __builtin_bit_cast(uint32_t, v[4 * e + f]) : 0u;
+        *reinterpret_cast<u32x4*>(st + lane * kWidenSlot + 64 * g + 16 * e) = u;
+      }
     }
+    // The wave reads what its own lanes wrote.
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const int slot = 8 * c + (lane >> 3), piece = lane & 7;
+      const int64_t r = tile * 16 + (slot & 15);
+      const uint32_t b = (uint32_t)slot >> 4;
+      if (b < q && r < w.n)
+        *reinterpret_cast<u32x4*>(out + r * (int64_t)(gp * 32u) + s * 512u + b * 128u + half * 64u + piece * 8u) =
+            *reinterpret_cast<const u32x4*>(st + slot * kWidenSlot + 16 * piece);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   }
 }
 
@@ -114,6 +140,8 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* __restric
 
 // ---- C = A B^T ------------------------------------------------------------------
 
+constexpr int kMaxGemmSplits = 8;
+
 enum Epilogue : int { kStoreF32 = 0, kGlu = 1 };
 
 struct GemmArgs {
@@ -123,8 +151,9 @@ struct GemmArgs {
   int64_t ldb;
   int64_t m, n;        // outputs (kGlu: n = I, b holds 2I rows)
   int64_t k;           // summed columns of a (k % 8 == 0); b is zero from there to the next multiple of 64
-  float* c;
+  float* c;            // split z (blockIdx.y) of the summed axis writes c + z * split_stride
   int64_t ldc;
+  int64_t split_stride;
   int vec;             // c rows 16-byte aligned
   // kGlu
   uint16_t* h;
@@ -229,13 +258,14 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
   const uint32_t frag = (uint32_t)(lane & 15) * 128u + (((uint32_t)lane >> 4) ^ ((uint32_t)lane & 7u)) * 16u;
   const uint32_t fa = (uint32_t)(wm * TM * 16) * 128u + frag;
   const uint32_t fb = kABytes + (uint32_t)(wn * TN * 16) * 128u + frag;
-  const int steps = (int)((g.k + 63) / 64);
-  if (steps > 0) load(0, 0u);
+  const int64_t all = (g.k + 63) / 64;
+  const int s0 = (int)(all * blockIdx.y / gridDim.y), s1 = (int)(all * (blockIdx.y + 1) / gridDim.y);
+  if (s0 < s1) load(s0, 0u);
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
   uint32_t buf = 0;
-  for (int s = 0; s < steps; ++s) {
-    if (s + 1 < steps) load(s + 1, kBuf - buf);
+  for (int s = s0; s < s1; ++s) {
+    if (s + 1 < s1) load(s + 1, kBuf - buf);
 #pragma unroll
     for (uint32_t half = 0; half < 2; ++half) {
       bf16x8 wv[TN], xv[TM];
@@ -282,7 +312,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
         }
       }
     } else {
-      float* c = g.c + token * g.ldc;
+      float* c = g.c + (int64_t)blockIdx.y * g.split_stride + token * g.ldc;
 #pragma unroll
       for (int n = 0; n < TN; ++n) {
         const int64_t i = n0 + (wn * TN + n) * 16 + 4 * (lane >> 4);
@@ -299,7 +329,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
 }
 
 template <int BM, int BN, int WM, int WN, int kEpi>
-hipError_t launch_gemm_one(GemmArgs g, hipStream_t s) {
+hipError_t launch_gemm_one(GemmArgs g, int splits, hipStream_t s) {
   constexpr int kOut = kEpi == kGlu ? BN / 2 : BN;
   constexpr size_t shm = 2 * (BM + BN) * 128;
   static LdsAllowance seen;
@@ -310,16 +340,86 @@ hipError_t launch_gemm_one(GemmArgs g, hipStream_t s) {
   if (tm * tn > 0x7FFFFFFF) return hipErrorInvalidValue;
   g.tiles_m = (int)tm;
   g.tiles_n = (int)tn;
-  hipLaunchKernelGGL((gemm_kernel<BM, BN, WM, WN, kEpi>), dim3((unsigned)(tm * tn)), dim3(64 * WM * WN), shm, s, g);
+  hipLaunchKernelGGL((gemm_kernel<BM, BN, WM, WN, kEpi>), dim3((unsigned)(tm * tn), (unsigned)splits),
+                     dim3(64 * WM * WN), shm, s, g);
   return hipGetLastError();
 }
 
-template <int kEpi>
-hipError_t launch_gemm_pick(const GemmArgs& g, hipStream_t s) {
-  const int64_t cols = kEpi == kGlu ? 2 * g.n : g.n;
-  const int64_t big = ((g.m + 255) / 256) * ((cols + 255) / 256);
-  if (big >= 192) return launch_gemm_one<256, 256, 2, 4, kEpi>(g, s);
-  return launch_gemm_one<128, 128, 2, 2, kEpi>(g, s);
+// Partial planes added in split order, four columns per thread.
+__global__ __launch_bounds__(256) void gemm_reduce_kernel(const float* __restrict__ part, int64_t stride, int splits,
+                                                          int64_t m, int64_t n, float* __restrict__ y, int64_t ldy,
+                                                          int vec) {
+  const int64_t nq = (n + 3) / 4, e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (e >= m * nq) return;
+  const int64_t r = e / nq, c = 4 * (e - r * nq);
+  const float* p = part + r * (4 * nq) + c;   // plane rows are padded to four columns
+  f32x4 v[kMaxGemmSplits];
+#pragma unroll
+  for (int z = 0; z < kMaxGemmSplits; ++z)
+    v[z] = z < splits ? *reinterpret_cast<const f32x4*>(p + z * stride) : f32x4{0.f, 0.f, 0.f, 0.f};
+  f32x4 acc = v[0];
+#pragma unroll
+  for (int z = 1; z < kMaxGemmSplits; ++z) acc += v[z];
+  float* o = y + r * ldy + c;
+  if (vec && c + 3 < n) {
+    *reinterpret_cast<f32x4*>(o) = acc;
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (c + q < n) o[q] = acc[q];
+  }
+}
+
+// Block shape and splits of the summed axis for m tokens, n outputs (weight
+// rows) and k summed.
+struct GemmPlan {
+  bool big;     // 256 x 256 blocks of 8 waves, else 128 x 128 of 4
+  int splits;
+};
+GemmPlan plan_gemm(int64_t m, int64_t n, int64_t k, bool may_split) {
+  GemmPlan p{((m + 255) / 256) * ((n + 255) / 256) >= 192, 1};
+  if (p.big || !may_split) return p;
+  // Two 128 x 128 blocks fit a CU.  Fewer tiles than that leave CUs idle: the
+  // summed axis is split, at eight or more steps of 64 each, so that the
+  // partial planes stay small next to the products.
+  const int64_t tiles = ((m + 127) / 128) * ((n + 127) / 128), steps = (k + 63) / 64;
+  int64_t s = 512 / (tiles > 0 ? tiles : 1);
+  s = s < steps / 8 ? s : steps / 8;
+  s = s < kMaxGemmSplits ? s : kMaxGemmSplits;
+  p.splits = s > 1 ? (int)s : 1;
+  return p;
+}
+int64_t plane_floats(int64_t m, int64_t n) { return m * ((n + 3) / 4 * 4); }
+int64_t split_bytes(int64_t m, int64_t n, int64_t k) {
+  const GemmPlan p = plan_gemm(m, n, k, true);
+  return p.splits > 1 ? p.splits * plane_floats(m, n) * 4 : 0;
+}
+
+hipError_t launch_glu_gemm(const GemmArgs& g, hipStream_t s) {
+  if (plan_gemm(g.m, 2 * g.n, g.k, false).big) return launch_gemm_one<256, 256, 2, 4, kGlu>(g, 1, s);
+  return launch_gemm_one<128, 128, 2, 2, kGlu>(g, 1, s);
+}
+
+// part: split_bytes(m, n, k) bytes, 16-byte aligned.
+hipError_t launch_f32_gemm(GemmArgs g, float* part, hipStream_t s) {
+  const GemmPlan p = plan_gemm(g.m, g.n, g.k, true);
+  if (p.splits == 1) {
+    if (p.big) return launch_gemm_one<256, 256, 2, 4, kStoreF32>(g, 1, s);
+    return launch_gemm_one<128, 128, 2, 2, kStoreF32>(g, 1, s);
+  }
+  float* y = g.c;
+  const int64_t ldy = g.ldc;
+  const int vec = g.vec;
+  g.c = part;
+  g.ldc = (g.n + 3) / 4 * 4;
+  g.split_stride = plane_floats(g.m, g.n);
+  g.vec = 1;
+  const hipError_t e = launch_gemm_one<128, 128, 2, 2, kStoreF32>(g, p.splits, s);
+  if (e != hipSuccess) return e;
+  const int64_t blocks = (g.m * ((g.n + 3) / 4) + 255) / 256;
+  hipLaunchKernelGGL(gemm_reduce_kernel, dim3((unsigned)blocks), dim3(256), 0, s, part, g.split_stride, p.splits, g.m,
+                     g.n, y, ldy, vec);
+  return hipGetLastError();
 }
 
 int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
@@ -370,7 +470,7 @@ __global__ __launch_bounds__(256) void glu_back_kernel(const float* __restrict__
 
 int64_t gemm_workspace_bytes(int64_t n, int64_t k, int64_t m) {
   if (m <= kSmallM) return gemm_small_m_workspace_bytes(n, k, m);
-  return align256(n * padded_k(k) * 2);
+  return align256(n * padded_k(k) * 2) + align256(split_bytes(m, n, k));
 }
 
 hipError_t launch_gemm(const PlaneView& w, const uint16_t* x, int64_t m, int64_t ldx, float* y, int64_t ldy, void* ws,
@@ -393,11 +493,11 @@ hipError_t launch_gemm(const PlaneView& w, const uint16_t* x, int64_t m, int64_t
   g.c = y;
   g.ldc = ldy;
   g.vec = (uintptr_t)y % 16 == 0 && ldy % 4 == 0;
-  return launch_gemm_pick<kStoreF32>(g, s);
+  return launch_f32_gemm(g, reinterpret_cast<float*>(wide + align256(w.n * padded_k(k) * 2) / 2), s);
 }
 
 int64_t gemm_backward_workspace_bytes(int64_t n, int64_t k, int64_t m) {
-  return align256(k * padded_n(n) * 2) + (n % 8 ? align256(m * padded_n(n) * 2) : 0);
+  return align256(k * padded_n(n) * 2) + (n % 8 ? align256(m * padded_n(n) * 2) : 0) + align256(split_bytes(m, k, n));
 }
 
 hipError_t launch_gemm_backward(const PlaneView& w, const uint16_t* dy, int64_t m, int64_t ld_dy, float* dx,
@@ -414,8 +514,10 @@ hipError_t launch_gemm_backward(const PlaneView& w, const uint16_t* dy, int64_t 
   g.a = dy;
   g.lda = ld_dy;
   g.k = w.n;
+  uint16_t* rest = wide + align256(k * np * 2) / 2;
   if (w.n % 8) {
-    uint16_t* padded = wide + align256(k * np * 2) / 2;
+    uint16_t* padded = rest;
+    rest += align256(m * np * 2) / 2;
     for (int64_t r = 0; r < m; r += 65535) {   // grid rows of one launch
       const int64_t rows = m - r < 65535 ? m - r : 65535;
       hipLaunchKernelGGL(pad_rows_kernel, dim3((unsigned)((np + 255) / 256), (unsigned)rows), dim3(256), 0, s,
@@ -425,7 +527,7 @@ hipError_t launch_gemm_backward(const PlaneView& w, const uint16_t* dy, int64_t 
     if (e != hipSuccess) return e;
     g.a = padded;
     g.lda = np;
-    g.k = np;
+    g.k = (w.n + 7) / 8 * 8;
   }
   g.b = wide;
   g.ldb = np;
@@ -434,7 +536,7 @@ hipError_t launch_gemm_backward(const PlaneView& w, const uint16_t* dy, int64_t 
   g.c = dx;
   g.ldc = ld_dx;
   g.vec = (uintptr_t)dx % 16 == 0 && ld_dx % 4 == 0;
-  return launch_gemm_pick<kStoreF32>(g, s);
+  return launch_f32_gemm(g, reinterpret_cast<float*>(rest), s);
 }
 
 int64_t glu_workspace_bytes(int64_t n_gu, int64_t k, int64_t m) {
@@ -461,7 +563,7 @@ hipError_t launch_glu(const PlaneView& gate_up, const uint16_t* x, int64_t m, in
   g.pre = pre;
   g.ld_pre = ld_pre;
   g.act = act;
-  return launch_gemm_pick<kGlu>(g, s);
+  return launch_glu_gemm(g, s);
 }
 
 hipError_t launch_glu_backward(const float* pre, int64_t ld_pre, const float* dh, int64_t ld_dh, int32_t act,

@@ -8,24 +8,24 @@
 // any order (n <= 2^19), so chunks, atomics and scans give one result and the
 // running sums the draw compares are those the total is made of.
 //
-// A row is cut into tiles of 1024 entries and chunks of whole tiles; five
-// launches:
+// A row is cut into up to 16 chunks; five launches:
 //   stats    per chunk: largest and smallest logit
 //   hist     per chunk: entry counts and weights over 1024 bins of max l - l
 //            (equal steps over the row's span, at most 32 T; the last bin
-//            takes the rest).  The bin is a monotone function of the logit.
-//   border   per row: the bins in which top-k, top-p and min-p can fall, from
-//            the row's bin sums
-//   collect  per chunk: the weight of each tile's entries in bins before those,
-//            and the list of entries inside them (a few hundred)
-//   choose   per row: the listed entries are ranked against each other, which
-//            gives the exact cut; the tile sums are completed and searched for
-//            u times their total, and the token is found inside its tile
+//            takes the rest), as running sums over the bins.  The bin is a
+//            monotone function of the logit.
+//   border   per row: the bins in which top-k, top-p and min-p can fall
+//   collect  per chunk: the list of the entries inside those bins (a few hundred)
+//   choose   per row: the list is sorted, which gives the exact cut; the kept
+//            weight of each chunk follows from its running sums and the list,
+//            and u times the total is found in a chunk, a wave's part of it and
+//            an entry
 // A row whose border bins hold more than kCand entries (large ties) is cut by
 // bisection over the logits' 32-bit order instead, in the last launch.
 //
-// What bounds it: the row is read from memory once and twice more from cache,
-// and two of the three passes evaluate an exponential per entry in 64 bits.
+// What bounds it: the row is read from memory once and twice more from cache;
+// the hist pass evaluates a 64-bit exponential and one or two LDS atomics for
+// every entry.
 #include "q3_device.h"
 #include "q3_internal.h"
 
@@ -34,12 +34,10 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
-constexpr int kTile = 1024;        // entries per tile (one per thread)
-constexpr int kMaxTiles = 512;     // n <= 2^19
+constexpr int kMaxChunks = 16;     // per row
 constexpr int kBins = 1024;        // one per thread
 constexpr int kCand = 2048;        // listed entries per row
 constexpr int kNone = kBins;       // "no border": after every bin
-constexpr double kOne = 17592186044416.0;   // 2^44, the weight of the largest entry
 
 struct RowInfo {
   uint64_t mass_lo;    // weight of the bins before lo
@@ -49,16 +47,14 @@ struct RowInfo {
   int bk;              // the bin of rank top_k (kNone: no such bin)
   int cnt_lo, cnt_bk;  // entries in the bins before lo and before bk
   int want_bk;         // bk's entries are listed too, for the weight of the top_k entries
-  int slow;            // the lists do not fit: bisection
-  int listed;          // entries listed so far
+  int listed;          // entries listed (more than kCand: bisection)
 };
 
 struct Ws {
   float2* stats;         // [m][chunks] (max, min)
   RowInfo* info;         // [m]
-  uint32_t* hist_cnt;    // [m][chunks][kBins]
-  uint64_t* hist_mass;   // [m][chunks][kBins]
-  uint64_t* tile_mass;   // [m][tiles]
+  uint32_t* hist_cnt;    // [m][chunks][kBins] running sums (rows with top-k only)
+  uint64_t* hist_mass;   // [m][chunks][kBins] running sums
   uint64_t* cand;        // [m][kCand] (order << 32 | index)
 };
 
@@ -66,6 +62,7 @@ struct Ws {
 // with their off values.
 struct Settings {
   double inv_t;
+  double inv_t2;   // log2(e) / t
   float t;
   int k;
   double p, min_p;
@@ -78,6 +75,7 @@ __device__ __forceinline__ Settings settings(const SampleArgs& a, int row) {
   if (!(t > 0.f)) t = 1.f;
   s.t = t;
   s.inv_t = 1.0 / (double)t;
+  s.inv_t2 = 1.4426950408889634 * s.inv_t;
   const int k = a.top_k ? a.top_k[row] : 0;
   s.k = greedy ? 1 : (k > 0 && k < a.n ? k : a.n);
   const float p = a.top_p ? a.top_p[row] : 1.f;
@@ -102,12 +100,30 @@ __device__ __forceinline__ float logit_of(uint32_t k) {
 // that is +inf.
 __device__ __forceinline__ bool live(float l, float mx) { return l > -INFINITY && (mx < INFINITY || l == mx); }
 
-// 2^44 exp((l - mx)/t), rounded to an integer.
-__device__ __forceinline__ uint64_t weight(float l, float mx, double inv_t) {
-  const double x = l == mx ? 0.0 : ((double)l - (double)mx) * inv_t;
+// 2^44 exp((l - mx)/t), rounded to an integer: 2^x = 2^n 2^f with |f| <= 1/2 and
+// the Taylor series of 2^f up to f^11, whose remainder is below 2^-47 (the
+// integers' half step at w = 1 is 2^-45).
+__device__ __forceinline__ uint64_t weight(float l, float mx, double inv_t2) {
+  const double x = l == mx ? 0.0 : ((double)l - (double)mx) * inv_t2;
+  const double n = __builtin_rint(x), f = x - n;
+  constexpr double c[12] = {1.0,
+                            6.931471805599453e-01,
+                            2.402265069591007e-01,
+                            5.550410866482158e-02,
+                            9.618129107628477e-03,
+                            1.3333558146428441e-03,
+                            1.5403530393381606e-04,
+                            1.5252733804059837e-05,
+                            1.3215486790144305e-06,
+                            1.0178086009239699e-07,
+                            7.0549116208011225e-09,
+                            4.4455382718708101e-10};   // ln(2)^k / k!
+  double p = c[11];
+#pragma unroll
+  for (int k = 10; k >= 0; --k) p = __builtin_fma(p, f, c[k]);
   // Adding 2^52 leaves the rounded integer in the low bits.
-  const double w = exp(x) * kOne + 4503599627370496.0;
-  return __builtin_bit_cast(uint64_t, w) & 0x000FFFFFFFFFFFFFull;
+  const double w = __builtin_ldexp(p, (int)n + 44) + 4503599627370496.0;
+  return x > -46.0 ? __builtin_bit_cast(uint64_t, w) & 0x000FFFFFFFFFFFFFull : 0;
 }
 
 // Bins of equal steps of mx - l over the row's span, at most 32 temperatures.
@@ -128,10 +144,6 @@ __device__ __forceinline__ int bin_of(float l, const Binning& b) {
 
 // ---- block-wide helpers (kThreads threads) ----------------------------------
 
-template <typename T>
-__device__ __forceinline__ T wave_up(T v, int off) {
-  return __shfl_up(v, off, 64);
-}
 __device__ __forceinline__ uint64_t wave_up64(uint64_t v, int off) {
   return (uint64_t)__shfl_up((unsigned long long)v, off, 64);
 }
@@ -196,19 +208,37 @@ __device__ __forceinline__ float2 row_stats(const float2* st, int chunks) {
 
 // ---- launches -----------------------------------------------------------------
 
-__global__ __launch_bounds__(kThreads) void sample_stats_kernel(SampleArgs a, Ws ws, int tiles_per_chunk) {
+// Entries [begin, end) of a chunk.
+struct Range {
+  int begin, end;
+};
+__device__ __forceinline__ Range chunk_range(int c, int per, int n) {
+  return {c * per, (c + 1) * per < n ? (c + 1) * per : n};
+}
+
+// Calls f(logit, index) for the block's entries of [r.begin, r.end), kBatch
+// loads ahead of their use.
+template <int kBatch, typename F>
+__device__ __forceinline__ void for_entries(const float* __restrict__ l, Range r, F&& f) {
+  int i = r.begin + threadIdx.x;
+  for (; i + (kBatch - 1) * kThreads < r.end; i += kBatch * kThreads) {
+    float v[kBatch];
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) v[q] = l[i + q * kThreads];
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) f(v[q], i + q * kThreads);
+  }
+  for (; i < r.end; i += kThreads) f(l[i], i);
+}
+
+__global__ __launch_bounds__(kThreads) void sample_stats_kernel(SampleArgs a, Ws ws, int per) {
   __shared__ float2 part[kWaves];
   const int row = blockIdx.y, c = blockIdx.x;
-  const float* l = a.logits + (int64_t)row * a.ld;
-  const int i0 = c * tiles_per_chunk * kTile;
-  const int i1 = min(a.n, i0 + tiles_per_chunk * kTile);
   float mx = -INFINITY, mn = INFINITY;
-#pragma unroll 4
-  for (int i = i0 + threadIdx.x; i < i1; i += kThreads) {
-    const float v = l[i];
+  for_entries<8>(a.logits + (int64_t)row * a.ld, chunk_range(c, per, a.n), [&](float v, int) {
     mx = fmaxf(mx, v);   // NaN leaves the other operand
     mn = v > -INFINITY ? fminf(mn, v) : mn;
-  }
+  });
 #pragma unroll
   for (int off = 32; off > 0; off /= 2) {
     mx = fmaxf(mx, __shfl_xor(mx, off, 64));
@@ -225,56 +255,56 @@ __global__ __launch_bounds__(kThreads) void sample_stats_kernel(SampleArgs a, Ws
   }
 }
 
-__global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a, Ws ws, int tiles_per_chunk) {
+__global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a, Ws ws, int per) {
   __shared__ uint32_t cnt[kBins];
   __shared__ unsigned long long mass[kBins];
+  __shared__ uint64_t part[kWaves];
   const int row = blockIdx.y, c = blockIdx.x, chunks = gridDim.x;
   const float2 st = row_stats(ws.stats + (int64_t)row * chunks, chunks);
   const Settings s = settings(a, row);
   const Binning b = binning(st.x, st.y, s.t);
+  const bool counts = s.k < a.n;   // only top-k asks how many entries a bin holds
   cnt[threadIdx.x] = 0;
   mass[threadIdx.x] = 0;
   __syncthreads();
-  const float* l = a.logits + (int64_t)row * a.ld;
-  const int i0 = c * tiles_per_chunk * kTile;
-  const int i1 = min(a.n, i0 + tiles_per_chunk * kTile);
-#pragma unroll 4
-  for (int i = i0 + threadIdx.x; i < i1; i += kThreads) {
-    const float v = l[i];
-    if (!live(v, st.x)) continue;
+  for_entries<4>(a.logits + (int64_t)row * a.ld, chunk_range(c, per, a.n), [&](float v, int) {
+    if (!live(v, st.x)) return;
     const int k = bin_of(v, b);
-    atomicAdd(&cnt[k], 1u);
-    atomicAdd(&mass[k], (unsigned long long)weight(v, st.x, s.inv_t));
-  }
+    const uint64_t q = weight(v, st.x, s.inv_t2);
+    if (counts) atomicAdd(&cnt[k], 1u);
+    if (q) atomicAdd(&mass[k], (unsigned long long)q);
+  });
   __syncthreads();
   const int64_t at = ((int64_t)row * chunks + c) * kBins + threadIdx.x;
-  ws.hist_cnt[at] = cnt[threadIdx.x];
-  ws.hist_mass[at] = mass[threadIdx.x];
+  ws.hist_mass[at] = block_scan(mass[threadIdx.x], part);
+  if (counts) ws.hist_cnt[at] = (uint32_t)block_scan(cnt[threadIdx.x], part);
 }
 
 __global__ __launch_bounds__(kThreads) void sample_border_kernel(SampleArgs a, Ws ws, int chunks) {
-  __shared__ uint64_t part[kWaves];
   __shared__ int ipart[kWaves];
-  __shared__ uint64_t mass_in[kBins];   // inclusive sums
+  __shared__ uint64_t mass_in[kBins];   // sums up to and with each bin
   __shared__ uint32_t cnt_in[kBins];
   const int row = blockIdx.x, t = threadIdx.x;
   const float2 st = row_stats(ws.stats + (int64_t)row * chunks, chunks);
   const Settings s = settings(a, row);
   const Binning b = binning(st.x, st.y, s.t);
-  uint64_t mass = 0, cnt = 0;
-  for (int c = 0; c < chunks; ++c) {
-    const int64_t at = ((int64_t)row * chunks + c) * kBins + t;
-    cnt += ws.hist_cnt[at];
-    mass += ws.hist_mass[at];
+  const bool counts = s.k < a.n;
+  uint64_t mi = 0;
+  uint32_t ci = 0;
+  const int64_t at = (int64_t)row * chunks * kBins + t;
+#pragma unroll
+  for (int c = 0; c < kMaxChunks; ++c) {   // all loads before the first use
+    mi += c < chunks ? ws.hist_mass[at + (int64_t)c * kBins] : 0;
+    ci += counts && c < chunks ? ws.hist_cnt[at + (int64_t)c * kBins] : 0;
   }
-  const uint64_t mi = block_scan(mass, part), ci = block_scan(cnt, part);
   mass_in[t] = mi;
-  cnt_in[t] = (uint32_t)ci;
+  cnt_in[t] = ci;
   __syncthreads();
-  const uint64_t total = mass_in[kBins - 1], entries = cnt_in[kBins - 1];
+  const uint64_t total = mass_in[kBins - 1];
+  const uint32_t entries = cnt_in[kBins - 1];
   auto first = [&](bool hit) { return block_min(hit ? t : kNone, ipart); };
   // The bin of the last of the top_k entries.
-  const int bk = (uint64_t)s.k < entries ? first(ci >= (uint64_t)s.k) : kNone;
+  const int bk = (uint32_t)s.k < entries ? first(ci >= (uint32_t)s.k) : kNone;
   // The weight of the top_k entries lies between the sums before and after
   // that bin, and top-p's border between the bins where p times those fall.
   int lo = bk, hi = bk;
@@ -297,56 +327,40 @@ __global__ __launch_bounds__(kThreads) void sample_border_kernel(SampleArgs a, W
     lo = min(lo, e_lo);
     hi = min(hi, e_hi);
   }
-  const int want_bk = s.use_p && bk != kNone && !(lo <= bk && bk <= hi);
   if (t == 0) {
     RowInfo r;
     auto mass_before = [&](int k) -> uint64_t { return k > 0 ? mass_in[k - 1] : 0; };
-    auto cnt_before = [&](int k) -> uint32_t { return k > 0 ? cnt_in[k - 1] : 0; };
+    // Without counts only whether there are entries before matters (bin 0 holds the maximum).
+    auto cnt_before = [&](int k) -> int { return k > 0 ? (counts ? (int)cnt_in[k - 1] : 1) : 0; };
     r.total = total;
     r.lo = lo;
     r.hi = hi;
     r.bk = bk;
-    r.want_bk = want_bk;
+    r.want_bk = s.use_p && bk != kNone && !(lo <= bk && bk <= hi);
     r.mass_lo = mass_before(lo);
-    r.cnt_lo = (int)cnt_before(lo);
+    r.cnt_lo = cnt_before(lo);
     r.mass_bk = mass_before(bk);
-    r.cnt_bk = (int)cnt_before(bk);
-    uint32_t listed = lo == kNone ? 0 : cnt_in[min(hi, kBins - 1)] - cnt_before(lo);
-    if (want_bk) listed += cnt_in[bk] - cnt_before(bk);
-    r.slow = listed > (uint32_t)kCand;
+    r.cnt_bk = cnt_before(bk);
     r.listed = 0;
     ws.info[row] = r;
   }
 }
 
-__global__ __launch_bounds__(kThreads) void sample_collect_kernel(SampleArgs a, Ws ws, int tiles_per_chunk, int tiles) {
-  __shared__ uint64_t part[kWaves];
-  __shared__ RowInfo r;
-  const int row = blockIdx.y, c = blockIdx.x, chunks = gridDim.x, t = threadIdx.x;
+__global__ __launch_bounds__(kThreads) void sample_collect_kernel(SampleArgs a, Ws ws, int per) {
+  const int row = blockIdx.y, c = blockIdx.x, chunks = gridDim.x;
+  const RowInfo& r = ws.info[row];
+  const int lo = r.lo, hi = r.hi, bk = r.want_bk ? r.bk : -1;
+  if (lo == kNone) return;   // nothing is cut
   const float2 st = row_stats(ws.stats + (int64_t)row * chunks, chunks);
   const Settings s = settings(a, row);
   const Binning b = binning(st.x, st.y, s.t);
-  if (t == 0) r = ws.info[row];
-  __syncthreads();
-  if (r.slow) return;   // the whole block: r is shared
-  const float* l = a.logits + (int64_t)row * a.ld;
-  const int t0 = c * tiles_per_chunk, t1 = min(tiles, t0 + tiles_per_chunk);
-  for (int tile = t0; tile < t1; ++tile) {
-    const int i = tile * kTile + t;
-    const float v = i < a.n ? l[i] : -INFINITY;
-    uint64_t q = 0;
-    if (live(v, st.x)) {
-      const int k = bin_of(v, b);
-      if (k < r.lo) {
-        q = weight(v, st.x, s.inv_t);
-      } else if (k <= r.hi || (r.want_bk && k == r.bk)) {
-        const int at = atomicAdd(&ws.info[row].listed, 1);
-        if (at < kCand) ws.cand[(int64_t)row * kCand + at] = (uint64_t)order_of(v) << 32 | (uint32_t)i;
-      }
+  for_entries<8>(a.logits + (int64_t)row * a.ld, chunk_range(c, per, a.n), [&](float v, int i) {
+    const int k = bin_of(v, b);
+    if (((k >= lo && k <= hi) || k == bk) && live(v, st.x)) {
+      const int at = atomicAdd(&ws.info[row].listed, 1);
+      if (at < kCand) ws.cand[(int64_t)row * kCand + at] = (uint64_t)order_of(v) << 32 | (uint32_t)i;
     }
-    const uint64_t sum = block_sum(q, part);
-    if (t == 0) ws.tile_mass[(int64_t)row * tiles + tile] = sum;
-  }
+  });
 }
 
 // Kept entries: order (logit, then lower index) at or before the cut, or in a
@@ -364,14 +378,14 @@ __device__ __forceinline__ bool kept(float v, int i, float mx, const Binning& b,
 }
 
 // The number of entries ordered above `o` and their weight.
-__device__ void above(const float* l, int n, float mx, double inv_t, uint32_t o, uint64_t* part, uint64_t& cnt,
+__device__ void above(const float* l, int n, float mx, double inv_t2, uint32_t o, uint64_t* part, uint64_t& cnt,
                       uint64_t& mass) {
   uint64_t c = 0, w = 0;
   for (int i = threadIdx.x; i < n; i += kThreads) {
     const float v = l[i];
     if (live(v, mx) && order_of(v) > o) {
       ++c;
-      w += weight(v, mx, inv_t);
+      w += weight(v, mx, inv_t2);
     }
   }
   cnt = block_sum(c, part);
@@ -389,7 +403,7 @@ __device__ Cut bisect(const SampleArgs& a, const float* l, float mx, const Setti
     while (good - bad > 1) {
       const uint32_t mid = bad + (good - bad) / 2;
       uint64_t cnt, mass;
-      above(l, n, mx, s.inv_t, mid, part, cnt, mass);
+      above(l, n, mx, s.inv_t2, mid, part, cnt, mass);
       bool ok = cnt < (uint64_t)s.k;
       if (with_p) {
         ok = ok && (double)mass < limit;
@@ -423,18 +437,18 @@ __device__ Cut bisect(const SampleArgs& a, const float* l, float mx, const Setti
     uint64_t top = total;
     if (s.k < n) {
       const uint32_t ok = search(false, 0);
-      above(l, n, mx, s.inv_t, ok, part, cnt, mass);
+      above(l, n, mx, s.inv_t2, ok, part, cnt, mass);
       uint64_t c1, m1;
-      above(l, n, mx, s.inv_t, ok - 1, part, c1, m1);   // with the entries of order ok
+      above(l, n, mx, s.inv_t2, ok - 1, part, c1, m1);   // with the entries of order ok
       const uint64_t same = c1 - cnt, take = min((uint64_t)s.k - cnt, same);
       top = same ? mass + take * ((m1 - mass) / same) : mass;
     }
     limit = s.p * (double)top;
   }
   const uint32_t o = search(true, s.use_p ? limit : 1.0e300);
-  above(l, n, mx, s.inv_t, o, part, cnt, mass);
+  above(l, n, mx, s.inv_t2, o, part, cnt, mass);
   uint64_t c1, m1;
-  above(l, n, mx, s.inv_t, o - 1, part, c1, m1);
+  above(l, n, mx, s.inv_t2, o - 1, part, c1, m1);
   const uint64_t same = c1 - cnt;
   uint64_t take = min(same, (uint64_t)s.k - cnt);
   if (same && s.use_p) {
@@ -449,13 +463,41 @@ __device__ Cut bisect(const SampleArgs& a, const float* l, float mx, const Setti
   return Cut{o, same ? nth_index(o, take) : 0x7FFFFFFF, 0};
 }
 
-__global__ __launch_bounds__(kThreads) void sample_choose_kernel(SampleArgs a, Ws ws, int chunks, int tiles) {
+// Sorts key[0..N) in descending order, N a power of two from 128 to kCand; a
+// thread compares one pair at a time.  Strides up to 64 stay inside the 128
+// entries of one wave, so only the longer ones need block barriers.
+__device__ __forceinline__ void sort_desc(uint64_t* key, int N) {
+  const int t = threadIdx.x;
+  for (int k = 2; k <= N; k *= 2) {
+    for (int j = k / 2; j > 0; j /= 2) {
+      if (j >= 64) __syncthreads();   // entries written by other waves (j = 64: by the step before)
+      if (t < N / 2) {
+        const int i = 2 * t - (t & (j - 1)), p = i + j;
+        const uint64_t x = key[i], y = key[p];
+        if ((x < y) == ((i & k) == 0)) {
+          key[i] = y;
+          key[p] = x;
+        }
+      }
+      if (j > 64) {
+        __syncthreads();
+      } else {
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      }
+    }
+  }
+  __syncthreads();
+}
+
+__global__ __launch_bounds__(kThreads) void sample_choose_kernel(SampleArgs a, Ws ws, int chunks, int per) {
   __shared__ uint64_t part[kWaves];
   __shared__ int ipart[kWaves];
-  __shared__ unsigned long long mass[kMaxTiles];
-  __shared__ uint64_t key[kCand], wgt[kCand];
-  __shared__ unsigned long long cut_key;
-  const int row = blockIdx.x, t = threadIdx.x;
+  __shared__ unsigned long long mass[kMaxChunks];
+  __shared__ uint64_t key[kCand];
+  static_assert(kCand == 2 * kThreads, "two listed entries per thread");
+  const int row = blockIdx.x, t = threadIdx.x, wave = t >> 6, lane = t & 63;
   const float2 st = row_stats(ws.stats + (int64_t)row * chunks, chunks);
   const float mx = st.x;
   if (!(mx > -INFINITY)) {   // nothing to choose from
@@ -469,139 +511,173 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(SampleArgs a, W
   const Binning b = binning(mx, st.y, s.t);
   const RowInfo r = ws.info[row];
   const float* l = a.logits + (int64_t)row * a.ld;
-  Cut cut{0u, 0x7FFFFFFF, 0};
-  if (!r.slow) {
-    cut.lo = r.lo;
-    for (int i = t; i < tiles; i += kThreads) mass[i] = ws.tile_mass[(int64_t)row * tiles + i];
-    const int nc = min(r.listed, kCand);
-    // Sort key: larger logit first, then lower index; ~index makes "greater is
-    // ranked earlier" one comparison.
-    for (int i = t; i < nc; i += kThreads) {
-      const uint64_t e = ws.cand[(int64_t)row * kCand + i];
-      key[i] = e ^ 0xFFFFFFFFull;
-      wgt[i] = weight(logit_of((uint32_t)(e >> 32)), mx, s.inv_t);
-    }
-    if (t == 0) cut_key = ~0ull;
-    __syncthreads();
-    // Rank and preceding weight of each listed entry, among the listed ones.
-    int my_rank[kCand / kThreads];
-    uint64_t my_mass[kCand / kThreads];
-    uint64_t bk_mass = 0;   // listed entries of bin bk that are among the top_k
-#pragma unroll
-    for (int e = 0; e < kCand / kThreads; ++e) {
-      const int i = e * kThreads + t;
-      my_rank[e] = 0;
-      my_mass[e] = 0;
-      if (i < nc) {
-        const uint64_t k = key[i];
-        int rank = 0;
-        uint64_t before = 0;
-        for (int j = 0; j < nc; ++j) {
-          const bool g = key[j] > k;
-          rank += g;
-          before += g ? wgt[j] : 0;
-        }
-        my_rank[e] = rank;
-        my_mass[e] = before;
-      }
-    }
-    auto bin_at = [&](int i) { return bin_of(logit_of((uint32_t)(key[i] >> 32)), b); };
-    // Entries listed in bins lo..hi come before those of bin bk.
-    uint64_t inside = 0;
-    if (r.want_bk) {
-      uint64_t c = 0;
-#pragma unroll
-      for (int e = 0; e < kCand / kThreads; ++e) {
-        const int i = e * kThreads + t;
-        if (i < nc && bin_at(i) <= r.hi) ++c;
-      }
-      inside = block_sum(c, part);
-    }
-    uint64_t top = r.total;
-    if (s.use_p && r.bk != kNone) {
-#pragma unroll
-      for (int e = 0; e < kCand / kThreads; ++e) {
-        const int i = e * kThreads + t;
-        if (i < nc && bin_at(i) == r.bk) {
-          const int64_t rank = r.want_bk ? (int64_t)r.cnt_bk + my_rank[e] - (int64_t)inside
-                                         : (int64_t)r.cnt_lo + my_rank[e];
-          if (rank < s.k) bk_mass += wgt[i];
-        }
-      }
-      top = r.mass_bk + block_sum(bk_mass, part);
-    }
-    const double limit = s.p * (double)top;
-#pragma unroll
-    for (int e = 0; e < kCand / kThreads; ++e) {
-      const int i = e * kThreads + t;
-      if (i < nc && bin_at(i) <= r.hi) {
-        const int64_t rank = (int64_t)r.cnt_lo + my_rank[e];
-        bool ok = rank < s.k;
-        if (s.use_p) ok = ok && (rank == 0 || (double)(r.mass_lo + my_mass[e]) < limit);
-        if (s.use_min) {
-          const float v = logit_of((uint32_t)(key[i] >> 32));
-          ok = ok && (v == mx || exp(((double)v - (double)mx) * s.inv_t) >= s.min_p);
-        }
-        if (ok) {
-          const uint32_t index = ~(uint32_t)key[i];
-          atomicAdd(&mass[index / kTile], (unsigned long long)wgt[i]);
-          atomicMin(&cut_key, (unsigned long long)key[i]);
-        }
-      }
-    }
-    __syncthreads();
+  Cut cut{0u, 0x7FFFFFFF, r.lo};   // nothing cut: lo is past every bin
+  if (r.listed <= kCand) {
+    if (t < chunks) mass[t] = r.lo ? ws.hist_mass[((int64_t)row * chunks + t) * kBins + r.lo - 1] : 0;
     if (r.lo != kNone) {
-      cut.order = (uint32_t)(cut_key >> 32);   // none kept: above every logit
-      cut.index = cut_key == ~0ull ? -1 : (int)~(uint32_t)cut_key;
+      // Larger logit first, then lower index: ~index makes "greater is ranked
+      // earlier" one comparison.  Empty places sort last.
+      const int nc = r.listed;
+      int N = 128;
+      while (N < nc) N *= 2;
+      for (int i = t; i < N; i += kThreads) key[i] = i < nc ? ws.cand[(int64_t)row * kCand + i] ^ 0xFFFFFFFFull : 0;
+      __syncthreads();
+      sort_desc(key, N);
+      // Thread t holds places 2t and 2t+1; their rank and the weight before
+      // them, among the listed entries.
+      uint64_t w[2] = {0, 0}, before[2];
+      int bin[2] = {kNone, kNone};
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (2 * t + e < nc) {
+          const float v = logit_of((uint32_t)(key[2 * t + e] >> 32));
+          w[e] = weight(v, mx, s.inv_t2);
+          bin[e] = bin_of(v, b);
+        }
+      before[0] = block_scan(w[0] + w[1], part) - w[0] - w[1];
+      before[1] = before[0] + w[0];
+      // Entries of bins lo..hi come before those of a separate bin bk.
+      uint64_t top = r.total;
+      if (s.use_p && r.bk != kNone) {
+        const int64_t inside =
+            r.want_bk ? (int64_t)block_sum((uint64_t)(bin[0] <= r.hi) + (uint64_t)(bin[1] <= r.hi), part) : 0;
+        const int64_t base = r.want_bk ? (int64_t)r.cnt_bk - inside : (int64_t)r.cnt_lo;
+        uint64_t in_k = 0;   // weight of bin bk's entries among the top_k
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (bin[e] == r.bk && base + 2 * t + e < s.k) in_k += w[e];
+        top = r.mass_bk + block_sum(in_k, part);
+      }
+      const double limit = s.p * (double)top;
+      int last = -1;   // the last kept place
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (2 * t + e < nc && bin[e] <= r.hi) {
+          const int64_t rank = (int64_t)r.cnt_lo + 2 * t + e;
+          const uint64_t k = key[2 * t + e];
+          bool ok = rank < s.k;
+          if (s.use_p) ok = ok && (rank == 0 || (double)(r.mass_lo + before[e]) < limit);
+          if (s.use_min) {
+            const float v = logit_of((uint32_t)(k >> 32));
+            ok = ok && (v == mx || exp(((double)v - (double)mx) * s.inv_t) >= s.min_p);
+          }
+          if (ok) {
+            atomicAdd(&mass[~(uint32_t)k / (uint32_t)per], (unsigned long long)w[e]);
+            last = 2 * t + e;
+          }
+        }
+      last = -block_min(-last, ipart);
+      cut.order = last < 0 ? 0xFFFFFFFFu : (uint32_t)(key[last] >> 32);   // none: above every logit
+      cut.index = last < 0 ? -1 : (int)~(uint32_t)key[last];
     }
   } else {
     cut = bisect(a, l, mx, s, r.total, part);
-    for (int tile = 0; tile < tiles; ++tile) {
-      const int i = tile * kTile + t;
-      const float v = i < a.n ? l[i] : -INFINITY;
-      const uint64_t sum = block_sum(kept(v, i, mx, b, cut) ? weight(v, mx, s.inv_t) : 0, part);
-      if (t == 0) mass[tile] = sum;
+    for (int c = 0; c < chunks; ++c) {
+      uint64_t q = 0;
+      for_entries<1>(l, chunk_range(c, per, a.n),
+                     [&](float v, int i) { q += kept(v, i, mx, b, cut) ? weight(v, mx, s.inv_t2) : 0; });
+      q = block_sum(q, part);
+      if (t == 0) mass[c] = q;
     }
-    __syncthreads();
   }
-  // The tile, then the entry, whose running sum exceeds u times the total.
-  const uint64_t mine = t < tiles ? mass[t] : 0;
-  const uint64_t run = block_scan(mine, part);
-  const uint64_t total = block_sum(mine, part);
+  __syncthreads();
+  uint64_t total = 0;
+  for (int c = 0; c < chunks; ++c) total += mass[c];
   float u = a.u[row];
   if (!(u > 0.f)) u = 0.f;
   const double want = (double)u * (double)total;
-  int tile = block_min(mine && (double)run > want ? t : 0x7FFFFFFF, ipart);
-  const bool over = tile == 0x7FFFFFFF;   // u >= 1: the last entry with weight
-  if (over) tile = -block_min(mine ? -t : 0, ipart);
-  __syncthreads();
-  if (t == tile) part[0] = run - mine;
-  __syncthreads();
-  const uint64_t before = part[0];
-  const int i = tile * kTile + t;
-  const float v = i < a.n ? l[i] : -INFINITY;
-  const uint64_t q = kept(v, i, mx, b, cut) ? weight(v, mx, s.inv_t) : 0;
-  const uint64_t sum = before + block_scan(q, part);
-  int pick = block_min(!over && q && (double)sum > want ? t : 0x7FFFFFFF, ipart);
-  if (pick == 0x7FFFFFFF) pick = -block_min(q ? -t : 0, ipart);
-  if (t == pick) {
-    a.tokens[row] = i;
-    if (a.logprobs)
+  // The chunk, then the wave's part of it, then the entry whose running sum
+  // exceeds u times the total; for u >= 1 the last one with weight.
+  uint64_t run = 0;
+  int c = 0, last = 0;
+  uint64_t last_run = 0;
+  for (c = 0; c < chunks; ++c) {
+    const uint64_t q = mass[c];
+    if (q && (double)(run + q) > want) break;
+    if (q) {
+      last = c;
+      last_run = run;
+    }
+    run += q;
+  }
+  const bool over = c == chunks;
+  if (over) {
+    c = last;
+    run = last_run;
+  }
+  const Range rc = chunk_range(c, per, a.n);
+  const int part_len = ((rc.end - rc.begin + kWaves - 1) / kWaves + 63) & ~63;
+  {
+    uint64_t q = 0;
+    const int i1 = min(rc.end, rc.begin + (wave + 1) * part_len);
+#pragma unroll 4
+    for (int i = rc.begin + wave * part_len + lane; i < i1; i += 64) {
+      const float v = l[i];
+      if (kept(v, i, mx, b, cut)) q += weight(v, mx, s.inv_t2);
+    }
+#pragma unroll
+    for (int off = 32; off > 0; off /= 2) q += (uint64_t)__shfl_xor((unsigned long long)q, off, 64);
+    __syncthreads();
+    if (lane == 0) part[wave] = q;
+    __syncthreads();
+  }
+  int w = 0;
+  last = 0;
+  last_run = run;
+  for (w = 0; w < kWaves; ++w) {
+    const uint64_t q = part[w];
+    if (!over && q && (double)(run + q) > want) break;
+    if (q) {
+      last = w;
+      last_run = run;
+    }
+    run += q;
+  }
+  if (w == kWaves) {
+    w = last;
+    run = last_run;
+  }
+  const int i0 = rc.begin + w * part_len, i1 = min(rc.end, i0 + part_len);
+  int token = -1;
+  for (int base = i0; base < i1; base += kThreads) {
+    const int i = base + t;
+    const float v = i < i1 ? l[i] : -INFINITY;
+    const uint64_t q = i < i1 && kept(v, i, mx, b, cut) ? weight(v, mx, s.inv_t2) : 0;
+    const uint64_t sum = run + block_scan(q, part);
+    const int hit = block_min(!over && q && (double)sum > want ? i : 0x7FFFFFFF, ipart);
+    if (hit != 0x7FFFFFFF) {
+      token = hit;
+      break;
+    }
+    const int far = -block_min(q ? -i : 1, ipart);   // the last one with weight, -1 without
+    token = far >= 0 ? far : token;
+    __syncthreads();
+    if (t == kThreads - 1) part[0] = sum;
+    __syncthreads();
+    run = part[0];
+  }
+  if (t == 0) {
+    a.tokens[row] = token;
+    if (a.logprobs) {
+      const float v = l[token];
       a.logprobs[row] =
-          (float)((v == mx ? 0.0 : ((double)v - (double)mx) * s.inv_t) - log((double)total * (1.0 / kOne)));
+          (float)((v == mx ? 0.0 : ((double)v - (double)mx) * s.inv_t) - log((double)total * 0x1p-44));
+    }
   }
 }
 
+// Chunks for about 512 blocks over all rows (two per CU), at most 16 per row:
+// the border launch adds them up.
 struct Plan {
-  int tiles, tiles_per_chunk, chunks;
+  int per, chunks;
 };
-// Chunks for about 512 blocks over all rows (two per CU).
 Plan plan(int64_t m, int64_t n) {
+  const int64_t tiles = (n + kThreads - 1) / kThreads;
+  int64_t want = (512 + m - 1) / m;
+  want = want < kMaxChunks ? want : kMaxChunks;
   Plan p;
-  p.tiles = (int)((n + kTile - 1) / kTile);
-  const int64_t want = (512 + m - 1) / m;
-  p.tiles_per_chunk = (int)((p.tiles + want - 1) / want);
-  p.chunks = (p.tiles + p.tiles_per_chunk - 1) / p.tiles_per_chunk;
+  p.per = (int)((tiles + want - 1) / want) * kThreads;
+  p.chunks = (int)((n + p.per - 1) / p.per);
   return p;
 }
 int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
@@ -611,8 +687,7 @@ int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
 int64_t sample_workspace_bytes(int64_t m, int64_t n) {
   const Plan p = plan(m, n);
   return align256(m * p.chunks * (int64_t)sizeof(float2)) + align256(m * (int64_t)sizeof(RowInfo)) +
-         align256(m * p.chunks * kBins * 4) + align256(m * p.chunks * kBins * 8) + align256(m * p.tiles * 8) +
-         align256(m * kCand * 8);
+         align256(m * p.chunks * kBins * 4) + align256(m * p.chunks * kBins * 8) + align256(m * kCand * 8);
 }
 
 hipError_t launch_sample(const SampleArgs& a, void* workspace, hipStream_t s) {
@@ -629,14 +704,13 @@ hipError_t launch_sample(const SampleArgs& a, void* workspace, hipStream_t s) {
   ws.info = reinterpret_cast<RowInfo*>(take(m * (int64_t)sizeof(RowInfo)));
   ws.hist_cnt = reinterpret_cast<uint32_t*>(take(m * p.chunks * kBins * 4));
   ws.hist_mass = reinterpret_cast<uint64_t*>(take(m * p.chunks * kBins * 8));
-  ws.tile_mass = reinterpret_cast<uint64_t*>(take(m * p.tiles * 8));
   ws.cand = reinterpret_cast<uint64_t*>(take(m * kCand * 8));
   const dim3 grid((unsigned)p.chunks, (unsigned)a.m), rows((unsigned)a.m), block(kThreads);
-  hipLaunchKernelGGL(sample_stats_kernel, grid, block, 0, s, a, ws, p.tiles_per_chunk);
-  hipLaunchKernelGGL(sample_hist_kernel, grid, block, 0, s, a, ws, p.tiles_per_chunk);
+  hipLaunchKernelGGL(sample_stats_kernel, grid, block, 0, s, a, ws, p.per);
+  hipLaunchKernelGGL(sample_hist_kernel, grid, block, 0, s, a, ws, p.per);
   hipLaunchKernelGGL(sample_border_kernel, rows, block, 0, s, a, ws, p.chunks);
-  hipLaunchKernelGGL(sample_collect_kernel, grid, block, 0, s, a, ws, p.tiles_per_chunk, p.tiles);
-  hipLaunchKernelGGL(sample_choose_kernel, rows, block, 0, s, a, ws, p.chunks, p.tiles);
+  hipLaunchKernelGGL(sample_collect_kernel, grid, block, 0, s, a, ws, p.per);
+  hipLaunchKernelGGL(sample_choose_kernel, rows, block, 0, s, a, ws, p.chunks, p.per);
   return hipGetLastError();
 }
 

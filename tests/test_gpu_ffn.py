@@ -50,7 +50,9 @@ def check_product(got, a, w, extra=None):
 
 # rows that end inside tiles of 16, 64, 128 and 256, k that ends inside a 64- and a 512-step
 SHAPES = [(1, 32, 1), (5, 96, 3), (16, 64, 65), (45, 160, 100), (64, 512, 70), (100, 544, 129), (130, 1024, 200),
-          (256, 2080, 64), (257, 320, 257), (300, 4096, 66), (1000, 96, 500), (512, 512, 1)]
+          (256, 2080, 64), (257, 320, 257), (300, 4096, 66), (1000, 96, 500), (512, 512, 1),
+          # few tiles and a long summed axis: split (forwards, backwards, both), ragged columns
+          (130, 4128, 100), (4100, 96, 100), (2045, 2080, 130)]
 
 
 @pytest.mark.parametrize("n,k,m", SHAPES)
