@@ -43,6 +43,7 @@ struct RowInfo {
   uint64_t mass_lo;    // weight of the bins before lo
   uint64_t mass_bk;    // weight of the bins before bk
   uint64_t total;      // weight of the row
+  float mx, c;         // the row's binning
   int lo, hi;          // the cut is in bins lo..hi (kNone: nothing is cut)
   int bk;              // the bin of rank top_k (kNone: no such bin)
   int cnt_lo, cnt_bk;  // entries in the bins before lo and before bk
@@ -333,6 +334,8 @@ __global__ __launch_bounds__(kThreads) void sample_border_kernel(SampleArgs a, W
     // Without counts only whether there are entries before matters (bin 0 holds the maximum).
     auto cnt_before = [&](int k) -> int { return k > 0 ? (counts ? (int)cnt_in[k - 1] : 1) : 0; };
     r.total = total;
+    r.mx = b.mx;
+    r.c = b.c;
     r.lo = lo;
     r.hi = hi;
     r.bk = bk;
@@ -347,34 +350,40 @@ __global__ __launch_bounds__(kThreads) void sample_border_kernel(SampleArgs a, W
 }
 
 __global__ __launch_bounds__(kThreads) void sample_collect_kernel(SampleArgs a, Ws ws, int per) {
-  const int row = blockIdx.y, c = blockIdx.x, chunks = gridDim.x;
+  __shared__ uint64_t list[kCand];
+  __shared__ int count, base;
+  const int row = blockIdx.y, c = blockIdx.x, t = threadIdx.x;
   const RowInfo& r = ws.info[row];
   const int lo = r.lo, hi = r.hi, bk = r.want_bk ? r.bk : -1;
   if (lo == kNone) return;   // nothing is cut
-  const float2 st = row_stats(ws.stats + (int64_t)row * chunks, chunks);
-  const Settings s = settings(a, row);
-  const Binning b = binning(st.x, st.y, s.t);
+  const Binning b{r.mx, r.c};
+  if (t == 0) count = 0;
+  __syncthreads();
   for_entries<8>(a.logits + (int64_t)row * a.ld, chunk_range(c, per, a.n), [&](float v, int i) {
     const int k = bin_of(v, b);
-    if (((k >= lo && k <= hi) || k == bk) && live(v, st.x)) {
-      const int at = atomicAdd(&ws.info[row].listed, 1);
-      if (at < kCand) ws.cand[(int64_t)row * kCand + at] = (uint64_t)order_of(v) << 32 | (uint32_t)i;
+    if (((k >= lo && k <= hi) || k == bk) && live(v, b.mx)) {
+      const int at = atomicAdd(&count, 1);
+      if (at < kCand) list[at] = (uint64_t)order_of(v) << 32 | (uint32_t)i;
     }
   });
+  __syncthreads();
+  // One place in the row's list per block; its order does not matter.
+  if (t == 0) base = count ? atomicAdd(&ws.info[row].listed, count) : 0;
+  __syncthreads();
+  for (int i = t; i < count && base + i < kCand; i += kThreads) ws.cand[(int64_t)row * kCand + base + i] = list[i];
 }
 
 // Kept entries: order (logit, then lower index) at or before the cut, or in a
-// bin before `lo`.
+// bin before `lo` (0 where the order alone says it).
 struct Cut {
   uint32_t order;
   int index;
   int lo;
 };
-__device__ __forceinline__ bool kept(float v, int i, float mx, const Binning& b, const Cut& c) {
-  if (!live(v, mx)) return false;
-  if (bin_of(v, b) < c.lo) return true;
+__device__ __forceinline__ bool kept(float v, int i, const Binning& b, const Cut& c) {
+  if (!live(v, b.mx)) return false;
   const uint32_t o = order_of(v);
-  return o > c.order || (o == c.order && i <= c.index);
+  return o > c.order || (o == c.order && i <= c.index) || (c.lo && bin_of(v, b) < c.lo);
 }
 
 // The number of entries ordered above `o` and their weight.
@@ -463,30 +472,59 @@ __device__ Cut bisect(const SampleArgs& a, const float* l, float mx, const Setti
   return Cut{o, same ? nth_index(o, take) : 0x7FFFFFFF, 0};
 }
 
-// Sorts key[0..N) in descending order, N a power of two from 128 to kCand; a
-// thread compares one pair at a time.  Strides up to 64 stay inside the 128
-// entries of one wave, so only the longer ones need block barriers.
-__device__ __forceinline__ void sort_desc(uint64_t* key, int N) {
-  const int t = threadIdx.x;
-  for (int k = 2; k <= N; k *= 2) {
+// Sorts the wave's 64 keys in descending order (bitonic, across lanes).
+__device__ __forceinline__ uint64_t wave_sort_desc(uint64_t v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int k = 2; k <= 64; k *= 2)
+#pragma unroll
     for (int j = k / 2; j > 0; j /= 2) {
-      if (j >= 64) __syncthreads();   // entries written by other waves (j = 64: by the step before)
-      if (t < N / 2) {
-        const int i = 2 * t - (t & (j - 1)), p = i + j;
-        const uint64_t x = key[i], y = key[p];
-        if ((x < y) == ((i & k) == 0)) {
-          key[i] = y;
-          key[p] = x;
-        }
-      }
-      if (j > 64) {
-        __syncthreads();
-      } else {
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-      }
+      const uint64_t o = (uint64_t)__shfl_xor((unsigned long long)v, j, 64);
+      const bool larger = ((lane & j) == 0) == ((lane & k) == 0);   // this lane keeps the larger of the two
+      v = (v > o) == larger ? v : o;
     }
+  return v;
+}
+
+// Sorts key[0..nc) in descending order, nc <= kCand, keys distinct: each wave
+// sorts runs of 64, then a key's place is its place in its run plus, for every
+// other run, how many keys there are larger (binary searches, independent of
+// each other).
+__device__ void sort_desc(uint64_t* key, int nc) {
+  const int t = threadIdx.x, lane = t & 63;
+  const int runs = (nc + 63) >> 6;
+  uint64_t mine[kCand / kThreads];
+  int place[kCand / kThreads];
+#pragma unroll
+  for (int e = 0; e < kCand / kThreads; ++e) {
+    const int i = e * kThreads + t;
+    if ((i >> 6) < runs) {
+      mine[e] = wave_sort_desc(i < nc ? key[i] : 0);   // empty places last
+      key[i] = mine[e];                                // kCand is a whole number of runs
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < kCand / kThreads; ++e) {
+    const int i = e * kThreads + t;
+    if ((i >> 6) >= runs) continue;
+    int at = lane;
+#pragma unroll 4
+    for (int r = 0; r < runs; ++r) {
+      const uint64_t* run = key + 64 * r;
+      int p = 0;
+#pragma unroll
+      for (int step = 32; step > 0; step /= 2) p += run[p + step - 1] > mine[e] ? step : 0;
+      p += run[p] > mine[e];
+      at += r == (i >> 6) ? 0 : p;
+    }
+    place[e] = at;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < kCand / kThreads; ++e) {
+    const int i = e * kThreads + t;
+    if ((i >> 6) < runs && mine[e]) key[place[e]] = mine[e];
   }
   __syncthreads();
 }
@@ -498,8 +536,8 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(SampleArgs a, W
   __shared__ uint64_t key[kCand];
   static_assert(kCand == 2 * kThreads, "two listed entries per thread");
   const int row = blockIdx.x, t = threadIdx.x, wave = t >> 6, lane = t & 63;
-  const float2 st = row_stats(ws.stats + (int64_t)row * chunks, chunks);
-  const float mx = st.x;
+  const RowInfo r = ws.info[row];
+  const float mx = r.mx;
   if (!(mx > -INFINITY)) {   // nothing to choose from
     if (t == 0) {
       a.tokens[row] = -1;
@@ -508,21 +546,18 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(SampleArgs a, W
     return;
   }
   const Settings s = settings(a, row);
-  const Binning b = binning(mx, st.y, s.t);
-  const RowInfo r = ws.info[row];
+  const Binning b{mx, r.c};
   const float* l = a.logits + (int64_t)row * a.ld;
-  Cut cut{0u, 0x7FFFFFFF, r.lo};   // nothing cut: lo is past every bin
+  Cut cut{0u, 0x7FFFFFFF, 0};   // nothing cut: every live entry is ordered above 0
   if (r.listed <= kCand) {
     if (t < chunks) mass[t] = r.lo ? ws.hist_mass[((int64_t)row * chunks + t) * kBins + r.lo - 1] : 0;
     if (r.lo != kNone) {
       // Larger logit first, then lower index: ~index makes "greater is ranked
-      // earlier" one comparison.  Empty places sort last.
+      // earlier" one comparison.
       const int nc = r.listed;
-      int N = 128;
-      while (N < nc) N *= 2;
-      for (int i = t; i < N; i += kThreads) key[i] = i < nc ? ws.cand[(int64_t)row * kCand + i] ^ 0xFFFFFFFFull : 0;
+      for (int i = t; i < nc; i += kThreads) key[i] = ws.cand[(int64_t)row * kCand + i] ^ 0xFFFFFFFFull;
       __syncthreads();
-      sort_desc(key, N);
+      sort_desc(key, nc);
       // Thread t holds places 2t and 2t+1; their rank and the weight before
       // them, among the listed entries.
       uint64_t w[2] = {0, 0}, before[2];
@@ -567,15 +602,19 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(SampleArgs a, W
           }
         }
       last = -block_min(-last, ipart);
-      cut.order = last < 0 ? 0xFFFFFFFFu : (uint32_t)(key[last] >> 32);   // none: above every logit
-      cut.index = last < 0 ? -1 : (int)~(uint32_t)key[last];
+      if (last >= 0) {
+        cut.order = (uint32_t)(key[last] >> 32);
+        cut.index = (int)~(uint32_t)key[last];
+      } else {   // none of the listed: the bins before lo
+        cut = Cut{0xFFFFFFFFu, -1, r.lo};
+      }
     }
   } else {
     cut = bisect(a, l, mx, s, r.total, part);
     for (int c = 0; c < chunks; ++c) {
       uint64_t q = 0;
       for_entries<1>(l, chunk_range(c, per, a.n),
-                     [&](float v, int i) { q += kept(v, i, mx, b, cut) ? weight(v, mx, s.inv_t2) : 0; });
+                     [&](float v, int i) { q += kept(v, i, b, cut) ? weight(v, mx, s.inv_t2) : 0; });
       q = block_sum(q, part);
       if (t == 0) mass[c] = q;
     }
@@ -608,12 +647,16 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(SampleArgs a, W
   const Range rc = chunk_range(c, per, a.n);
   const int part_len = ((rc.end - rc.begin + kWaves - 1) / kWaves + 63) & ~63;
   {
+    constexpr int kBatch = 10;   // loads ahead of their use
     uint64_t q = 0;
     const int i1 = min(rc.end, rc.begin + (wave + 1) * part_len);
-#pragma unroll 4
-    for (int i = rc.begin + wave * part_len + lane; i < i1; i += 64) {
-      const float v = l[i];
-      if (kept(v, i, mx, b, cut)) q += weight(v, mx, s.inv_t2);
+    for (int i = rc.begin + wave * part_len + lane; i < i1; i += 64 * kBatch) {
+      float v[kBatch];
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) v[e] = i + 64 * e < i1 ? l[i + 64 * e] : -INFINITY;
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e)
+        if (kept(v[e], i + 64 * e, b, cut)) q += weight(v[e], mx, s.inv_t2);
     }
 #pragma unroll
     for (int off = 32; off > 0; off /= 2) q += (uint64_t)__shfl_xor((unsigned long long)q, off, 64);
@@ -642,7 +685,7 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(SampleArgs a, W
   for (int base = i0; base < i1; base += kThreads) {
     const int i = base + t;
     const float v = i < i1 ? l[i] : -INFINITY;
-    const uint64_t q = i < i1 && kept(v, i, mx, b, cut) ? weight(v, mx, s.inv_t2) : 0;
+    const uint64_t q = i < i1 && kept(v, i, b, cut) ? weight(v, mx, s.inv_t2) : 0;
     const uint64_t sum = run + block_scan(q, part);
     const int hit = block_min(!over && q && (double)sum > want ? i : 0x7FFFFFFF, ipart);
     if (hit != 0x7FFFFFFF) {
@@ -658,7 +701,9 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(SampleArgs a, W
   }
   if (t == 0) {
     a.tokens[row] = token;
-    if (a.logprobs) {
+    if (a.logprobs && token < 0) {   // only if the logits changed under the call
+      a.logprobs[row] = -INFINITY;
+    } else if (a.logprobs) {
       const float v = l[token];
       a.logprobs[row] =
           (float)((v == mx ? 0.0 : ((double)v - (double)mx) * s.inv_t) - log((double)total * 0x1p-44));
@@ -666,7 +711,8 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(SampleArgs a, W
   }
 }
 
-// Chunks for about 512 blocks over all rows (two per CU), at most 16 per row:
+// Chunks for about 512 blocks over all rows (two per CU; 1024: 64x151936 69 ->
+// 73 us), at most 16 per row:
 // the border launch adds them up.
 struct Plan {
   int per, chunks;
