@@ -48,12 +48,12 @@ struct RowInfo {
   int bk;              // the bin of rank top_k (kNone: no such bin)
   int cnt_lo, cnt_bk;  // entries in the bins before lo and before bk
   int want_bk;         // bk's entries are listed too, for the weight of the top_k entries
-  int listed;          // entries listed (more than kCand: bisection)
 };
 
 struct Ws {
   float2* stats;         // [m][chunks] (max, min)
   RowInfo* info;         // [m]
+  int* listed;           // [m] entries listed (more than kCand: bisection)
   uint32_t* hist_cnt;    // [m][chunks][kBins] running sums (rows with top-k only)
   uint64_t* hist_mass;   // [m][chunks][kBins] running sums
   uint64_t* cand;        // [m][kCand] (order << 32 | index)
@@ -101,27 +101,31 @@ __device__ __forceinline__ float logit_of(uint32_t k) {
 // that is +inf.
 __device__ __forceinline__ bool live(float l, float mx) { return l > -INFINITY && (mx < INFINITY || l == mx); }
 
+// p f + c in one instruction with c in scalar registers (left to the compiler,
+// each step also copies its constant into the accumulator).
+__device__ __forceinline__ double fma_const(double p, double f, double c) {
+  double r;
+  asm("v_fma_f64 %0, %1, %2, %3" : "=v"(r) : "v"(p), "v"(f), "s"(c));
+  return r;
+}
+
 // 2^44 exp((l - mx)/t), rounded to an integer: 2^x = 2^n 2^f with |f| <= 1/2 and
-// the Taylor series of 2^f up to f^11, whose remainder is below 2^-47 (the
-// integers' half step at w = 1 is 2^-45).
+// 2^f by the polynomial of degree 10 through its values at the 11 Chebyshev
+// nodes of [-1/2, 1/2] (error below 2^-51, exact at 0; the integers' half step
+// at w = 1 is 2^-45).
 __device__ __forceinline__ uint64_t weight(float l, float mx, double inv_t2) {
   const double x = l == mx ? 0.0 : ((double)l - (double)mx) * inv_t2;
   const double n = __builtin_rint(x), f = x - n;
-  constexpr double c[12] = {1.0,
-                            6.931471805599453e-01,
-                            2.402265069591007e-01,
-                            5.550410866482158e-02,
-                            9.618129107628477e-03,
-                            1.3333558146428441e-03,
-                            1.5403530393381606e-04,
-                            1.5252733804059837e-05,
-                            1.3215486790144305e-06,
-                            1.0178086009239699e-07,
-                            7.0549116208011225e-09,
-                            4.4455382718708101e-10};   // ln(2)^k / k!
-  double p = c[11];
-#pragma unroll
-  for (int k = 10; k >= 0; --k) p = __builtin_fma(p, f, c[k]);
+  double p = fma_const(7.072585949269223e-09, f, 1.0208690299958306e-07);
+  p = fma_const(p, f, 1.321544258792169e-06);
+  p = fma_const(p, f, 1.5252657260200837e-05);
+  p = fma_const(p, f, 0.0001540353044173605);
+  p = fma_const(p, f, 0.0013333558230164974);
+  p = fma_const(p, f, 0.009618129107606888);
+  p = fma_const(p, f, 0.05550410866444772);
+  p = fma_const(p, f, 0.24022650695910097);
+  p = fma_const(p, f, 0.69314718055995);
+  p = fma_const(p, f, 1.0);
   // Adding 2^52 leaves the rounded integer in the low bits.
   const double w = __builtin_ldexp(p, (int)n + 44) + 4503599627370496.0;
   return x > -46.0 ? __builtin_bit_cast(uint64_t, w) & 0x000FFFFFFFFFFFFFull : 0;
@@ -217,26 +221,45 @@ __device__ __forceinline__ Range chunk_range(int c, int per, int n) {
   return {c * per, (c + 1) * per < n ? (c + 1) * per : n};
 }
 
-// Calls f(logit, index) for the block's entries of [r.begin, r.end), kBatch
-// loads ahead of their use.
-template <int kBatch, typename F>
-__device__ __forceinline__ void for_entries(const float* __restrict__ l, Range r, F&& f) {
-  int i = r.begin + threadIdx.x;
-  for (; i + (kBatch - 1) * kThreads < r.end; i += kBatch * kThreads) {
-    float v[kBatch];
+// The block's entries of a range in batches of kBatch per thread, each batch
+// loaded while the one before it is used; the first one when the object is
+// made.  Places past the range hold -inf.
+template <int kBatch>
+struct Entries {
+  const float* l;
+  int begin, end;
+  float a[kBatch], b[kBatch];
+  __device__ __forceinline__ void load(float (&v)[kBatch], int base) const {
 #pragma unroll
-    for (int q = 0; q < kBatch; ++q) v[q] = l[i + q * kThreads];
-#pragma unroll
-    for (int q = 0; q < kBatch; ++q) f(v[q], i + q * kThreads);
+    for (int q = 0; q < kBatch; ++q) {
+      const int i = base + q * kThreads + (int)threadIdx.x;
+      const float x = l[i < end ? i : end - 1];   // ranges are not empty; no branch around the load
+      v[q] = i < end ? x : -INFINITY;
+    }
   }
-  for (; i < r.end; i += kThreads) f(l[i], i);
-}
+  __device__ __forceinline__ Entries(const float* l_, Range r) : l(l_), begin(r.begin), end(r.end) { load(a, begin); }
+  // f(logit, index); called once.
+  template <typename F>
+  __device__ __forceinline__ void each(F&& f) {
+    constexpr int kStep = kBatch * kThreads;
+    for (int base = begin; base < end; base += 2 * kStep) {
+      load(b, base + kStep);
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) f(a[q], base + q * kThreads + (int)threadIdx.x);
+      if (base + kStep >= end) break;
+      load(a, base + 2 * kStep);
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) f(b[q], base + kStep + q * kThreads + (int)threadIdx.x);
+    }
+  }
+};
 
 __global__ __launch_bounds__(kThreads) void sample_stats_kernel(SampleArgs a, Ws ws, int per) {
   __shared__ float2 part[kWaves];
   const int row = blockIdx.y, c = blockIdx.x;
   float mx = -INFINITY, mn = INFINITY;
-  for_entries<8>(a.logits + (int64_t)row * a.ld, chunk_range(c, per, a.n), [&](float v, int) {
+  Entries<8> in(a.logits + (int64_t)row * a.ld, chunk_range(c, per, a.n));
+  in.each([&](float v, int) {
     mx = fmaxf(mx, v);   // NaN leaves the other operand
     mn = v > -INFINITY ? fminf(mn, v) : mn;
   });
@@ -253,6 +276,7 @@ __global__ __launch_bounds__(kThreads) void sample_stats_kernel(SampleArgs a, Ws
       mn = fminf(mn, part[w].y);
     }
     ws.stats[(int64_t)row * gridDim.x + c] = make_float2(mx, mn);
+    if (c == 0) ws.listed[row] = 0;
   }
 }
 
@@ -261,6 +285,7 @@ __global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a, Ws 
   __shared__ unsigned long long mass[kBins];
   __shared__ uint64_t part[kWaves];
   const int row = blockIdx.y, c = blockIdx.x, chunks = gridDim.x;
+  Entries<4> in(a.logits + (int64_t)row * a.ld, chunk_range(c, per, a.n));
   const float2 st = row_stats(ws.stats + (int64_t)row * chunks, chunks);
   const Settings s = settings(a, row);
   const Binning b = binning(st.x, st.y, s.t);
@@ -268,11 +293,10 @@ __global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a, Ws 
   cnt[threadIdx.x] = 0;
   mass[threadIdx.x] = 0;
   __syncthreads();
-  for_entries<4>(a.logits + (int64_t)row * a.ld, chunk_range(c, per, a.n), [&](float v, int) {
-    if (!live(v, st.x)) return;
+  in.each([&](float v, int) {
     const int k = bin_of(v, b);
-    const uint64_t q = weight(v, st.x, s.inv_t2);
-    if (counts) atomicAdd(&cnt[k], 1u);
+    const uint64_t q = weight(v, st.x, s.inv_t2);   // 0 for masked entries
+    if (counts && live(v, st.x)) atomicAdd(&cnt[k], 1u);
     if (q) atomicAdd(&mass[k], (unsigned long long)q);
   });
   __syncthreads();
@@ -281,14 +305,15 @@ __global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a, Ws 
   if (counts) ws.hist_cnt[at] = (uint32_t)block_scan(cnt[threadIdx.x], part);
 }
 
+// The bins in which the row's cut can fall, from its chunks' running sums.  A
+// launch of its own: found by every collect block for itself, the sums' reads
+// cost more than the launch (64x151936: 5 + 9 us against 20 in one).
 __global__ __launch_bounds__(kThreads) void sample_border_kernel(SampleArgs a, Ws ws, int chunks) {
-  __shared__ int ipart[kWaves];
   __shared__ uint64_t mass_in[kBins];   // sums up to and with each bin
   __shared__ uint32_t cnt_in[kBins];
+  __shared__ int ipart[kWaves];
   const int row = blockIdx.x, t = threadIdx.x;
-  const float2 st = row_stats(ws.stats + (int64_t)row * chunks, chunks);
   const Settings s = settings(a, row);
-  const Binning b = binning(st.x, st.y, s.t);
   const bool counts = s.k < a.n;
   uint64_t mi = 0;
   uint32_t ci = 0;
@@ -298,6 +323,8 @@ __global__ __launch_bounds__(kThreads) void sample_border_kernel(SampleArgs a, W
     mi += c < chunks ? ws.hist_mass[at + (int64_t)c * kBins] : 0;
     ci += counts && c < chunks ? ws.hist_cnt[at + (int64_t)c * kBins] : 0;
   }
+  const float2 st = row_stats(ws.stats + (int64_t)row * chunks, chunks);
+  const Binning b = binning(st.x, st.y, s.t);
   mass_in[t] = mi;
   cnt_in[t] = ci;
   __syncthreads();
@@ -312,7 +339,8 @@ __global__ __launch_bounds__(kThreads) void sample_border_kernel(SampleArgs a, W
   if (s.use_p) {
     const uint64_t s_lo = bk == kNone ? total : (bk ? mass_in[bk - 1] : 0);
     const uint64_t s_hi = bk == kNone ? total : mass_in[bk];
-    const int p_lo = first((double)mi >= s.p * (double)s_lo), p_hi = first((double)mi >= s.p * (double)s_hi);
+    const int p_lo = first((double)mi >= s.p * (double)s_lo);
+    const int p_hi = s_lo == s_hi ? p_lo : first((double)mi >= s.p * (double)s_hi);
     lo = min(lo, p_lo);
     hi = min(hi, p_hi);
   }
@@ -328,38 +356,37 @@ __global__ __launch_bounds__(kThreads) void sample_border_kernel(SampleArgs a, W
     lo = min(lo, e_lo);
     hi = min(hi, e_hi);
   }
-  if (t == 0) {
-    RowInfo r;
-    auto mass_before = [&](int k) -> uint64_t { return k > 0 ? mass_in[k - 1] : 0; };
-    // Without counts only whether there are entries before matters (bin 0 holds the maximum).
-    auto cnt_before = [&](int k) -> int { return k > 0 ? (counts ? (int)cnt_in[k - 1] : 1) : 0; };
-    r.total = total;
-    r.mx = b.mx;
-    r.c = b.c;
-    r.lo = lo;
-    r.hi = hi;
-    r.bk = bk;
-    r.want_bk = s.use_p && bk != kNone && !(lo <= bk && bk <= hi);
-    r.mass_lo = mass_before(lo);
-    r.cnt_lo = cnt_before(lo);
-    r.mass_bk = mass_before(bk);
-    r.cnt_bk = cnt_before(bk);
-    r.listed = 0;
-    ws.info[row] = r;
-  }
+  if (t != 0) return;
+  RowInfo r;
+  auto mass_before = [&](int k) -> uint64_t { return k > 0 ? mass_in[k - 1] : 0; };
+  // Without counts only whether there are entries before matters (bin 0 holds the maximum).
+  auto cnt_before = [&](int k) -> int { return k > 0 ? (counts ? (int)cnt_in[k - 1] : 1) : 0; };
+  r.total = total;
+  r.mx = b.mx;
+  r.c = b.c;
+  r.lo = lo;
+  r.hi = hi;
+  r.bk = bk;
+  r.want_bk = s.use_p && bk != kNone && !(lo <= bk && bk <= hi);
+  r.mass_lo = mass_before(lo);
+  r.cnt_lo = cnt_before(lo);
+  r.mass_bk = mass_before(bk);
+  r.cnt_bk = cnt_before(bk);
+  ws.info[row] = r;
 }
 
 __global__ __launch_bounds__(kThreads) void sample_collect_kernel(SampleArgs a, Ws ws, int per) {
   __shared__ uint64_t list[kCand];
   __shared__ int count, base;
   const int row = blockIdx.y, c = blockIdx.x, t = threadIdx.x;
+  Entries<8> in(a.logits + (int64_t)row * a.ld, chunk_range(c, per, a.n));
   const RowInfo& r = ws.info[row];
   const int lo = r.lo, hi = r.hi, bk = r.want_bk ? r.bk : -1;
   if (lo == kNone) return;   // nothing is cut
   const Binning b{r.mx, r.c};
   if (t == 0) count = 0;
   __syncthreads();
-  for_entries<8>(a.logits + (int64_t)row * a.ld, chunk_range(c, per, a.n), [&](float v, int i) {
+  in.each([&](float v, int i) {
     const int k = bin_of(v, b);
     if (((k >= lo && k <= hi) || k == bk) && live(v, b.mx)) {
       const int at = atomicAdd(&count, 1);
@@ -368,7 +395,7 @@ __global__ __launch_bounds__(kThreads) void sample_collect_kernel(SampleArgs a, 
   });
   __syncthreads();
   // One place in the row's list per block; its order does not matter.
-  if (t == 0) base = count ? atomicAdd(&ws.info[row].listed, count) : 0;
+  if (t == 0) base = count ? atomicAdd(&ws.listed[row], count) : 0;
   __syncthreads();
   for (int i = t; i < count && base + i < kCand; i += kThreads) ws.cand[(int64_t)row * kCand + base + i] = list[i];
 }
@@ -549,12 +576,13 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(SampleArgs a, W
   const Binning b{mx, r.c};
   const float* l = a.logits + (int64_t)row * a.ld;
   Cut cut{0u, 0x7FFFFFFF, 0};   // nothing cut: every live entry is ordered above 0
-  if (r.listed <= kCand) {
+  const int listed = r.lo == kNone ? 0 : ws.listed[row];
+  if (listed <= kCand) {
     if (t < chunks) mass[t] = r.lo ? ws.hist_mass[((int64_t)row * chunks + t) * kBins + r.lo - 1] : 0;
     if (r.lo != kNone) {
       // Larger logit first, then lower index: ~index makes "greater is ranked
       // earlier" one comparison.
-      const int nc = r.listed;
+      const int nc = listed;
       for (int i = t; i < nc; i += kThreads) key[i] = ws.cand[(int64_t)row * kCand + i] ^ 0xFFFFFFFFull;
       __syncthreads();
       sort_desc(key, nc);
@@ -613,8 +641,8 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(SampleArgs a, W
     cut = bisect(a, l, mx, s, r.total, part);
     for (int c = 0; c < chunks; ++c) {
       uint64_t q = 0;
-      for_entries<1>(l, chunk_range(c, per, a.n),
-                     [&](float v, int i) { q += kept(v, i, b, cut) ? weight(v, mx, s.inv_t2) : 0; });
+      Entries<4> in(l, chunk_range(c, per, a.n));
+      in.each([&](float v, int i) { q += kept(v, i, b, cut) ? weight(v, mx, s.inv_t2) : 0; });
       q = block_sum(q, part);
       if (t == 0) mass[c] = q;
     }
@@ -732,7 +760,7 @@ int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
 
 int64_t sample_workspace_bytes(int64_t m, int64_t n) {
   const Plan p = plan(m, n);
-  return align256(m * p.chunks * (int64_t)sizeof(float2)) + align256(m * (int64_t)sizeof(RowInfo)) +
+  return align256(m * p.chunks * (int64_t)sizeof(float2)) + align256(m * (int64_t)sizeof(RowInfo)) + align256(m * 4) +
          align256(m * p.chunks * kBins * 4) + align256(m * p.chunks * kBins * 8) + align256(m * kCand * 8);
 }
 
@@ -748,6 +776,7 @@ hipError_t launch_sample(const SampleArgs& a, void* workspace, hipStream_t s) {
   Ws ws;
   ws.stats = reinterpret_cast<float2*>(take(m * p.chunks * (int64_t)sizeof(float2)));
   ws.info = reinterpret_cast<RowInfo*>(take(m * (int64_t)sizeof(RowInfo)));
+  ws.listed = reinterpret_cast<int*>(take(m * 4));
   ws.hist_cnt = reinterpret_cast<uint32_t*>(take(m * p.chunks * kBins * 4));
   ws.hist_mass = reinterpret_cast<uint64_t*>(take(m * p.chunks * kBins * 8));
   ws.cand = reinterpret_cast<uint64_t*>(take(m * kCand * 8));
