@@ -10,7 +10,7 @@ using namespace q3::check;
 
 namespace {
 
-constexpr int64_t kMaxK = int64_t(1) << 24;   // summed axis of the many-token products
+constexpr int64_t kMaxK = int64_t(1) << 21;   // rows and columns: 256 widened rows stay below 2 GiB
 constexpr int64_t kMaxM = int64_t(1) << 31;   // exclusive
 
 // A packed matrix and bf16 token rows of `cols` columns in front of it.  A

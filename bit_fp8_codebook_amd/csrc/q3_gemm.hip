@@ -11,6 +11,8 @@
 // of tokens; so the matrix is widened once, exactly, to bf16 in the caller's
 // workspace (for the gradient: transposed) and all three run on one kernel:
 // C = A B^T with both operands bf16 and contiguous along the summed axis.
+#include <type_traits>
+
 #include "q3_act.h"
 #include "q3_device.h"
 #include "q3_internal.h"
@@ -170,24 +172,64 @@ __device__ __forceinline__ void load_lds16(rsrc_t r, uint8_t* dst, uint32_t voff
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, voff, soff, 0, 0);
 }
 
-// Block of WM x WN waves on a BM x BN tile (tokens x weight rows), 64 of the
-// summed axis at a time through two LDS buffers filled by direct-to-LDS loads.
+// acc[m] += w x[m]^T.  Eight products (a wave of the large block) are one piece
+// of assembly with their sums in accumulation registers: the 256 of them are
+// exactly that file, and left to the register allocator the sums move between
+// the two files all through the loop.  What the compiler then does not know it
+// need not: the leading s_nop covers a vector instruction that wrote an operand,
+// a sum is next used 64 products later, and mfma_done() lets the last ones end.
+template <int TM>
+__device__ __forceinline__ void mfma_row(bf16x8 w, const bf16x8 (&x)[TM], f32x4 (&acc)[TM]) {
+  if constexpr (TM == 8) {
+    asm volatile(
+        "s_nop 1\n"
+        "v_mfma_f32_16x16x32_bf16 %0, %8, %9, %0\n"
+        "v_mfma_f32_16x16x32_bf16 %1, %8, %10, %1\n"
+        "v_mfma_f32_16x16x32_bf16 %2, %8, %11, %2\n"
+        "v_mfma_f32_16x16x32_bf16 %3, %8, %12, %3\n"
+        "v_mfma_f32_16x16x32_bf16 %4, %8, %13, %4\n"
+        "v_mfma_f32_16x16x32_bf16 %5, %8, %14, %5\n"
+        "v_mfma_f32_16x16x32_bf16 %6, %8, %15, %6\n"
+        "v_mfma_f32_16x16x32_bf16 %7, %8, %16, %7\n"
+        : "+a"(acc[0]), "+a"(acc[1]), "+a"(acc[2]), "+a"(acc[3]), "+a"(acc[4]), "+a"(acc[5]), "+a"(acc[6]),
+          "+a"(acc[7])
+        : "v"(w), "v"(x[0]), "v"(x[1]), "v"(x[2]), "v"(x[3]), "v"(x[4]), "v"(x[5]), "v"(x[6]), "v"(x[7]));
+  } else {
+#pragma unroll
+    for (int m = 0; m < TM; ++m) acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x[m], acc[m], 0, 0, 0);
+  }
+}
+template <int TM>
+__device__ __forceinline__ void mfma_done() {
+  if constexpr (TM == 8) asm volatile("s_nop 15\ns_nop 15" ::: "memory");
+}
+
+// Block of four waves (2 x 2) on a 32 TM x 32 TN tile (tokens x weight rows), 64
+// of the summed axis at a time (whole 128-byte lines: 64-byte pieces ask the L2
+// twice as often, and with four buffers of 32 the L2 bound the kernel at 1.23
+// PFLOP/s) through two LDS buffers filled by direct-to-LDS loads.  A step has
+// two halves of 32: while the products of one half run from registers, the
+// fragments of the next are read.  The second half's fragments are read early in
+// the first half, so that the buffer is free and the loads of the step after
+// next leave a whole step and more before they are waited for (asked for half a
+// step later, a miss of the L2 held up every step).
 // A buffer row is 128 bytes in 8 chunks of 16; row r keeps chunk c at position
 // c ^ (r & 7) (the loads permute which chunk a lane fetches), so the 16 rows a
 // fragment read touches fall on distinct banks.  Weights are the MFMA's A
 // operand: a lane then holds four consecutive weight rows of one token, which
 // leave in one store.
-// kGlu: the 16 TN weight rows of a wave are 8 TN gate rows and the 8 TN up
-// rows of the same outputs, so the product is formed in registers.
-template <int BM, int BN, int WM, int WN, int kEpi>
-__global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
-  constexpr int kW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
+// kGlu: half of a wave's weight rows are gate rows and half the up rows of the
+// same outputs, so the product is formed in registers.
+template <int TM, int TN, int kEpi>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TM * TN > 32 ? 1 : 2)))
+void gemm_kernel(GemmArgs g) {
+  constexpr int BM = 32 * TM, BN = 32 * TN;
   constexpr uint32_t kABytes = BM * 128, kBuf = (BM + BN) * 128;
   constexpr int kOut = kEpi == kGlu ? BN / 2 : BN;   // outputs per tile
   extern __shared__ __align__(16) uint8_t lds[];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave / WN, wn = wave % WN;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
 
   // Tiles go to the 8 XCDs in contiguous runs (blocks are dealt round robin),
   // and inside a run in columns of up to 8 token tiles, so the blocks that
@@ -197,53 +239,47 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
   const int t = xcd * per + (xcd < rem ? xcd : rem) + (id >> 3);
   const int gsize = 8 * g.tiles_n, grp = t / gsize, in = t - grp * gsize;
   const int gm = g.tiles_m - grp * 8 < 8 ? g.tiles_m - grp * 8 : 8;
-  const int64_t m0 = (int64_t)(grp * 8 + in % gm) * BM;
-  const int64_t n0 = (int64_t)(in / gm) * kOut;
+  const int64_t m0 = (int64_t)__builtin_amdgcn_readfirstlane(grp * 8 + in % gm) * BM;   // divisions are vector work
+  const int64_t n0 = (int64_t)__builtin_amdgcn_readfirstlane(in / gm) * kOut;
 
-  const int64_t rows_a = g.m - m0 < BM ? g.m - m0 : BM;
-  const rsrc_t ra = make_rsrc(g.a + m0 * g.lda, (uint32_t)(((rows_a - 1) * g.lda + g.k) * 2));
+  // A load instruction brings 8 rows: lane l row l/8, the chunk that belongs at
+  // position l%8.  Each wave loads a quarter of the token rows and a quarter
+  // of the weight rows, which lie together in memory (kGlu: the gate or the
+  // up rows of one wave column).
+  constexpr int kLoadsA = TM, kLoadsB = TN;
   const int r8 = lane >> 3, chunk = (lane & 7) ^ r8;
   const uint32_t lda2 = (uint32_t)g.lda * 2u, ldb2 = (uint32_t)g.ldb * 2u;
-  const uint32_t va = (uint32_t)r8 * lda2, vb = (uint32_t)r8 * ldb2 + 16u * chunk;
-  // Weight rows of the tile in runs of 8: first row of run j (wave-uniform).
-  auto b_row = [&](int j) -> int64_t {
-    if constexpr (kEpi == kGlu) {
-      constexpr int kHalf = 8 * TN;   // outputs per wave
-      const int wcol = 8 * j / (16 * TN), o = 8 * j % (16 * TN);
-      return n0 + wcol * kHalf + (o < kHalf ? o : g.n + o - kHalf);
-    } else {
-      return n0 + 8 * j;
-    }
-  };
-  constexpr int kLoadsA = BM / 8 / kW, kLoadsB = BN / 8 / kW;
-  static_assert(BM % (8 * kW) == 0 && BN % (8 * kW) == 0, "whole loads per wave");
-  const uint16_t* pb[kLoadsB];
-  uint32_t vbl[kLoadsB];
-#pragma unroll
-  for (int q = 0; q < kLoadsB; ++q) {
-    const int64_t row = b_row(wave * kLoadsB + q);
-    const int64_t end = kEpi == kGlu ? (row < g.n ? g.n : 2 * g.n) : g.n;
-    pb[q] = g.b + row * g.ldb;
-    vbl[q] = row + r8 < end && (kEpi != kGlu || row < 2 * g.n) ? vb : kOob;
-  }
-  uint32_t val[kLoadsA];
+  const int64_t rows_a = g.m - m0 < BM ? g.m - m0 : BM;
+  const rsrc_t ra = make_rsrc(g.a + m0 * g.lda, (uint32_t)(((rows_a - 1) * g.lda + g.k) * 2));
+  const int64_t b0 = kEpi == kGlu ? n0 + (wave >> 1) * (8 * TN) : n0 + wave * (8 * TN);
+  const int64_t rows_b = g.n - b0;   // weight rows from b0 on (may be negative)
+  const rsrc_t rb = make_rsrc(g.b + (b0 + (kEpi == kGlu && (wave & 1) ? g.n : 0)) * g.ldb, (uint32_t)(8 * TN) * ldb2);
+  uint32_t va[kLoadsA], vb[kLoadsB];
 #pragma unroll
   for (int q = 0; q < kLoadsA; ++q)
-    val[q] = m0 + 8 * (wave * kLoadsA + q) + r8 < g.m ? va : kOob;
+    va[q] = 8 * (wave * kLoadsA + q) + r8 < rows_a ? (uint32_t)r8 * lda2 : kOob;
+#pragma unroll
+  for (int q = 0; q < kLoadsB; ++q) vb[q] = 8 * q + r8 < rows_b ? (uint32_t)r8 * ldb2 + 16u * chunk : kOob;
 
-  auto load = [&](int s, uint32_t buf) {
+  const int64_t all = (g.k + 63) / 64;
+  const int s0 = (int)(all * blockIdx.y / gridDim.y), s1 = (int)(all * (blockIdx.y + 1) / gridDim.y);
+  // Loads q0 .. q1-1 of step s; steps past the last read out of range (no traffic).
+  auto load = [&](int s, int q0, int q1) {
+    uint8_t* buf = lds + (s & 1) * kBuf;
+    const bool live = s < s1;
     // Chunks past k (only in the last step) read the row's first chunk of the
     // step instead: finite values that meet b's zeros.
     const uint32_t ca = 64 * (int64_t)s + 8 * chunk < g.k ? 16u * chunk : 0u;
 #pragma unroll
-    for (int q = 0; q < kLoadsA; ++q) {
-      const uint32_t row8 = (uint32_t)(wave * kLoadsA + q) * 8u;
-      load_lds16(ra, lds + buf + row8 * 128u, val[q] + ca, row8 * lda2 + 128u * (uint32_t)s);
-    }
-#pragma unroll
-    for (int q = 0; q < kLoadsB; ++q) {
-      const uint32_t row8 = (uint32_t)(wave * kLoadsB + q) * 8u;
-      load_lds16(make_rsrc(pb[q], 8u * ldb2), lds + buf + kABytes + row8 * 128u, vbl[q], 128u * (uint32_t)s);
+    for (int q = q0; q < q1; ++q) {
+      if (q < kLoadsA) {
+        const uint32_t row = (uint32_t)(wave * kLoadsA + q) * 8u;
+        load_lds16(ra, buf + row * 128u, live ? va[q] + ca : kOob, row * lda2 + 128u * (uint32_t)s);
+      } else {
+        const int p = q - kLoadsA;
+        const uint32_t row = (uint32_t)(wave * kLoadsB + p) * 8u;
+        load_lds16(rb, buf + kABytes + row * 128u, live ? vb[p] : kOob, (uint32_t)(8 * p) * ldb2 + 128u * (uint32_t)s);
+      }
     }
   };
 
@@ -253,38 +289,69 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
 #pragma unroll
     for (int m = 0; m < TM; ++m) acc[n][m] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // Fragment address: row lane%16 of a 16-row tile, chunk lane/16 (+4 for the
-  // second half of the step), swizzled.
+  // Fragment address: row lane%16 of a 16-row tile, chunk 4 half + lane/16, swizzled.
   const uint32_t frag = (uint32_t)(lane & 15) * 128u + (((uint32_t)lane >> 4) ^ ((uint32_t)lane & 7u)) * 16u;
-  const uint32_t fa = (uint32_t)(wm * TM * 16) * 128u + frag;
-  const uint32_t fb = kABytes + (uint32_t)(wn * TN * 16) * 128u + frag;
-  const int64_t all = (g.k + 63) / 64;
-  const int s0 = (int)(all * blockIdx.y / gridDim.y), s1 = (int)(all * (blockIdx.y + 1) / gridDim.y);
-  if (s0 < s1) load(s0, 0u);
-  __builtin_amdgcn_s_waitcnt(0);
-  __syncthreads();
-  uint32_t buf = 0;
+  const uint32_t fa = (uint32_t)(wm * TM) * 2048u + frag;
+  const uint32_t fb = kABytes + (uint32_t)(wn * TN) * 2048u + frag;
+  auto read_w = [&](int s, uint32_t half, int n) {
+    return *reinterpret_cast<const bf16x8*>(lds + (s & 1) * kBuf + (fb ^ 64u * half) + n * 2048u);
+  };
+  auto read_x = [&](int s, uint32_t half, int m) {
+    return *reinterpret_cast<const bf16x8*>(lds + (s & 1) * kBuf + (fa ^ 64u * half) + m * 2048u);
+  };
+  struct Frags {
+    bf16x8 w[TN], x[TM];
+  };
+  constexpr int kLoads = kLoadsA + kLoadsB;
+  constexpr int kEarly = TN / 4;            // rows of products beside which a half's fragments are read
+  constexpr int kLoads1 = TN - kEarly;      // loads in the first half, one a row; the rest in the second
+  auto meet = [&](auto wait) {
+    __builtin_amdgcn_s_waitcnt(decltype(wait)::value);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  constexpr std::integral_constant<int, 0xC07F> read_done{};   // lgkmcnt(0)
+  constexpr std::integral_constant<int, kLoads1 | 0x0F70> landed{};   // vmcnt(kLoads1)
+  static_assert(kLoads1 < 16, "vmcnt's low field");
+  Frags f0, f1;
+  load(s0, 0, kLoads);
+  load(s0 + 1, 0, kLoads);
+  meet(std::integral_constant<int, (kLoads & 15) | (kLoads >> 4) << 14 | 0x0F70>{});
+#pragma unroll
+  for (int n = 0; n < TN; ++n) f0.w[n] = read_w(s0, 0, n);
+#pragma unroll
+  for (int m = 0; m < TM; ++m) f0.x[m] = read_x(s0, 0, m);
   for (int s = s0; s < s1; ++s) {
-    if (s + 1 < s1) load(s + 1, kBuf - buf);
+    // First half: its products; the second half's fragments beside the first
+    // rows, then the first loads of step s+2 into the buffer that is free by then.
 #pragma unroll
-    for (uint32_t half = 0; half < 2; ++half) {
-      bf16x8 wv[TN], xv[TM];
+    for (int n = 0; n < TN; ++n) {
+      if (n < kEarly) {
 #pragma unroll
-      for (int n = 0; n < TN; ++n)
-        wv[n] = *reinterpret_cast<const bf16x8*>(lds + buf + ((fb + n * 2048u) ^ (64u * half)));
+        for (int i = 4 * n; i < 4 * n + 4; ++i) f1.w[i] = read_w(s, 1, i);
 #pragma unroll
-      for (int m = 0; m < TM; ++m)
-        xv[m] = *reinterpret_cast<const bf16x8*>(lds + buf + ((fa + m * 2048u) ^ (64u * half)));
-#pragma unroll
-      for (int n = 0; n < TN; ++n)
-#pragma unroll
-        for (int m = 0; m < TM; ++m)
-          acc[n][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[n], xv[m], acc[n][m], 0, 0, 0);
+        for (int m = n * TM / kEarly; m < (n + 1) * TM / kEarly; ++m) f1.x[m] = read_x(s, 1, m);
+      } else {
+        load(s + 2, n - kEarly, n - kEarly + 1);
+      }
+      mfma_row<TM>(f0.w[n], f0.x, acc[n]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (n == kEarly - 1) meet(read_done);
     }
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    buf = kBuf - buf;
+    meet(landed);   // step s+1: all but the loads just asked for
+    // Second half; the next step's first fragments and the rest of the loads.
+#pragma unroll
+    for (int n = 0; n < TN; ++n) {
+      f0.w[n] = read_w(s + 1, 0, n);
+#pragma unroll
+      for (int m = n * TM / TN; m < (n + 1) * TM / TN; ++m) f0.x[m] = read_x(s + 1, 0, m);
+      load(s + 2, kLoads1 + n * (kLoads - kLoads1) / TN, kLoads1 + (n + 1) * (kLoads - kLoads1) / TN);
+      mfma_row<TM>(f1.w[n], f1.x, acc[n]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
+  __builtin_amdgcn_s_waitcnt(0);   // no load into LDS outlives the block
+  mfma_done<TM>();
 
   // Lane l holds weight rows 4*(l/16)..+3 of each tile for token l%16.
 #pragma unroll
@@ -328,20 +395,20 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
   }
 }
 
-template <int BM, int BN, int WM, int WN, int kEpi>
+template <int TM, int TN, int kEpi>
 hipError_t launch_gemm_one(GemmArgs g, int splits, hipStream_t s) {
-  constexpr int kOut = kEpi == kGlu ? BN / 2 : BN;
+  constexpr int BM = 32 * TM, BN = 32 * TN, kOut = kEpi == kGlu ? BN / 2 : BN;
   constexpr size_t shm = 2 * (BM + BN) * 128;
   static LdsAllowance seen;
   const hipError_t e =
-      allow_dynamic_lds(reinterpret_cast<const void*>(gemm_kernel<BM, BN, WM, WN, kEpi>), shm, seen);
+      allow_dynamic_lds(reinterpret_cast<const void*>(gemm_kernel<TM, TN, kEpi>), shm, seen);
   if (e != hipSuccess) return e;
   const int64_t tm = (g.m + BM - 1) / BM, tn = (g.n + kOut - 1) / kOut;
   if (tm * tn > 0x7FFFFFFF) return hipErrorInvalidValue;
   g.tiles_m = (int)tm;
   g.tiles_n = (int)tn;
-  hipLaunchKernelGGL((gemm_kernel<BM, BN, WM, WN, kEpi>), dim3((unsigned)(tm * tn), (unsigned)splits),
-                     dim3(64 * WM * WN), shm, s, g);
+  hipLaunchKernelGGL((gemm_kernel<TM, TN, kEpi>), dim3((unsigned)(tm * tn), (unsigned)splits),
+                     dim3(256), shm, s, g);
   return hipGetLastError();
 }
 
@@ -373,7 +440,7 @@ __global__ __launch_bounds__(256) void gemm_reduce_kernel(const float* __restric
 // Block shape and splits of the summed axis for m tokens, n outputs (weight
 // rows) and k summed.
 struct GemmPlan {
-  bool big;     // 256 x 256 blocks of 8 waves, else 128 x 128 of 4
+  bool big;     // 256 x 256 blocks, else 128 x 128
   int splits;
 };
 GemmPlan plan_gemm(int64_t m, int64_t n, int64_t k, bool may_split) {
@@ -396,16 +463,16 @@ int64_t split_bytes(int64_t m, int64_t n, int64_t k) {
 }
 
 hipError_t launch_glu_gemm(const GemmArgs& g, hipStream_t s) {
-  if (plan_gemm(g.m, 2 * g.n, g.k, false).big) return launch_gemm_one<256, 256, 2, 4, kGlu>(g, 1, s);
-  return launch_gemm_one<128, 128, 2, 2, kGlu>(g, 1, s);
+  if (plan_gemm(g.m, 2 * g.n, g.k, false).big) return launch_gemm_one<8, 8, kGlu>(g, 1, s);
+  return launch_gemm_one<4, 4, kGlu>(g, 1, s);
 }
 
 // part: split_bytes(m, n, k) bytes, 16-byte aligned.
 hipError_t launch_f32_gemm(GemmArgs g, float* part, hipStream_t s) {
   const GemmPlan p = plan_gemm(g.m, g.n, g.k, true);
   if (p.splits == 1) {
-    if (p.big) return launch_gemm_one<256, 256, 2, 4, kStoreF32>(g, 1, s);
-    return launch_gemm_one<128, 128, 2, 2, kStoreF32>(g, 1, s);
+    if (p.big) return launch_gemm_one<8, 8, kStoreF32>(g, 1, s);
+    return launch_gemm_one<4, 4, kStoreF32>(g, 1, s);
   }
   float* y = g.c;
   const int64_t ldy = g.ldc;
@@ -414,7 +481,7 @@ hipError_t launch_f32_gemm(GemmArgs g, float* part, hipStream_t s) {
   g.ldc = (g.n + 3) / 4 * 4;
   g.split_stride = plane_floats(g.m, g.n);
   g.vec = 1;
-  const hipError_t e = launch_gemm_one<128, 128, 2, 2, kStoreF32>(g, p.splits, s);
+  const hipError_t e = launch_gemm_one<4, 4, kStoreF32>(g, p.splits, s);
   if (e != hipSuccess) return e;
   const int64_t blocks = (g.m * ((g.n + 3) / 4) + 255) / 256;
   hipLaunchKernelGGL(gemm_reduce_kernel, dim3((unsigned)blocks), dim3(256), 0, s, part, g.split_stride, p.splits, g.m,
