@@ -172,31 +172,36 @@ __device__ __forceinline__ void load_lds16(rsrc_t r, uint8_t* dst, uint32_t voff
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, voff, soff, 0, 0);
 }
 
-// acc[m] += w x[m]^T.  Eight products (a wave of the large block) are one piece
-// of assembly with their sums in accumulation registers: the 256 of them are
-// exactly that file, and left to the register allocator the sums move between
-// the two files all through the loop.  What the compiler then does not know it
-// need not: the leading s_nop covers a vector instruction that wrote an operand,
-// a sum is next used 64 products later, and mfma_done() lets the last ones end.
-template <int TM>
-__device__ __forceinline__ void mfma_row(bf16x8 w, const bf16x8 (&x)[TM], f32x4 (&acc)[TM]) {
-  if constexpr (TM == 8) {
+// acc0 += w x0^T, acc1 += w x1^T.  In the large block (kBig) as assembly with
+// the sums in accumulation registers: a wave's 256 of them are exactly that file,
+// and left to the register allocator the sums move between the two files all
+// through the loop.  What the compiler then does not know it need not: the
+// leading s_nop covers a vector instruction that wrote an operand, a sum is next
+// used 64 products later, and mfma_done() lets the last ones end.
+template <bool kBig>
+__device__ __forceinline__ void mfma_pair(bf16x8 w, bf16x8 x0, bf16x8 x1, f32x4& acc0, f32x4& acc1) {
+  if constexpr (kBig) {
     asm volatile(
         "s_nop 1\n"
-        "v_mfma_f32_16x16x32_bf16 %0, %8, %9, %0\n"
-        "v_mfma_f32_16x16x32_bf16 %1, %8, %10, %1\n"
-        "v_mfma_f32_16x16x32_bf16 %2, %8, %11, %2\n"
-        "v_mfma_f32_16x16x32_bf16 %3, %8, %12, %3\n"
-        "v_mfma_f32_16x16x32_bf16 %4, %8, %13, %4\n"
-        "v_mfma_f32_16x16x32_bf16 %5, %8, %14, %5\n"
-        "v_mfma_f32_16x16x32_bf16 %6, %8, %15, %6\n"
-        "v_mfma_f32_16x16x32_bf16 %7, %8, %16, %7\n"
-        : "+a"(acc[0]), "+a"(acc[1]), "+a"(acc[2]), "+a"(acc[3]), "+a"(acc[4]), "+a"(acc[5]), "+a"(acc[6]),
-          "+a"(acc[7])
-        : "v"(w), "v"(x[0]), "v"(x[1]), "v"(x[2]), "v"(x[3]), "v"(x[4]), "v"(x[5]), "v"(x[6]), "v"(x[7]));
+        "v_mfma_f32_16x16x32_bf16 %0, %2, %3, %0\n"
+        "v_mfma_f32_16x16x32_bf16 %1, %2, %4, %1\n"
+        : "+a"(acc0), "+a"(acc1)
+        : "v"(w), "v"(x0), "v"(x1));
   } else {
+    acc0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x0, acc0, 0, 0, 0);
+    acc1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x1, acc1, 0, 0, 0);
+  }
+}
+// acc[m] += w x[m]^T, two products at a time, each pair behind beside(pair): a
+// read or a load between every two products, so that the matrix core does not
+// run dry while the wave issues them.
+template <int TM, typename Beside>
+__device__ __forceinline__ void mfma_row(bf16x8 w, const bf16x8 (&x)[TM], f32x4 (&acc)[TM], Beside&& beside) {
 #pragma unroll
-    for (int m = 0; m < TM; ++m) acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x[m], acc[m], 0, 0, 0);
+  for (int m = 0; m < TM; m += 2) {
+    beside(m / 2);
+    mfma_pair<TM == 8>(w, x[m], x[m + 1], acc[m], acc[m + 1]);
+    __builtin_amdgcn_sched_barrier(0);
   }
 }
 template <int TM>
@@ -257,29 +262,27 @@ void gemm_kernel(GemmArgs g) {
   uint32_t va[kLoadsA], vb[kLoadsB];
 #pragma unroll
   for (int q = 0; q < kLoadsA; ++q)
-    va[q] = 8 * (wave * kLoadsA + q) + r8 < rows_a ? (uint32_t)r8 * lda2 : kOob;
+    va[q] = 8 * (wave * kLoadsA + q) + r8 < rows_a ? (uint32_t)r8 * lda2 + 16u * chunk : kOob + 128u;
 #pragma unroll
   for (int q = 0; q < kLoadsB; ++q) vb[q] = 8 * q + r8 < rows_b ? (uint32_t)r8 * ldb2 + 16u * chunk : kOob;
 
   const int64_t all = (g.k + 63) / 64;
   const int s0 = (int)(all * blockIdx.y / gridDim.y), s1 = (int)(all * (blockIdx.y + 1) / gridDim.y);
-  // Loads q0 .. q1-1 of step s; steps past the last read out of range (no traffic).
-  auto load = [&](int s, int q0, int q1) {
+  // Load q of step s into the buffer of its parity.  Steps past the last load the
+  // last one again (never used), so every step has the same number in flight.
+  auto load = [&](int s, int q) {
     uint8_t* buf = lds + (s & 1) * kBuf;
-    const bool live = s < s1;
-    // Chunks past k (only in the last step) read the row's first chunk of the
-    // step instead: finite values that meet b's zeros.
-    const uint32_t ca = 64 * (int64_t)s + 8 * chunk < g.k ? 16u * chunk : 0u;
-#pragma unroll
-    for (int q = q0; q < q1; ++q) {
-      if (q < kLoadsA) {
-        const uint32_t row = (uint32_t)(wave * kLoadsA + q) * 8u;
-        load_lds16(ra, buf + row * 128u, live ? va[q] + ca : kOob, row * lda2 + 128u * (uint32_t)s);
-      } else {
-        const int p = q - kLoadsA;
-        const uint32_t row = (uint32_t)(wave * kLoadsB + p) * 8u;
-        load_lds16(rb, buf + kABytes + row * 128u, live ? vb[p] : kOob, (uint32_t)(8 * p) * ldb2 + 128u * (uint32_t)s);
-      }
+    const int at = s < s1 ? s : s1 - 1;
+    if (q < kLoadsA) {
+      // Chunks past k (only in the last step) read the row's first chunk of the
+      // step instead: finite values that meet b's zeros.
+      const uint32_t back = 64 * (int64_t)at + 8 * chunk < g.k ? 0u : 16u * chunk;
+      const uint32_t row = (uint32_t)(wave * kLoadsA + q) * 8u;
+      load_lds16(ra, buf + row * 128u, va[q] - back, row * lda2 + 128u * (uint32_t)at);
+    } else {
+      const int p = q - kLoadsA;
+      const uint32_t row = (uint32_t)(wave * kLoadsB + p) * 8u;
+      load_lds16(rb, buf + kABytes + row * 128u, vb[p], (uint32_t)(8 * p) * ldb2 + 128u * (uint32_t)at);
     }
   };
 
@@ -314,8 +317,10 @@ void gemm_kernel(GemmArgs g) {
   constexpr std::integral_constant<int, kLoads1 | 0x0F70> landed{};   // vmcnt(kLoads1)
   static_assert(kLoads1 < 16, "vmcnt's low field");
   Frags f0, f1;
-  load(s0, 0, kLoads);
-  load(s0 + 1, 0, kLoads);
+  if (s0 < s1) {
+#pragma unroll
+    for (int q = 0; q < 2 * kLoads; ++q) load(s0 + q / kLoads, q % kLoads);
+  }
   meet(std::integral_constant<int, (kLoads & 15) | (kLoads >> 4) << 14 | 0x0F70>{});
 #pragma unroll
   for (int n = 0; n < TN; ++n) f0.w[n] = read_w(s0, 0, n);
@@ -326,28 +331,37 @@ void gemm_kernel(GemmArgs g) {
     // rows, then the first loads of step s+2 into the buffer that is free by then.
 #pragma unroll
     for (int n = 0; n < TN; ++n) {
-      if (n < kEarly) {
+      mfma_row<TM>(f0.w[n], f0.x, acc[n], [&](int pair) {
+        constexpr int kReads = (TM + TN) / kEarly / (TM / 2);   // beside each pair
+        if (n < kEarly) {
 #pragma unroll
-        for (int i = 4 * n; i < 4 * n + 4; ++i) f1.w[i] = read_w(s, 1, i);
-#pragma unroll
-        for (int m = n * TM / kEarly; m < (n + 1) * TM / kEarly; ++m) f1.x[m] = read_x(s, 1, m);
-      } else {
-        load(s + 2, n - kEarly, n - kEarly + 1);
-      }
-      mfma_row<TM>(f0.w[n], f0.x, acc[n]);
-      __builtin_amdgcn_sched_barrier(0);
+          for (int i = 0; i < kReads; ++i) {
+            const int f = (n * (TM / 2) + pair) * kReads + i;
+            if (f < TN) f1.w[f] = read_w(s, 1, f);
+            else f1.x[f - TN] = read_x(s, 1, f - TN);
+          }
+        } else if (pair == 1) {
+          load(s + 2, n - kEarly);
+        }
+      });
       if (n == kEarly - 1) meet(read_done);
     }
     meet(landed);   // step s+1: all but the loads just asked for
     // Second half; the next step's first fragments and the rest of the loads.
 #pragma unroll
     for (int n = 0; n < TN; ++n) {
-      f0.w[n] = read_w(s + 1, 0, n);
+      mfma_row<TM>(f1.w[n], f1.x, acc[n], [&](int pair) {
+        constexpr int kRest = kLoads - kLoads1;
+        const int q = kLoads1 + n * kRest / TN, q1 = kLoads1 + (n + 1) * kRest / TN;
+        if (pair == 0) {
+          f0.w[n] = read_w(s + 1, 0, n);
 #pragma unroll
-      for (int m = n * TM / TN; m < (n + 1) * TM / TN; ++m) f0.x[m] = read_x(s + 1, 0, m);
-      load(s + 2, kLoads1 + n * (kLoads - kLoads1) / TN, kLoads1 + (n + 1) * (kLoads - kLoads1) / TN);
-      mfma_row<TM>(f1.w[n], f1.x, acc[n]);
-      __builtin_amdgcn_sched_barrier(0);
+          for (int m = n * TM / TN; m < (n + 1) * TM / TN; ++m) f0.x[m] = read_x(s + 1, 0, m);
+        } else if (pair == 1 && q < q1) {
+          load(s + 2, q);
+        }
+        if (pair == TM / 2 - 1 && q + 1 < q1) load(s + 2, q + 1);
+      });
     }
   }
   __builtin_amdgcn_s_waitcnt(0);   // no load into LDS outlives the block
