@@ -1597,16 +1597,20 @@ hipError_t launch_gemm_small_m(const PlaneView& w, const uint16_t* x, int64_t m,
 namespace {
 
 // The gated product of NT column tiles.  Activations that fit are staged whole,
-// K split over the waves of a block until about 2048 waves share the launch;
-// on whole steps two or more column tiles take the wide kernel with one gate
-// and one up tile per wave; the rest streams through 4-wave blocks.
+// K split over the waves of a block until about 1024 waves share the launch
+// (28672 x 4096 at 1 token: 13.4 us with 896 waves and no split, 15.6 with
+// 1792, 22 with 3584); on whole steps two or more column tiles take the wide
+// kernel with one gate and one up tile per wave; the rest streams through 4-wave
+// blocks.  Staging more than 64 KB leaves one block on a CU, which only pays
+// where there are too few pairs of tiles for two (16 tokens, K = 4096: 896
+// pairs 22.0 us staged and 14.0 streamed, 256 pairs 10.4 and 13.5).
 template <int NT>
 hipError_t launch_glu_nt(KArgs a, hipStream_t s) {
   const size_t fk = full_k_bytes(a.m, a.G);
   const int steps = (((a.G + 3) & ~3) + 15) / 16;
-  if (fk <= (size_t)kFullKBudget) {
+  if (fk <= 64 * 1024 || (fk <= (size_t)kFullKBudget && a.half_tiles < 512)) {
     int sk = 1;
-    while (sk < 8 && sk * 2 <= steps && (int64_t)a.half_tiles * sk < 2048) sk *= 2;
+    while (sk < 8 && sk * 2 <= steps && (int64_t)a.half_tiles * sk < 1024) sk *= 2;
     a.sk = sk;
     const int w = sk > 4 ? 8 : 4;
     size_t shm = fk;
