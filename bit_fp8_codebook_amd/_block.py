@@ -297,16 +297,18 @@ def q3_residual_norm_backward(r_out: torch.Tensor, pre_weight: torch.Tensor = No
         _rows(dx, (m, n), torch.float32, dev, "dx")
     if dr_out is not None:
         _rows(dr_out, (m, n), r_out.dtype, dev, "dr_out")
-    # bf16 rows that are pitched so that q3_gemm_backward takes them as they are
+    # The gradients summed over the tokens share one allocation; bf16 rows are
+    # pitched so that q3_gemm_backward takes them as they are.
     wide = (n + 7) // 8 * 8
-    g = ResidualNormGrads(dr=torch.empty((m, n), dtype=r_out.dtype, device=dev),
-                          dpre_weight=torch.empty(n, dtype=torch.float32, device=dev))
+    sums = torch.empty((3, (n + 3) // 4 * 4), dtype=torch.float32, device=dev)
+    g = ResidualNormGrads(dr=r_out.new_empty((m, n)), dpre_weight=sums[0, :n])
     if y is not None:
-        g.dy = torch.empty((m, wide), dtype=torch.bfloat16, device=dev)[:, :n]
+        dy = torch.empty((m, wide), dtype=torch.bfloat16, device=dev)
+        g.dy = dy if wide == n else dy[:, :n]
     if gate is not None:
-        g.dgate = torch.empty(gate.shape, dtype=torch.float32, device=dev)
+        g.dgate = y.new_empty((m, n)) if gate.dim() == 2 else sums[2, :n]
     if post_weight is not None:
-        g.dpost_weight = torch.empty(n, dtype=torch.float32, device=dev)
+        g.dpost_weight = sums[1, :n]
     ws = _ws(workspace, lib().q3_residual_norm_backward_workspace_bytes(m, n), dev)
     grads = Q3ResidualNormGrads(_ptr(dx), _pitch(dx), _ptr(dr_out), _pitch(dr_out), g.dr.data_ptr(), n, _ptr(g.dy),
                                 wide, _ptr(g.dgate), n, _ptr(g.dpost_weight), g.dpre_weight.data_ptr())

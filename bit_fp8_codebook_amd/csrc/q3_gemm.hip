@@ -508,6 +508,16 @@ int64_t padded_k(int64_t k) { return (k + 127) / 128 * 128; }
 int64_t padded_n(int64_t n) { return (n + 63) / 64 * 64; }
 constexpr int64_t kSmallM = 64;
 
+// Whether m tokens go through the packed planes 64 at a time: widening costs as
+// much as about three such passes over a tall matrix, and on a short one a pass
+// does not fill the chip.  Measured, passes against widening: 28672 x 4096 at 256
+// tokens 99 and 135 us, at 512 192 and 152; 14336 x 4096 at 192 tokens 55 and 61,
+// at 256 74 and 65; 4096 x 4096 at 128 tokens 31 and 26.
+bool in_passes(int64_t n, int64_t m) {
+  const int64_t passes = (m + kSmallM - 1) / kSmallM, most = n / 4608;
+  return passes <= (most < 8 ? most : 8) || passes == 1;
+}
+
 hipError_t launch_widen(const PlaneView& w, uint16_t* out, hipStream_t s) {
   const uint32_t gp = (uint32_t)((w.groups + 3) & ~3);
   const int steps = (int)((gp + 15) / 16);
@@ -550,7 +560,11 @@ __global__ __launch_bounds__(256) void glu_back_kernel(const float* __restrict__
 }  // namespace
 
 int64_t gemm_workspace_bytes(int64_t n, int64_t k, int64_t m) {
-  if (m <= kSmallM) return gemm_small_m_workspace_bytes(n, k, m);
+  if (in_passes(n, m)) {
+    const int64_t full = m >= kSmallM ? gemm_small_m_workspace_bytes(n, k, kSmallM) : 0;
+    const int64_t last = m % kSmallM ? gemm_small_m_workspace_bytes(n, k, m % kSmallM) : 0;
+    return full > last ? full : last;
+  }
   return align256(n * padded_k(k) * 2) + align256(split_bytes(m, n, k));
 }
 
@@ -558,8 +572,15 @@ hipError_t launch_gemm(const PlaneView& w, const uint16_t* x, int64_t m, int64_t
                        hipStream_t s) {
   const int64_t k = (int64_t)w.groups * 32;
   if (w.n == 0) return hipSuccess;
-  if (m <= kSmallM)
-    return launch_gemm_small_m(w, x, m, ldx, y, ldy, ws, ws ? gemm_workspace_bytes(w.n, k, m) : 0, s);
+  if (in_passes(w.n, m)) {
+    const int64_t bytes = ws ? gemm_workspace_bytes(w.n, k, m) : 0;
+    for (int64_t i = 0; i < m; i += kSmallM) {
+      const int64_t c = m - i < kSmallM ? m - i : kSmallM;
+      const hipError_t e = launch_gemm_small_m(w, x + i * ldx, c, ldx, y + i * ldy, ldy, ws, bytes, s);
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+  }
   uint16_t* wide = static_cast<uint16_t*>(ws);
   const hipError_t e = launch_widen(w, wide, s);
   if (e != hipSuccess) return e;
@@ -621,13 +642,21 @@ hipError_t launch_gemm_backward(const PlaneView& w, const uint16_t* dy, int64_t 
 }
 
 int64_t glu_workspace_bytes(int64_t n_gu, int64_t k, int64_t m) {
-  return m <= kSmallM ? 0 : align256(n_gu * padded_k(k) * 2);
+  return in_passes(n_gu, m) ? 0 : align256(n_gu * padded_k(k) * 2);
 }
 
 hipError_t launch_glu(const PlaneView& gate_up, const uint16_t* x, int64_t m, int64_t ldx, int32_t act, uint16_t* h,
                       int64_t ldh, float* pre, int64_t ld_pre, void* ws, hipStream_t s) {
   if (gate_up.n == 0) return hipSuccess;
-  if (m <= kSmallM) return launch_glu_small_m(gate_up, x, m, ldx, act, h, ldh, pre, ld_pre, s);
+  if (in_passes(gate_up.n, m)) {
+    for (int64_t i = 0; i < m; i += kSmallM) {
+      const int64_t c = m - i < kSmallM ? m - i : kSmallM;
+      const hipError_t e = launch_glu_small_m(gate_up, x + i * ldx, c, ldx, act, h + i * ldh, ldh,
+                                              pre ? pre + i * ld_pre : nullptr, ld_pre, s);
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+  }
   uint16_t* wide = static_cast<uint16_t*>(ws);
   const hipError_t e = launch_widen(gate_up, wide, s);
   if (e != hipSuccess) return e;

@@ -185,7 +185,7 @@ __global__ __launch_bounds__(block_threads<T>()) void residual_norm_kernel(NormA
 }
 
 // A group's sums over its rows.  Each thread adds to its own columns only, so
-// nothing is shared and no barrier is needed.  Up to 8192 columns they live in
+// nothing is shared and no barrier is needed.  Up to 12288 columns they live in
 // LDS; above, where three rows would not fit, in the group's partial rows.
 template <int T, int V, int EL>
 __device__ __forceinline__ void add_own(float* acc, int n, int t, const float (&v)[EL]) {
@@ -222,6 +222,7 @@ void residual_norm_back_kernel(NormBackArgs a) {
   const int n = a.n;
   const float inv_n = 1.0f / (float)n;
   constexpr bool kLds = EL < 16;
+  constexpr bool kKeep = T * EL <= 8192;   // weights in registers; above, read again for each row
   float* part[3] = {a.part_pre, a.part_post, a.part_gate};
   float* acc[3];
 #pragma unroll
@@ -238,8 +239,10 @@ void residual_norm_back_kernel(NormBackArgs a) {
   }
 
   float pre_w[EL], post_w[EL];
-  weights<T, V, EL>(a.pre_w, n, t, pre_w);
-  weights<T, V, EL>(a.post_w, n, t, post_w);
+  if constexpr (kKeep) {
+    weights<T, V, EL>(a.pre_w, n, t, pre_w);
+    weights<T, V, EL>(a.post_w, n, t, post_w);
+  }
   const bool gates = a.gate != nullptr;
   struct Row {
     Loaded<V, EL, E> r, dr;
@@ -260,6 +263,7 @@ void residual_norm_back_kernel(NormBackArgs a) {
     const auto& da = cur.da;
     const auto& y = cur.y;
     const auto& g = cur.g;
+    if constexpr (!kKeep) weights<T, V, EL>(a.pre_w, n, t, pre_w);
     float q[3] = {0.f, 0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < EL; ++e) {
@@ -280,6 +284,7 @@ void residual_norm_back_kernel(NormBackArgs a) {
     store_row<T, V, EL>(row_of(static_cast<E*>(a.dr), row, a.ld_dr, n), t, grad, E{});
     if (a.y) {
       float dg[EL];
+      if constexpr (!kKeep) weights<T, V, EL>(a.post_w, n, t, post_w);
       if (a.post_w) {
         const float sy = rsqrtf(q[2] * inv_n + a.eps);
         float p[1] = {0.f};
@@ -354,7 +359,8 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* p0, cons
 }
 
 // Threads of a row's group: 8 elements each up to 8192 columns (the backward
-// pass 12 between 4096 and 6144, so that two groups fit a CU), then 1024 x 16.
+// pass 12 between 4096 and 6144, so that two groups fit a CU), then 1024 x 16
+// (the backward pass 1024 x 12 up to 12288).
 int threads_for(int n, bool back) {
   int t = 64;
   while (t < 1024 && t * 8 < n) t *= 2;
@@ -365,6 +371,9 @@ template <bool kBack, typename F>
 hipError_t pick(int32_t r_type, bool vec, int n, F&& f) {
   auto by_t = [&](auto e, auto v) -> hipError_t {
     constexpr std::integral_constant<int, 8> e8{};
+    if constexpr (kBack)
+      if (n > 8192 && n <= 12288)
+        return f(e, v, std::integral_constant<int, 1024>{}, std::integral_constant<int, 12>{});
     if (n > 8192) return f(e, v, std::integral_constant<int, 1024>{}, std::integral_constant<int, 16>{});
     switch (threads_for(n, kBack)) {
       case 64: return f(e, v, std::integral_constant<int, 64>{}, e8);

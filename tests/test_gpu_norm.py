@@ -108,7 +108,7 @@ def check_backward(q3, v, dx, dr, scale=0.7, eps=1e-6, **kw):
 
 # every thread-group size (n up to 512, 1024, ..., 16384), columns that do and do not move in vectors
 SIZES = [(1, 1), (3, 2), (5, 64), (7, 99), (9, 512), (4, 513), (3, 1024), (6, 2048), (2, 4095), (3, 4096), (2, 5120),
-         (2, 8192), (3, 8191), (2, 8196), (1, 16384), (2, 16383)]
+         (2, 8192), (3, 8191), (2, 8196), (300, 8200), (3, 12288), (2, 12287), (2, 12292), (1, 16384), (2, 16383)]
 
 
 @pytest.mark.parametrize("m,n", SIZES)
