@@ -262,7 +262,7 @@ void gemm_kernel(GemmArgs g) {
   uint32_t va[kLoadsA], vb[kLoadsB];
 #pragma unroll
   for (int q = 0; q < kLoadsA; ++q)
-    va[q] = 8 * (wave * kLoadsA + q) + r8 < rows_a ? (uint32_t)r8 * lda2 + 16u * chunk : kOob + 128u;
+    va[q] = 8 * (wave * kLoadsA + q) + r8 < rows_a ? (uint32_t)r8 * lda2 + 16u * chunk : kOob;
 #pragma unroll
   for (int q = 0; q < kLoadsB; ++q) vb[q] = 8 * q + r8 < rows_b ? (uint32_t)r8 * ldb2 + 16u * chunk : kOob;
 
@@ -274,11 +274,11 @@ void gemm_kernel(GemmArgs g) {
     uint8_t* buf = lds + (s & 1) * kBuf;
     const int at = s < s1 ? s : s1 - 1;
     if (q < kLoadsA) {
-      // Chunks past k (only in the last step) read the row's first chunk of the
-      // step instead: finite values that meet b's zeros.
-      const uint32_t back = 64 * (int64_t)at + 8 * chunk < g.k ? 0u : 16u * chunk;
+      // Chunks past k (only in the last step) arrive as zeros, as all loads out
+      // of range do: b's zeros there would make NaN of anything infinite.
+      const uint32_t v = 64 * (int64_t)at + 8 * chunk < g.k ? va[q] : kOob;
       const uint32_t row = (uint32_t)(wave * kLoadsA + q) * 8u;
-      load_lds16(ra, buf + row * 128u, va[q] - back, row * lda2 + 128u * (uint32_t)at);
+      load_lds16(ra, buf + row * 128u, v, row * lda2 + 128u * (uint32_t)at);
     } else {
       const int p = q - kLoadsA;
       const uint32_t row = (uint32_t)(wave * kLoadsB + p) * 8u;

@@ -114,6 +114,48 @@ def test_gemm_pitched_rows(q3):
         assert (y[:, n:] == 5).all() and (dx[:, k:] == 6).all()
 
 
+def one_infinity(rows, cols, at, seed):
+    """Row i holds an infinity at column at[i % len(at)] and numbers elsewhere."""
+    t = tokens(rows, cols, seed)
+    for i in range(rows):
+        t[i, at[i % len(at)]] = float("inf") if i % 3 else -float("inf")
+    return t
+
+
+@pytest.mark.parametrize("m", [3, 70, 300])
+@pytest.mark.parametrize("n,k", [(45, 96), (100, 544), (200, 32)])
+def test_gemm_infinities(q3, n, k, m):
+    # an infinity leaves its sign (0 times it: NaN) and nothing else; columns behind a tile's end add nothing
+    layer = synth.make_layer(n, k, seed=n)
+    w, w64 = pack_layer(q3, layer), weights(layer)
+    for cols, f, mat in ((k, q3.q3_gemm, w64), (n, q3.q3_gemm_backward, w64.T)):
+        last = (cols - 1) // 64 * 64
+        at = [last, min(last + 7, cols - 1), cols - 1, 0, cols // 2]
+        x = one_infinity(m, cols, at, 5)
+        got = h64(f(w, x))
+        for i in range(m):
+            a = at[i % len(at)]
+            with np.errstate(invalid="ignore"):
+                want = h64(x)[i, a] * mat[:, a]
+            np.testing.assert_array_equal(got[i], want)
+
+
+def test_gemm_after_not_a_number(q3):
+    # what an earlier call left in the chip's memories does not reach columns that a tile pads
+    big = synth.make_layer(256, 512, seed=1)
+    wb = pack_layer(q3, big)
+    for m in (3, 70, 600):
+        for n, k in ((45, 32), (100, 96), (300, 160)):
+            layer = synth.make_layer(n, k, seed=2)
+            w, w64 = pack_layer(q3, layer), weights(layer)
+            x, dy = tokens(m, k, 1), tokens(m, n, 2)
+            nan = torch.full((600, 512), float("nan"), dtype=torch.bfloat16, device="cuda")
+            q3.q3_gemm(wb, nan)
+            check_product(q3.q3_gemm(w, x), h64(x), w64)
+            q3.q3_gemm(wb, nan)
+            check_product(q3.q3_gemm_backward(w, dy), h64(dy), w64.T)
+
+
 def test_gemm_empty_matrix(q3):
     w = q3.empty_packed(0, 64, "cuda")
     assert q3.q3_gemm(w, tokens(70, 64, 1)).shape == (70, 0)
