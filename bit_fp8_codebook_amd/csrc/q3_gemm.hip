@@ -177,16 +177,28 @@ __device__ __forceinline__ void load_lds16(rsrc_t r, uint8_t* dst, uint32_t voff
 // and left to the register allocator the sums move between the two files all
 // through the loop.  What the compiler then does not know it need not: the
 // leading s_nop covers a vector instruction that wrote an operand, a sum is next
-// used 64 products later, and mfma_done() lets the last ones end.
+// used 64 products later, and the last pair of a step (`last`) ends before the
+// statement does (20 wait states, more than any product needs; they pass beside
+// the products), so whatever follows the loop may read or move sums at once.
 template <bool kBig>
-__device__ __forceinline__ void mfma_pair(bf16x8 w, bf16x8 x0, bf16x8 x1, f32x4& acc0, f32x4& acc1) {
+__device__ __forceinline__ void mfma_pair(bf16x8 w, bf16x8 x0, bf16x8 x1, f32x4& acc0, f32x4& acc1, bool last) {
   if constexpr (kBig) {
-    asm volatile(
-        "s_nop 1\n"
-        "v_mfma_f32_16x16x32_bf16 %0, %2, %3, %0\n"
-        "v_mfma_f32_16x16x32_bf16 %1, %2, %4, %1\n"
-        : "+a"(acc0), "+a"(acc1)
-        : "v"(w), "v"(x0), "v"(x1));
+    if (last)
+      asm volatile(
+          "s_nop 1\n"
+          "v_mfma_f32_16x16x32_bf16 %0, %2, %3, %0\n"
+          "v_mfma_f32_16x16x32_bf16 %1, %2, %4, %1\n"
+          "s_nop 15\n"
+          "s_nop 3\n"
+          : "+a"(acc0), "+a"(acc1)
+          : "v"(w), "v"(x0), "v"(x1));
+    else
+      asm volatile(
+          "s_nop 1\n"
+          "v_mfma_f32_16x16x32_bf16 %0, %2, %3, %0\n"
+          "v_mfma_f32_16x16x32_bf16 %1, %2, %4, %1\n"
+          : "+a"(acc0), "+a"(acc1)
+          : "v"(w), "v"(x0), "v"(x1));
   } else {
     acc0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x0, acc0, 0, 0, 0);
     acc1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x1, acc1, 0, 0, 0);
@@ -196,17 +208,14 @@ __device__ __forceinline__ void mfma_pair(bf16x8 w, bf16x8 x0, bf16x8 x1, f32x4&
 // read or a load between every two products, so that the matrix core does not
 // run dry while the wave issues them.
 template <int TM, typename Beside>
-__device__ __forceinline__ void mfma_row(bf16x8 w, const bf16x8 (&x)[TM], f32x4 (&acc)[TM], Beside&& beside) {
+__device__ __forceinline__ void mfma_row(bf16x8 w, const bf16x8 (&x)[TM], f32x4 (&acc)[TM], bool last,
+                                         Beside&& beside) {
 #pragma unroll
   for (int m = 0; m < TM; m += 2) {
     beside(m / 2);
-    mfma_pair<TM == 8>(w, x[m], x[m + 1], acc[m], acc[m + 1]);
+    mfma_pair<TM == 8>(w, x[m], x[m + 1], acc[m], acc[m + 1], last && m + 2 == TM);
     __builtin_amdgcn_sched_barrier(0);
   }
-}
-template <int TM>
-__device__ __forceinline__ void mfma_done() {
-  if constexpr (TM == 8) asm volatile("s_nop 15\ns_nop 15" ::: "memory");
 }
 
 // Block of four waves (2 x 2) on a 32 TM x 32 TN tile (tokens x weight rows), 64
@@ -331,7 +340,7 @@ void gemm_kernel(GemmArgs g) {
     // rows, then the first loads of step s+2 into the buffer that is free by then.
 #pragma unroll
     for (int n = 0; n < TN; ++n) {
-      mfma_row<TM>(f0.w[n], f0.x, acc[n], [&](int pair) {
+      mfma_row<TM>(f0.w[n], f0.x, acc[n], false, [&](int pair) {
         constexpr int kReads = (TM + TN) / kEarly / (TM / 2);   // beside each pair
         if (n < kEarly) {
 #pragma unroll
@@ -350,7 +359,7 @@ void gemm_kernel(GemmArgs g) {
     // Second half; the next step's first fragments and the rest of the loads.
 #pragma unroll
     for (int n = 0; n < TN; ++n) {
-      mfma_row<TM>(f1.w[n], f1.x, acc[n], [&](int pair) {
+      mfma_row<TM>(f1.w[n], f1.x, acc[n], n + 1 == TN, [&](int pair) {
         constexpr int kRest = kLoads - kLoads1;
         const int q = kLoads1 + n * kRest / TN, q1 = kLoads1 + (n + 1) * kRest / TN;
         if (pair == 0) {
@@ -365,7 +374,6 @@ void gemm_kernel(GemmArgs g) {
     }
   }
   __builtin_amdgcn_s_waitcnt(0);   // no load into LDS outlives the block
-  mfma_done<TM>();
 
   // Lane l holds weight rows 4*(l/16)..+3 of each tile for token l%16.
 #pragma unroll
