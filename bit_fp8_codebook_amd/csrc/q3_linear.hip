@@ -153,7 +153,7 @@ struct StepData {
 // at or past s_end re-read step s_end-1 (cached, never computed).  On a partial
 // last step, lanes past its quads (last_ok false) read zeros for both codes
 // and scales; a zero scale byte widens to a zero fp32 scale, so those lanes
-// contribute exactly zero whatever activations they meet.
+// contribute exactly zero to any finite activation (they are given zeros).
 template <int R, int kWd>
 __device__ __forceinline__ void load_step(const Planes& p, const RowTile (&rt)[R], bool last_ok, int s, int s_end,
                                           StepData<R, kWd>& d) {
@@ -556,28 +556,30 @@ void linear_kernel(KArgs a) {
     };
     // Lane addresses of token slots at the step's start in a row-per-token x
     // layout of the given row stride, for buffer base `base` (absent tokens of
-    // matrix-core mode go to `zero`, a 1 KB zero block, and stay there).
-    auto run = [&](const StepData<R, kWd>& d, uint32_t base, uint32_t rstride, uint32_t zero, uint32_t adv) {
+    // matrix-core mode go to `zero`, a 1 KB zero block, and stay there; so do
+    // lanes with no groups in the step (`here` false), whose place may be the
+    // next token's: its infinities and NaN must not meet their zero weights).
+    auto run = [&](const StepData<R, kWd>& d, uint32_t base, uint32_t rstride, uint32_t zero, uint32_t adv,
+                   bool here) {
       if constexpr (kDot) {
         uint32_t xa[NT];
 #pragma unroll
-        for (int m = 0; m < NT; ++m) xa[m] = (m < cnt ? base + m * rstride + adv : zero) + 256u * kb;
+        for (int m = 0; m < NT; ++m) xa[m] = (m < cnt && here ? base + m * rstride + adv : zero) + 256u * kb;
         dot_step<NT, R>(d, rt, xa, lds, dacc);
       } else {
         uint32_t xb[NT];
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
           const int j = 16 * c + i;
-          xb[c] = (j < cnt ? base + j * rstride + adv : zero) + 256u * kb;
+          xb[c] = (j < cnt && here ? base + j * rstride + adv : zero) + 256u * kb;
         }
         mfma_step<NT, R>(d, rt, xb, lds, acc);
       }
     };
 
     if constexpr (kMode == kShared) {
-      // Stage all activations: row j holds token j's K values (zero past K,
-      // including the row's 16-byte pad, which lanes past a partial last
-      // step's quads read with a zero scale); a 1 KB zero block follows.  The
+      // Stage all activations: row j holds token j's K values (zero past K);
+      // a 1 KB zero block follows.  The
       // first batch of activation loads goes out before the weight loads:
       // loads complete in issue order, so activations queued behind a step of
       // weights would hold up every wave of the block at the barrier below.
@@ -615,12 +617,12 @@ void linear_kernel(KArgs a) {
       for (int s = s0; s < s1; s += 2) {
         load_step(p, rt, last_ok, s + 1, s1, B);
         __builtin_amdgcn_sched_barrier(0);
-        run(A, 0u, rstride, zero_base, 1024u * s);
+        run(A, 0u, rstride, zero_base, 1024u * s, s + 1 < p.steps || last_ok);
         __builtin_amdgcn_sched_barrier(0);
         if (s + 1 >= s1) break;
         load_step(p, rt, last_ok, s + 2, s1, A);
         __builtin_amdgcn_sched_barrier(0);
-        run(B, 0u, rstride, zero_base, 1024u * (s + 1));
+        run(B, 0u, rstride, zero_base, 1024u * (s + 1), s + 2 < p.steps || last_ok);
         __builtin_amdgcn_sched_barrier(0);
       }
     } else {
@@ -667,7 +669,7 @@ void linear_kernel(KArgs a) {
         fetch(s + 1, xr);
         load_step(p, rt, last_ok, s + 1, s1, B);
         __builtin_amdgcn_sched_barrier(0);
-        run(A, 0u, rstride, zero_base, 0u);
+        run(A, 0u, rstride, zero_base, 0u, true);
         __builtin_amdgcn_sched_barrier(0);
         put(1, xr);   // buffer 1 was last read at step s-1
         __syncthreads();
@@ -675,7 +677,7 @@ void linear_kernel(KArgs a) {
         fetch(s + 2, xr);
         load_step(p, rt, last_ok, s + 2, s1, A);
         __builtin_amdgcn_sched_barrier(0);
-        run(B, buf_bytes, rstride, zero_base, 0u);
+        run(B, buf_bytes, rstride, zero_base, 0u, true);
         __builtin_amdgcn_sched_barrier(0);
         put(0, xr);
         __syncthreads();
@@ -876,7 +878,7 @@ void wide_kernel(KArgs a) {
   }
   const rsrc_t xr = make_rsrc(a.x, (uint32_t)((a.x_rows - 1) * a.ldx * 2 + (int64_t)a.G * 64));
   const uint32_t ldx_bytes = (uint32_t)(a.ldx * 2);
-  const uint32_t lane16 = 16u * (uint32_t)lane;
+  const uint32_t lane16 = 16u * (uint32_t)lane, row_bytes = (uint32_t)a.G * 64u;
   if (tid < 64) *reinterpret_cast<u32x4*>(lds + zero_base + 16u * tid) = u32x4{0u, 0u, 0u, 0u};
 
   for (int slice = 0; slice < a.m; slice += kSlice) {
@@ -902,7 +904,8 @@ void wide_kernel(KArgs a) {
     auto loads_of = [&](StepData<R>& dst, uint32_t buf, int sn) {
       const bool live = sn < s_end;
       const uint32_t sc = (uint32_t)(live ? sn : s_end - 1);
-      return [&, buf, live, sc](auto q) {
+      const uint32_t xl = live && 1024u * sc + lane16 < row_bytes ? lane16 : kOob;   // zeros past K
+      return [&, buf, live, sc, xl](auto q) {
         constexpr int Q = decltype(q)::value;
         if constexpr (Q < 3 * R) {
           constexpr int r = Q / 3, j = Q % 3;
@@ -916,7 +919,7 @@ void wide_kernel(KArgs a) {
           const int j = wave + kW * (Q - 4 * R);
           __builtin_amdgcn_raw_ptr_buffer_load_lds(
               xr, (__attribute__((address_space(3))) void*)(lds + buf + (uint32_t)j * rstride), 16,
-              live && j < cnt ? lane16 : kOob, (uint32_t)(slice + (j < cnt ? j : 0)) * ldx_bytes + 1024u * sc, 0, 0);
+              j < cnt ? xl : kOob, (uint32_t)(slice + (j < cnt ? j : 0)) * ldx_bytes + 1024u * sc, 0, 0);
         }
       };
     };
@@ -1105,12 +1108,13 @@ void wide_hs_kernel(KArgs a) {
   // lane l takes token 2q + l/32 and the chunk stored at position l%32.  The
   // position-to-chunk map depends on the token's low four bits, which for
   // this wave's loads take two values (j even, j odd).
-  uint32_t xsrc[2];
+  uint32_t xsrc[2], xcol[2];
 #pragma unroll
   for (int par = 0; par < 2; ++par) {
     const uint32_t t = 2u * (uint32_t)(wave + kW * par) + (uint32_t)(lane >> 5);
     const uint32_t c = ((uint32_t)lane & 31u) ^ (t & 15u);
-    xsrc[par] = (uint32_t)(lane >> 5) * ldx_bytes + 256u * (c >> 3) + 16u * (c & 7u);
+    xcol[par] = 256u * (c >> 3) + 16u * (c & 7u);
+    xsrc[par] = (uint32_t)(lane >> 5) * ldx_bytes + xcol[par];
   }
   const uint32_t i7 = (uint32_t)i & 7u;
 
@@ -1135,8 +1139,14 @@ void wide_hs_kernel(KArgs a) {
       const uint32_t sc = (uint32_t)(live ? sn : s_end - 1);
       const uint32_t vc = live ? vcode + 8u * decltype(hc)::value : kOob;
       const uint32_t vs = live ? vscale : kOob;
+      uint32_t xl[2];   // zeros past K
+#pragma unroll
+      for (int par = 0; par < 2; ++par) {
+        const uint32_t h = 128u * decltype(hc)::value;
+        xl[par] = live && 1024u * sc + h + xcol[par] < (uint32_t)a.G * 64u ? xsrc[par] + h : kOob;
+      }
       using Half = decltype(hc);
-      return [&, buf, live, sc, vc, vs](auto q) {
+      return [&, buf, sc, vc, vs, xl](auto q) {
         constexpr uint32_t H = Half::value;
         // The first half-step reads the first 8 bytes of every 16-byte piece
         // and the second the rest, half a step later.  Non-temporal loads in
@@ -1163,7 +1173,7 @@ void wide_hs_kernel(KArgs a) {
           const int t = 2 * qi + (lane >> 5);
           __builtin_amdgcn_raw_ptr_buffer_load_lds(
               xr, (__attribute__((address_space(3))) void*)(lds + buf + (uint32_t)qi * 1024u), 16,
-              live && t < cnt ? xsrc[jq & 1] + 128u * H : kOob,
+              t < cnt ? xl[jq & 1] : kOob,
               (uint32_t)(slice + (2 * qi < cnt ? 2 * qi : 0)) * ldx_bytes + 1024u * sc, 0, 0);
         }
       };

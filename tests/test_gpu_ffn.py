@@ -140,6 +140,33 @@ def test_gemm_infinities(q3, n, k, m):
             np.testing.assert_array_equal(got[i], want)
 
 
+@pytest.mark.parametrize("n,k", [(64, 96), (128, 544), (128, 1120), (20032, 96), (64, 512)])
+def test_one_token_not_a_number(q3, n, k):
+    # the other tokens' results are what they are without it, where K ends inside a step too
+    layer = synth.make_layer(n, k, seed=1)
+    w = pack_layer(q3, layer)
+    for m in (2, 3, 8, 9, 16, 17, 33, 49, 64, 70, 129):
+        x = tokens(m, k, 1, pitch=2)   # what stands behind the rows is NaN as well
+        calls = [lambda a: q3.q3_gemm(w, a), lambda a: q3.q3_glu(w, a)]
+        if m <= 8:
+            calls.append(lambda a: q3.q3_gemv(w, a))
+        for f in calls:
+            clean = f(x)
+            assert torch.isfinite(clean).all()
+            for bad in (0, m // 2, m - 1):
+                for value in (float("nan"), float("inf")):
+                    other = x.clone()
+                    other[bad] = value
+                    wide = torch.full((m, x.stride(0)), value, dtype=torch.bfloat16, device="cuda")
+                    wide[:, :k] = other
+                    for a in (other, wide[:, :k]):
+                        got = f(a)
+                        rows = [i for i in range(m) if i != bad]
+                        assert torch.equal(got[rows], clean[rows])
+                        if value != value:
+                            assert got[bad].isnan().all()
+
+
 def test_gemm_after_not_a_number(q3):
     # what an earlier call left in the chip's memories does not reach columns that a tile pads
     big = synth.make_layer(256, 512, seed=1)
