@@ -26,6 +26,11 @@ class Q3ResidualNormGrads(ctypes.Structure):
                 ("dpost_weight", c_vp), ("dpre_weight", c_vp)]
 
 
+class Q3FfnNorms(ctypes.Structure):
+    _fields_ = [("pre_weight", c_vp), ("post_weight", c_vp), ("next_weight", c_vp), ("gate", c_vp),
+                ("ld_gate", c_i64), ("scale", c_f32), ("eps", c_f32)]
+
+
 _int = ctypes.c_int
 _mat = ctypes.POINTER(Q3Matrix)
 
@@ -43,6 +48,9 @@ SIGNATURES = {
     "q3_residual_norm_backward_workspace_bytes": (c_i64, [c_i64, c_i64]),
     "q3_residual_norm_backward": (_int, [c_vp, c_i64, c_vp, c_vp, c_i64, c_f32, c_vp, c_i64, c_i32, c_vp, c_f32,
                                          c_i64, c_i64, ctypes.POINTER(Q3ResidualNormGrads), c_vp, c_i64, c_vp]),
+    "q3_ffn_workspace_bytes": (c_i64, [c_i64, c_i64, c_i64]),
+    "q3_ffn": (_int, [_mat, _mat, c_i32, ctypes.POINTER(Q3FfnNorms), c_vp, c_i64, c_vp, c_i64, c_i32, c_vp, c_i64,
+                      c_i64, c_vp, c_i64, c_vp]),
     "q3_sample_workspace_bytes": (c_i64, [c_i64, c_i64]),
     "q3_sample": (_int, [c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_vp, c_vp, c_vp]),
 }
@@ -316,6 +324,39 @@ def q3_residual_norm_backward(r_out: torch.Tensor, pre_weight: torch.Tensor = No
           r_out.data_ptr(), _pitch(r_out), _R_TYPES[r_out.dtype], _ptr(pre_weight), eps, m, n, ctypes.byref(grads),
           *_ws_args(ws))
     return g
+
+
+# ------------------------------------------------------------------ feed-forward sublayer
+
+def q3_ffn_workspace_bytes(n_gu: int, k: int, m: int) -> int:
+    return lib().q3_ffn_workspace_bytes(n_gu, k, m)
+
+
+def q3_ffn(gate_up: PackedMatrix, down: PackedMatrix, r: torch.Tensor, pre_weight: torch.Tensor = None,
+           post_weight: torch.Tensor = None, gate: torch.Tensor = None, scale: float = 1.0,
+           next_weight: torch.Tensor = None, act: str = "silu", eps: float = 1e-6, r_out: torch.Tensor = None,
+           x: torch.Tensor = None, workspace: torch.Tensor = None):
+    """r' = r + scale * gate * norm(down . h; post_weight), h the gated block of
+    norm(r; pre_weight), and x = norm(r'; next_weight) -> (r', x), as the separate
+    calls give them.  r_out may be r."""
+    code = _act(act)
+    # y, the down product, is the call's own: r's shape stands for it in the checks
+    m, n, dev, _ = _norm_args(r, pre_weight, None, None, None)
+    _vector(post_weight, n, torch.float32, dev, "post_weight")
+    _vector(next_weight, n, torch.float32, dev, "next_weight")
+    if n != gate_up.k or down.n != n or 2 * down.k != gate_up.n:
+        raise ValueError(f"r [m][{n}], gate_up [{gate_up.n}][{gate_up.k}] and down [{down.n}][{down.k}] do not chain")
+    ld_gate = 0
+    if gate is not None:
+        _rows(gate, (n,) if gate.dim() == 1 else (m, n), torch.float32, dev, "gate")
+        ld_gate = _pitch(gate) if gate.dim() == 2 else 0
+    r_out = r.new_empty((m, n)) if r_out is None else _rows(r_out, (m, n), r.dtype, dev, "r_out")
+    x = r.new_empty((m, n), dtype=torch.bfloat16) if x is None else _rows(x, (m, n), torch.bfloat16, dev, "x")
+    ws = _ws(workspace, lib().q3_ffn_workspace_bytes(gate_up.n, n, m), dev)
+    norms = Q3FfnNorms(_ptr(pre_weight), _ptr(post_weight), _ptr(next_weight), _ptr(gate), ld_gate, scale, eps)
+    _call("q3_ffn", dev, _matrix(gate_up, dev), _matrix(down, dev), code, ctypes.byref(norms), r.data_ptr(), _pitch(r),
+          r_out.data_ptr(), _pitch(r_out), _R_TYPES[r.dtype], x.data_ptr(), _pitch(x), m, *_ws_args(ws))
+    return r_out, x
 
 
 # ------------------------------------------------------------------ sampling

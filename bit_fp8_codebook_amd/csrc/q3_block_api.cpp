@@ -56,8 +56,39 @@ q3_status check_norm(const float* y, int64_t ldy, const float* post_weight, cons
   return Q3_OK;
 }
 
+// The forward pass's own outputs.
+q3_status check_norm_out(const void* r, int64_t ldr, const void* r_out, int64_t ldr_out, int32_t r_type,
+                         const uint16_t* x, int64_t ldx, int64_t n) {
+  if ((r_out && ldr_out < n) || (x && ldx < n) || (r_out == r && ldr_out != ldr)) return Q3_ERR_INVALID_ARG;
+  if (!aligned(r_out, r_type == Q3_BF16 ? 2 : 4) || !aligned(x, 2)) return Q3_ERR_MISALIGNED;
+  return Q3_OK;
+}
+
 // Whether rows at p with this pitch all start on four elements of `size` bytes.
 bool quads(const void* p, int64_t ld, int size) { return !p || (aligned(p, 4 * size) && ld % 4 == 0); }
+
+q3_status run_norm(const q3::NormArgs& a, int32_t r_type, void* stream) {
+  const int e = r_type == Q3_BF16 ? 2 : 4;
+  const bool vec = a.n % 4 == 0 && quads(a.y, a.ldy, 4) && quads(a.post_w, 0, 4) && quads(a.gate, a.ld_gate, 4) &&
+                   quads(a.r, a.ldr, e) && quads(a.r_out, a.ldr_out, e) && quads(a.pre_w, 0, 4) &&
+                   quads(a.x, a.ldx, 2);
+  return from_hip(q3::launch_residual_norm(a, r_type, vec, static_cast<hipStream_t>(stream)));
+}
+
+// q3_ffn's workspace: x [m][k] and h [m][I] in bf16, y [m][k] in fp32 and what
+// the two products need, each from a 256-byte boundary on.
+struct FfnSpace {
+  int64_t h, y, products, bytes;
+};
+FfnSpace ffn_space(int64_t n_gu, int64_t k, int64_t m) {
+  FfnSpace f;
+  f.h = align256(m * k * 2);
+  f.y = f.h + align256(m * (n_gu / 2) * 2);
+  f.products = f.y + align256(m * k * 4);
+  const int64_t up = q3::glu_workspace_bytes(n_gu, k, m), down = q3::gemm_workspace_bytes(k, n_gu / 2, m);
+  f.bytes = f.products + (up > down ? up : down);
+  return f;
+}
 
 }  // namespace
 
@@ -140,9 +171,7 @@ Q3_API q3_status q3_residual_norm(const float* y, int64_t ldy, const float* post
   q3_status st = check_norm(y, ldy, post_weight, gate, ld_gate, r, ldr, r_type, pre_weight, eps, m, n);
   if (st != Q3_OK) return st;
   if ((y && !r_out) || (pre_weight && !x) || (!r_out && !x)) return Q3_ERR_INVALID_ARG;
-  if ((r_out && ldr_out < n) || (x && ldx < n) || (r_out == r && ldr_out != ldr)) return Q3_ERR_INVALID_ARG;
-  const int e = r_type == Q3_BF16 ? 2 : 4;
-  if (!aligned(r_out, e) || !aligned(x, 2)) return Q3_ERR_MISALIGNED;
+  if ((st = check_norm_out(r, ldr, r_out, ldr_out, r_type, x, ldx, n)) != Q3_OK) return st;
   if ((st = check_device()) != Q3_OK) return st;
   q3::NormArgs a{};
   a.y = y;
@@ -161,9 +190,7 @@ Q3_API q3_status q3_residual_norm(const float* y, int64_t ldy, const float* post
   a.ldx = ldx;
   a.m = m;
   a.n = static_cast<int>(n);
-  const bool vec = n % 4 == 0 && quads(y, ldy, 4) && quads(post_weight, 0, 4) && quads(gate, ld_gate, 4) &&
-                   quads(r, ldr, e) && quads(r_out, ldr_out, e) && quads(pre_weight, 0, 4) && quads(x, ldx, 2);
-  return from_hip(q3::launch_residual_norm(a, r_type, vec, static_cast<hipStream_t>(stream)));
+  return run_norm(a, r_type, stream);
 }
 
 Q3_API int64_t q3_residual_norm_backward_workspace_bytes(int64_t m, int64_t n) {
@@ -227,6 +254,67 @@ Q3_API q3_status q3_residual_norm_backward(const float* y, int64_t ldy, const fl
                    (!g.dgate || ld_gate == 0 || quads(g.dgate, g.ld_dgate, 4));
   return from_hip(q3::launch_residual_norm_back(a, r_type, vec, g.dpre_weight, g.dpost_weight, gate_row,
                                                 static_cast<hipStream_t>(stream)));
+}
+
+Q3_API int64_t q3_ffn_workspace_bytes(int64_t n_gu, int64_t k, int64_t m) {
+  if (bad_shape(n_gu, k, m) || n_gu % 64 || k > kMaxNorm) return 0;
+  return ffn_space(n_gu, k, m).bytes;
+}
+
+Q3_API q3_status q3_ffn(const q3_matrix* gate_up, const q3_matrix* down, int32_t act, const q3_ffn_norms* norms,
+                        const void* r, int64_t ldr, void* r_out, int64_t ldr_out, int32_t r_type, uint16_t* x_next,
+                        int64_t ldx_next, int64_t m, void* workspace, int64_t workspace_bytes, void* stream) {
+  q3_status st = check_matrix(gate_up);
+  if (st != Q3_OK) return st;
+  if ((st = check_matrix(down)) != Q3_OK) return st;
+  if (!norms || bad_act(act)) return Q3_ERR_INVALID_ARG;
+  const int64_t k = gate_up->k, inter = gate_up->n / 2;
+  if (bad_shape(gate_up->n, k, m) || gate_up->n % 64 || k > kMaxNorm || down->n != k || down->k != inter)
+    return Q3_ERR_UNSUPPORTED_SHAPE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const FfnSpace at = ffn_space(gate_up->n, k, m);
+  if ((st = check_workspace(workspace, workspace_bytes, at.bytes)) != Q3_OK) return st;
+  uint16_t* x = reinterpret_cast<uint16_t*>(ws);
+  uint16_t* h = reinterpret_cast<uint16_t*>(ws + at.h);
+  float* y = reinterpret_cast<float*>(ws + at.y);
+  void* rest = ws + at.products;
+  if ((st = check_product(gate_up, x, m, k, k)) != Q3_OK) return st;
+  if ((st = check_product(down, h, m, inter, inter)) != Q3_OK) return st;
+  if ((st = check_norm(y, k, norms->post_weight, norms->gate, norms->ld_gate, r, ldr, r_type, norms->pre_weight,
+                       norms->eps, m, k)) != Q3_OK)
+    return st;
+  if (!r_out || (norms->next_weight && !x_next)) return Q3_ERR_INVALID_ARG;
+  if (!aligned(norms->next_weight, 4)) return Q3_ERR_MISALIGNED;
+  if ((st = check_norm_out(r, ldr, r_out, ldr_out, r_type, x_next, ldx_next, k)) != Q3_OK) return st;
+  if ((st = check_device()) != Q3_OK) return st;
+
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  q3::NormArgs a{};
+  a.r = r;
+  a.ldr = ldr;
+  a.pre_w = norms->pre_weight;
+  a.eps = norms->eps;
+  a.m = m;
+  a.n = static_cast<int>(k);
+  q3::NormArgs first = a;
+  first.x = x;
+  first.ldx = k;
+  if ((st = run_norm(first, r_type, stream)) != Q3_OK) return st;
+  hipError_t e = q3::launch_glu(view_of(gate_up), x, m, k, act, h, inter, nullptr, 0, rest, s);
+  if (e == hipSuccess) e = q3::launch_gemm(view_of(down), h, m, inter, y, k, rest, s);
+  if (e != hipSuccess) return from_hip(e);
+  a.y = y;
+  a.ldy = k;
+  a.post_w = norms->post_weight;
+  a.gate = norms->gate;
+  a.ld_gate = norms->ld_gate;
+  a.scale = norms->scale;
+  a.r_out = r_out;
+  a.ldr_out = ldr_out;
+  a.pre_w = norms->next_weight;
+  a.x = x_next;
+  a.ldx = ldx_next;
+  return run_norm(a, r_type, stream);
 }
 
 Q3_API int64_t q3_sample_workspace_bytes(int64_t m, int64_t n) {

@@ -40,7 +40,8 @@ typedef enum q3_act { Q3_ACT_SILU = 0, Q3_ACT_GELU_TANH = 1 } q3_act;
  * for more the matrix dequantised exactly to bf16 in the workspace, multiplied
  * on the matrix cores with fp32 accumulation (or, where that is faster, 64
  * tokens at a time straight from the packed planes).  x bf16 [m][ldx],
- * ldx % 8 == 0, 16-byte aligned; y fp32 [m][ldy]; m < 2^31.
+ * ldx % 8 == 0, 16-byte aligned, 256 of its rows below 2 GiB; y fp32 [m][ldy];
+ * m < 2^31; n and k up to 2^21 here and in what follows.
  * workspace: 256-byte aligned, at least q3_gemm_workspace_bytes(n, k, m) bytes
  * (Q3_ERR_INVALID_ARG otherwise; it may be NULL where that is 0). */
 Q3_API int64_t q3_gemm_workspace_bytes(int64_t n, int64_t k, int64_t m);
@@ -63,8 +64,8 @@ Q3_API q3_status q3_gemm_backward(const q3_matrix* w, const uint16_t* dy, int64_
  * ldh >= I, ldh % 8 == 0, 16-byte aligned (so it is the down product's x).
  * pre (may be NULL): fp32 [m][ld_pre], the pre-activations [g; u] for the
  * backward pass, ld_pre >= 2I, ld_pre % 4 == 0, 16-byte aligned.
- * workspace: 256-byte aligned, q3_glu_workspace_bytes(2I, k, m) bytes (0 for up
- * to 64 tokens). */
+ * workspace: 256-byte aligned, q3_glu_workspace_bytes(2I, k, m) bytes (0
+ * where the packed planes are read directly, as for up to 64 tokens). */
 Q3_API int64_t q3_glu_workspace_bytes(int64_t n_gu, int64_t k, int64_t m);
 Q3_API q3_status q3_glu(const q3_matrix* gate_up, const uint16_t* x, int64_t m, int64_t ldx, int32_t act,
                         uint16_t* h, int64_t ldh, float* pre, int64_t ld_pre, void* workspace,
@@ -132,6 +133,31 @@ Q3_API q3_status q3_residual_norm_backward(const float* y, int64_t ldy, const fl
                                            int32_t r_type, const float* pre_weight, float eps, int64_t m, int64_t n,
                                            const q3_residual_norm_grads* grads, void* workspace,
                                            int64_t workspace_bytes, void* stream);
+
+/* ---- Feed-forward sublayer ----------------------------------------------------- */
+
+/* The operators above as one call, the dense counterpart of q3_moe_mlp:
+ *   y  = down . (act(g) * u),  [g; u] = gate_up . norm(r; pre_weight)
+ *   r' = r + scale * gate * norm(y; post_weight)    (norm, gate: as in q3_residual_norm)
+ *   x_next = norm(r'; next_weight)                  (NULL: not computed)
+ * bitwise what q3_residual_norm, q3_glu, q3_gemm and q3_residual_norm give one
+ * after the other.  gate_up [2I][k] and down [k][I], I % 32 == 0, k <= 16384;
+ * weights, gate, r, r_out and x_next as in q3_residual_norm (n = k; r_out may be
+ * r); any of the three weights may be NULL, next_weight must be where x_next is.
+ * workspace: 256-byte aligned, q3_ffn_workspace_bytes(2I, k, m) bytes. */
+typedef struct q3_ffn_norms {
+  const float* pre_weight;
+  const float* post_weight;
+  const float* next_weight;
+  const float* gate;
+  int64_t ld_gate;
+  float scale;
+  float eps;
+} q3_ffn_norms;
+Q3_API int64_t q3_ffn_workspace_bytes(int64_t n_gu, int64_t k, int64_t m);
+Q3_API q3_status q3_ffn(const q3_matrix* gate_up, const q3_matrix* down, int32_t act, const q3_ffn_norms* norms,
+                        const void* r, int64_t ldr, void* r_out, int64_t ldr_out, int32_t r_type, uint16_t* x_next,
+                        int64_t ldx_next, int64_t m, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* ---- Sampling ----------------------------------------------------------------- */
 

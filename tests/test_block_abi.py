@@ -162,3 +162,30 @@ def test_binding_refusals():
         b.q3_residual_norm(torch.zeros(2, 10))
     with pytest.raises(ValueError):
         b.q3_glu_backward(torch.zeros(2, 64), torch.zeros(2, 32))
+
+
+def test_ffn_refusals(L):
+    from bit_fp8_codebook_amd._block import Q3FfnNorms
+    need = L.q3_ffn_workspace_bytes(128, 64, 100)
+    assert need == 100 * 64 * 2 + 100 * 64 * 2 + 100 * 64 * 4 + L.q3_glu_workspace_bytes(128, 64, 100)
+    assert L.q3_ffn_workspace_bytes(96, 64, 100) == 0 and L.q3_ffn_workspace_bytes(128, 1 << 15, 100) == 0
+    assert L.q3_ffn_workspace_bytes(128, 64, 0) == 0 and L.q3_ffn_workspace_bytes(0, 64, 1) == 0
+
+    def call(gu=_mat(128), dn=_mat(64), act=0, null=False, r=FAKE, ldr=64, ro=FAKE, ldro=64, t=F32, x=FAKE, ldx=64, m=100,
+             ws=FAKE, b=need, **kw):
+        d = dict(pre_weight=FAKE, post_weight=FAKE, next_weight=FAKE, gate=FAKE, ld_gate=64, scale=1.0, eps=1e-6)
+        d.update(kw)
+        norms = Q3FfnNorms(**d)
+        return L.q3_ffn(ctypes.byref(gu) if gu else None, ctypes.byref(dn) if dn else None, act,
+                        None if null else ctypes.byref(norms), r, ldr, ro, ldro, t, x, ldx, m, ws, b, None)
+    assert call(gu=None) == 1 and call(dn=None) == 1 and call(null=True) == 1 and call(act=2) == 1
+    assert call(gu=_mat(96)) == 2 and call(dn=_mat(96)) == 2 and call(dn=_mat(64, 96)) == 2 and call(m=0) == 2
+    assert call(gu=_mat(0)) == 2 and call(gu=_mat(128, 16416), dn=_mat(16416, 64)) == 2
+    assert call(ws=None) == 1 and call(b=need - 1) == 1 and call(ws=FAKE + 128) == 3
+    assert call(r=None) == 1 and call(ro=None) == 1 and call(x=None) == 1 and call(t=2) == 1
+    assert call(ldr=63) == 1 and call(ldro=63) == 1 and call(ldx=63) == 1 and call(ld_gate=63) == 1
+    assert call(ldro=72) == 1                                             # in place with another pitch
+    assert call(eps=-1.0) == 1 and call(eps=float("nan")) == 1
+    assert call(r=FAKE + 2) == 3 and call(ro=FAKE + 2) == 3 and call(x=FAKE + 1) == 3
+    for name in ("pre_weight", "post_weight", "next_weight", "gate"):
+        assert call(**{name: FAKE + 2}) == 3
