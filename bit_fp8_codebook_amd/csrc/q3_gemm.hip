@@ -465,6 +465,12 @@ struct GemmPlan {
   bool big;     // 256 x 256 blocks, else 128 x 128
   int splits;
 };
+// From 192 large blocks on they fill most of the 256 CUs, and each operand byte
+// read serves twice the products; below, four times as many small ones balance
+// better.  Measured, large and small (us): 160 blocks (2048 tokens x 5120 x 4096)
+// 102 and 98; 192 (2048 x 6144 x 4096) 104 and 103, (2048 x 6144 x 8192) 196 and
+// 221; 200 (2560 x 5120 x 5120) 126 and 151; 256 (1024 x 16384 x 4096) 130 and 155;
+// 128 (2048 x 4096 x 11008) 246 and 191.
 GemmPlan plan_gemm(int64_t m, int64_t n, int64_t k, bool may_split) {
   GemmPlan p{((m + 255) / 256) * ((n + 255) / 256) >= 192, 1};
   if (p.big || !may_split) return p;
@@ -517,13 +523,16 @@ int64_t padded_n(int64_t n) { return (n + 63) / 64 * 64; }
 constexpr int64_t kSmallM = 64;
 
 // Whether m tokens go through the packed planes 64 at a time: widening costs as
-// much as about three such passes over a tall matrix, and on a short one a pass
-// does not fill the chip.  Measured, passes against widening: 28672 x 4096 at 256
-// tokens 99 and 135 us, at 512 192 and 152; 14336 x 4096 at 192 tokens 55 and 61,
-// at 256 74 and 65; 4096 x 4096 at 128 tokens 31 and 26.
+// much as a few such passes over a tall matrix, and on a short one a pass does
+// not fill the chip.  Measured at K = 4096, passes against widening (us): 4096
+// rows, 128 tokens 31 and 26; 11008, 128 33 and 46; 14336, 192 55 and 61, 256 74
+// and 65; 18432, 192 91 and 90, 256 121 and 88; 28672, 384 139 and 154, 512 192
+// and 152; 40000, 448 273 and 271, 512 310 and 272; 65536, 512 347 and 335; 151936,
+// 512 681 and 782, 768 1007 and 996.  K = 8192: 28672, 384 241 and 295; 57344, 512
+// 593 and 583.
 bool in_passes(int64_t n, int64_t m) {
-  const int64_t passes = (m + kSmallM - 1) / kSmallM, most = n / 4608;
-  return passes <= (most < 8 ? most : 8) || passes == 1;
+  const int64_t passes = (m + kSmallM - 1) / kSmallM, most = n / 4700;
+  return passes <= (most < 7 ? most : 7) || passes == 1;
 }
 
 hipError_t launch_widen(const PlaneView& w, uint16_t* out, hipStream_t s) {

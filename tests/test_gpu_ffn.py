@@ -85,7 +85,8 @@ def test_gemm_large_tiles(q3, n, k, m):
     check_product(q3.q3_gemm_backward(w, dy)[rows], h64(dy[rows]), w64.T)
 
 
-@pytest.mark.parametrize("n,m", [(9232, 70), (9232, 128), (9232, 129), (18500, 250), (40000, 513)])
+@pytest.mark.parametrize("n,m", [(9232, 70), (9232, 128), (9232, 129), (18500, 250), (40000, 513), (9408, 70),
+                                 (9408, 128), (9408, 129), (18816, 250), (40000, 445)])
 def test_gemm_tall_matrix_in_passes(q3, n, m):
     # tall matrices take 64 tokens at a time from the packed planes, up to a number that grows with n
     k = 96
@@ -95,7 +96,8 @@ def test_gemm_tall_matrix_in_passes(q3, n, m):
     check_product(q3.q3_gemm(w, x), h64(x), w64)
 
 
-@pytest.mark.parametrize("inter,m", [(4640, 70), (4640, 128), (4640, 129), (9248, 250)])
+@pytest.mark.parametrize("inter,m", [(4640, 70), (4640, 128), (4640, 129), (9248, 250), (4704, 70), (4704, 128),
+                                     (4704, 129), (9408, 250)])
 def test_glu_tall_matrix_in_passes(q3, inter, m):
     w, w64 = glu_case(q3, inter, 96, seed=3)
     check_glu(q3, w, w64, tokens(m, 96, 1), "silu")
