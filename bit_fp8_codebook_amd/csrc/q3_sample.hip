@@ -20,12 +20,17 @@
 //            weight of each chunk follows from its running sums and the list,
 //            and u times the total is found in a chunk, a wave's part of it and
 //            an entry
-// A row whose border bins hold more than kCand entries (large ties) is cut by
-// bisection over the logits' 32-bit order instead, in the last launch.
+// Short rows, and rows of which there are many, take the same five steps in one
+// block and launch.  A row whose border bins hold more than kCand entries (large
+// ties) is cut by bisection over the logits' 32-bit order instead, in the last
+// step.
 //
-// What bounds it: the row is read from memory once and twice more from cache;
-// the hist pass evaluates a 64-bit exponential and one or two LDS atomics for
-// every entry.
+// What bounds it: for few rows the chain of some twenty block-wide sums and
+// minima, about 0.5 us each with their two barriers, and the launches (1 x 1000
+// 15 us, 1 x 32000 28 us); for many the hist pass's 64-bit exponential for every
+// entry and its second evaluation where the draw falls (64 x 151936 61 us, of
+// which hist 20, choose 20; 4 copies of the sums against lanes that meet at a
+// bin change nothing).  The row is read from memory once, then from cache.
 #include "q3_device.h"
 #include "q3_internal.h"
 
@@ -147,21 +152,80 @@ __device__ __forceinline__ int bin_of(float l, const Binning& b) {
   return t < (float)(kBins - 1) ? (int)t : kBins - 1;   // NaN goes to the last
 }
 
-// ---- block-wide helpers (kThreads threads) ----------------------------------
+// ---- wave-wide helpers --------------------------------------------------------
+//
+// Lane exchanges as operand modifiers (DPP): a step through LDS permutes takes
+// some 65 cycles and the choose launch has over a hundred of them in a row.
 
-__device__ __forceinline__ uint64_t wave_up64(uint64_t v, int off) {
-  return (uint64_t)__shfl_up((unsigned long long)v, off, 64);
+enum Dpp : int { kQuad1032 = 0xB1, kQuad2301 = 0x4E, kQuad3210 = 0x1B, kShr1 = 0x111, kShr2 = 0x112, kShr4 = 0x114,
+                 kShr8 = 0x118, kRor8 = 0x128, kHalfMirror = 0x141, kBcast15 = 0x142, kBcast31 = 0x143 };
+// The value of the lane that `kCtrl` names; lanes without one, and rows outside
+// kRows, get `none`.
+template <int kCtrl, int kRows = 0xF>
+__device__ __forceinline__ uint32_t dpp(uint32_t v, uint32_t none) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, kCtrl, kRows, 0xF, false);
 }
+template <int kCtrl, int kRows = 0xF>
+__device__ __forceinline__ uint64_t dpp(uint64_t v, uint64_t none) {
+  return (uint64_t)dpp<kCtrl, kRows>((uint32_t)(v >> 32), (uint32_t)(none >> 32)) << 32 |
+         dpp<kCtrl, kRows>((uint32_t)v, (uint32_t)none);
+}
+// Folds the wave's values up to and with each lane: inside rows of 16, then over
+// the rows (the last lane of a row, then of the lower half, to what follows).
+// `none` is op's neutral value.
+template <typename T, typename Op>
+__device__ __forceinline__ T wave_fold(T v, T none, Op&& op) {
+  v = op(v, dpp<kShr1>(v, none));
+  v = op(v, dpp<kShr2>(v, none));
+  v = op(v, dpp<kShr4>(v, none));
+  v = op(v, dpp<kShr8>(v, none));
+  v = op(v, dpp<kBcast15, 0xA>(v, none));
+  v = op(v, dpp<kBcast31, 0xC>(v, none));
+  return v;
+}
+__device__ __forceinline__ uint64_t wave_scan(uint64_t v) {
+  return wave_fold(v, (uint64_t)0, [](uint64_t x, uint64_t y) { return x + y; });
+}
+__device__ __forceinline__ uint32_t last_lane(uint32_t v) { return (uint32_t)__builtin_amdgcn_readlane((int)v, 63); }
+__device__ __forceinline__ uint64_t last_lane(uint64_t v) {
+  return (uint64_t)last_lane((uint32_t)(v >> 32)) << 32 | last_lane((uint32_t)v);
+}
+__device__ __forceinline__ uint64_t wave_sum(uint64_t v) { return last_lane(wave_scan(v)); }
+__device__ __forceinline__ int wave_min(int v) {
+  return (int)last_lane(wave_fold((uint32_t)v, 0x7FFFFFFFu, [](uint32_t x, uint32_t y) {
+    return (int)y < (int)x ? y : x;
+  }));
+}
+__device__ __forceinline__ float wave_max(float v) {
+  return __builtin_bit_cast(float, last_lane(wave_fold(__builtin_bit_cast(uint32_t, v), 0xFF800000u,
+                                                       [](uint32_t x, uint32_t y) {
+    return __builtin_bit_cast(uint32_t, fmaxf(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y)));
+  })));
+}
+// The value of lane l ^ kBit.
+template <int kBit>
+__device__ __forceinline__ uint32_t lane_xor(uint32_t v) {
+  if constexpr (kBit == 1) return dpp<kQuad1032>(v, v);
+  if constexpr (kBit == 2) return dpp<kQuad2301>(v, v);
+  if constexpr (kBit == 4) {
+    const uint32_t m = dpp<kHalfMirror>(v, v);   // l ^ 7, then ^ 3
+    return dpp<kQuad3210>(m, m);
+  }
+  if constexpr (kBit == 8) return dpp<kRor8>(v, v);
+  if constexpr (kBit >= 16) return (uint32_t)__shfl_xor((int)v, kBit, 64);
+}
+template <int kBit>
+__device__ __forceinline__ uint64_t lane_xor(uint64_t v) {
+  return (uint64_t)lane_xor<kBit>((uint32_t)(v >> 32)) << 32 | lane_xor<kBit>((uint32_t)v);
+}
+
+// ---- block-wide helpers (kThreads threads) ----------------------------------
 
 // Inclusive prefix sum over the block; `part` holds kWaves values.  Leading
 // barrier included, so `part` may be reused at once.
 __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* part) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int off = 1; off < 64; off *= 2) {
-    const uint64_t o = wave_up64(v, off);
-    if (lane >= off) v += o;
-  }
+  v = wave_scan(v);
   __syncthreads();
   if (lane == 63) part[wave] = v;
   __syncthreads();
@@ -171,8 +235,7 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* part) {
   return v + before;
 }
 __device__ __forceinline__ uint64_t block_sum(uint64_t v, uint64_t* part) {
-#pragma unroll
-  for (int off = 32; off > 0; off /= 2) v += (uint64_t)__shfl_xor((unsigned long long)v, off, 64);
+  v = wave_sum(v);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
   __syncthreads();
@@ -183,11 +246,7 @@ __device__ __forceinline__ uint64_t block_sum(uint64_t v, uint64_t* part) {
 }
 // The smallest value over the block.
 __device__ __forceinline__ int block_min(int v, int* part) {
-#pragma unroll
-  for (int off = 32; off > 0; off /= 2) {
-    const int o = __shfl_xor(v, off, 64);
-    v = o < v ? o : v;
-  }
+  v = wave_min(v);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
   __syncthreads();
@@ -203,11 +262,8 @@ __device__ __forceinline__ float2 row_stats(const float2* st, int chunks) {
     r.x = fmaxf(r.x, v.x);
     r.y = fminf(r.y, v.y);
   }
-#pragma unroll
-  for (int off = 32; off > 0; off /= 2) {
-    r.x = fmaxf(r.x, __shfl_xor(r.x, off, 64));
-    r.y = fminf(r.y, __shfl_xor(r.y, off, 64));
-  }
+  r.x = wave_max(r.x);
+  r.y = -wave_max(-r.y);
   return r;
 }
 
@@ -254,28 +310,43 @@ struct Entries {
   }
 };
 
-__global__ __launch_bounds__(kThreads) void sample_stats_kernel(SampleArgs a, Ws ws, int per) {
-  __shared__ float2 part[kWaves];
-  const int row = blockIdx.y, c = blockIdx.x;
+// Largest and smallest live logit of the block's range (infinities when there is none).
+__device__ __forceinline__ float2 range_stats(const float* l, Range r, float2* part) {
   float mx = -INFINITY, mn = INFINITY;
-  Entries<8> in(a.logits + (int64_t)row * a.ld, chunk_range(c, per, a.n));
+  Entries<8> in(l, r);
   in.each([&](float v, int) {
     mx = fmaxf(mx, v);   // NaN leaves the other operand
     mn = v > -INFINITY ? fminf(mn, v) : mn;
   });
-#pragma unroll
-  for (int off = 32; off > 0; off /= 2) {
-    mx = fmaxf(mx, __shfl_xor(mx, off, 64));
-    mn = fminf(mn, __shfl_xor(mn, off, 64));
-  }
+  mx = wave_max(mx);
+  mn = -wave_max(-mn);
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = make_float2(mx, mn);
   __syncthreads();
+  for (int w = 0; w < kWaves; ++w) {
+    mx = fmaxf(mx, part[w].x);
+    mn = fminf(mn, part[w].y);
+  }
+  return make_float2(mx, mn);
+}
+
+// Entry counts (only top-k asks for them) and weights of a range over the bins,
+// which the caller has cleared.
+__device__ __forceinline__ void range_hist(Entries<4>& in, const Settings& s, const Binning& b, bool counts,
+                                           uint32_t* cnt, unsigned long long* mass) {
+  in.each([&](float v, int) {
+    const int k = bin_of(v, b);
+    const uint64_t q = weight(v, b.mx, s.inv_t2);   // 0 for masked entries
+    if (counts && live(v, b.mx)) atomicAdd(&cnt[k], 1u);
+    if (q) atomicAdd(&mass[k], (unsigned long long)q);
+  });
+}
+
+__global__ __launch_bounds__(kThreads) void sample_stats_kernel(SampleArgs a, Ws ws, int per) {
+  __shared__ float2 part[kWaves];
+  const int row = blockIdx.y, c = blockIdx.x;
+  const float2 st = range_stats(a.logits + (int64_t)row * a.ld, chunk_range(c, per, a.n), part);
   if (threadIdx.x == 0) {
-    for (int w = 1; w < kWaves; ++w) {
-      mx = fmaxf(mx, part[w].x);
-      mn = fminf(mn, part[w].y);
-    }
-    ws.stats[(int64_t)row * gridDim.x + c] = make_float2(mx, mn);
+    ws.stats[(int64_t)row * gridDim.x + c] = st;
     if (c == 0) ws.listed[row] = 0;
   }
 }
@@ -289,45 +360,22 @@ __global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a, Ws 
   const float2 st = row_stats(ws.stats + (int64_t)row * chunks, chunks);
   const Settings s = settings(a, row);
   const Binning b = binning(st.x, st.y, s.t);
-  const bool counts = s.k < a.n;   // only top-k asks how many entries a bin holds
+  const bool counts = s.k < a.n;
   cnt[threadIdx.x] = 0;
   mass[threadIdx.x] = 0;
   __syncthreads();
-  in.each([&](float v, int) {
-    const int k = bin_of(v, b);
-    const uint64_t q = weight(v, st.x, s.inv_t2);   // 0 for masked entries
-    if (counts && live(v, st.x)) atomicAdd(&cnt[k], 1u);
-    if (q) atomicAdd(&mass[k], (unsigned long long)q);
-  });
+  range_hist(in, s, b, counts, cnt, mass);
   __syncthreads();
   const int64_t at = ((int64_t)row * chunks + c) * kBins + threadIdx.x;
   ws.hist_mass[at] = block_scan(mass[threadIdx.x], part);
   if (counts) ws.hist_cnt[at] = (uint32_t)block_scan(cnt[threadIdx.x], part);
 }
 
-// The bins in which the row's cut can fall, from its chunks' running sums.  A
-// launch of its own: found by every collect block for itself, the sums' reads
-// cost more than the launch (64x151936: 5 + 9 us against 20 in one).
-__global__ __launch_bounds__(kThreads) void sample_border_kernel(SampleArgs a, Ws ws, int chunks) {
-  __shared__ uint64_t mass_in[kBins];   // sums up to and with each bin
-  __shared__ uint32_t cnt_in[kBins];
-  __shared__ int ipart[kWaves];
-  const int row = blockIdx.x, t = threadIdx.x;
-  const Settings s = settings(a, row);
-  const bool counts = s.k < a.n;
-  uint64_t mi = 0;
-  uint32_t ci = 0;
-  const int64_t at = (int64_t)row * chunks * kBins + t;
-#pragma unroll
-  for (int c = 0; c < kMaxChunks; ++c) {   // all loads before the first use
-    mi += c < chunks ? ws.hist_mass[at + (int64_t)c * kBins] : 0;
-    ci += counts && c < chunks ? ws.hist_cnt[at + (int64_t)c * kBins] : 0;
-  }
-  const float2 st = row_stats(ws.stats + (int64_t)row * chunks, chunks);
-  const Binning b = binning(st.x, st.y, s.t);
-  mass_in[t] = mi;
-  cnt_in[t] = ci;
-  __syncthreads();
+// The bins in which the row's cut can fall, from the sums up to and with each
+// bin (thread t's own mi and ci are those of bin t).
+__device__ RowInfo find_border(const Settings& s, const Binning& b, bool counts, uint64_t mi, uint32_t ci,
+                               const uint64_t* mass_in, const uint32_t* cnt_in, int* ipart) {
+  const int t = threadIdx.x;
   const uint64_t total = mass_in[kBins - 1];
   const uint32_t entries = cnt_in[kBins - 1];
   auto first = [&](bool hit) { return block_min(hit ? t : kNone, ipart); };
@@ -356,7 +404,6 @@ __global__ __launch_bounds__(kThreads) void sample_border_kernel(SampleArgs a, W
     lo = min(lo, e_lo);
     hi = min(hi, e_hi);
   }
-  if (t != 0) return;
   RowInfo r;
   auto mass_before = [&](int k) -> uint64_t { return k > 0 ? mass_in[k - 1] : 0; };
   // Without counts only whether there are entries before matters (bin 0 holds the maximum).
@@ -372,7 +419,47 @@ __global__ __launch_bounds__(kThreads) void sample_border_kernel(SampleArgs a, W
   r.cnt_lo = cnt_before(lo);
   r.mass_bk = mass_before(bk);
   r.cnt_bk = cnt_before(bk);
-  ws.info[row] = r;
+  return r;
+}
+
+// A launch of its own: found by every collect block for itself, the sums' reads
+// cost more than the launch (64x151936: 5 + 9 us against 20 in one).
+__global__ __launch_bounds__(kThreads) void sample_border_kernel(SampleArgs a, Ws ws, int chunks) {
+  __shared__ uint64_t mass_in[kBins];   // sums up to and with each bin
+  __shared__ uint32_t cnt_in[kBins];
+  __shared__ int ipart[kWaves];
+  const int row = blockIdx.x, t = threadIdx.x;
+  const Settings s = settings(a, row);
+  const bool counts = s.k < a.n;
+  uint64_t mi = 0;
+  uint32_t ci = 0;
+  const int64_t at = (int64_t)row * chunks * kBins + t;
+#pragma unroll
+  for (int c = 0; c < kMaxChunks; ++c) {   // all loads before the first use
+    mi += c < chunks ? ws.hist_mass[at + (int64_t)c * kBins] : 0;
+    ci += counts && c < chunks ? ws.hist_cnt[at + (int64_t)c * kBins] : 0;
+  }
+  const float2 st = row_stats(ws.stats + (int64_t)row * chunks, chunks);
+  const Binning b = binning(st.x, st.y, s.t);
+  mass_in[t] = mi;
+  cnt_in[t] = ci;
+  __syncthreads();
+  const RowInfo r = find_border(s, b, counts, mi, ci, mass_in, cnt_in, ipart);
+  if (t == 0) ws.info[row] = r;
+}
+
+// The entries of a range inside the border's bins, in any order: larger logit
+// first, then lower index is "greater is ranked earlier" with ~index below.
+__device__ __forceinline__ void range_list(Entries<8>& in, const RowInfo& r, uint64_t* list, int& count) {
+  const int lo = r.lo, hi = r.hi, bk = r.want_bk ? r.bk : -1;
+  const Binning b{r.mx, r.c};
+  in.each([&](float v, int i) {
+    const int k = bin_of(v, b);
+    if (((k >= lo && k <= hi) || k == bk) && live(v, b.mx)) {
+      const int at = atomicAdd(&count, 1);
+      if (at < kCand) list[at] = (uint64_t)order_of(v) << 32 | (uint32_t)~i;
+    }
+  });
 }
 
 __global__ __launch_bounds__(kThreads) void sample_collect_kernel(SampleArgs a, Ws ws, int per) {
@@ -381,18 +468,10 @@ __global__ __launch_bounds__(kThreads) void sample_collect_kernel(SampleArgs a, 
   const int row = blockIdx.y, c = blockIdx.x, t = threadIdx.x;
   Entries<8> in(a.logits + (int64_t)row * a.ld, chunk_range(c, per, a.n));
   const RowInfo& r = ws.info[row];
-  const int lo = r.lo, hi = r.hi, bk = r.want_bk ? r.bk : -1;
-  if (lo == kNone) return;   // nothing is cut
-  const Binning b{r.mx, r.c};
+  if (r.lo == kNone) return;   // nothing is cut
   if (t == 0) count = 0;
   __syncthreads();
-  in.each([&](float v, int i) {
-    const int k = bin_of(v, b);
-    if (((k >= lo && k <= hi) || k == bk) && live(v, b.mx)) {
-      const int at = atomicAdd(&count, 1);
-      if (at < kCand) list[at] = (uint64_t)order_of(v) << 32 | (uint32_t)i;
-    }
-  });
+  range_list(in, r, list, count);
   __syncthreads();
   // One place in the row's list per block; its order does not matter.
   if (t == 0) base = count ? atomicAdd(&ws.listed[row], count) : 0;
@@ -499,18 +578,25 @@ __device__ Cut bisect(const SampleArgs& a, const float* l, float mx, const Setti
   return Cut{o, same ? nth_index(o, take) : 0x7FFFFFFF, 0};
 }
 
+// One exchange of the sort below: the lane keeps the larger or the smaller of
+// its and lane ^ J's key.
+template <int K, int J>
+__device__ __forceinline__ uint64_t sort_step(uint64_t v) {
+  const int lane = threadIdx.x & 63;
+  const uint64_t o = lane_xor<J>(v);
+  const bool larger = ((lane & J) == 0) == ((lane & K) == 0);
+  v = (v > o) == larger ? v : o;
+  if constexpr (J > 1) return sort_step<K, J / 2>(v);
+  return v;
+}
 // Sorts the wave's 64 keys in descending order (bitonic, across lanes).
 __device__ __forceinline__ uint64_t wave_sort_desc(uint64_t v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int k = 2; k <= 64; k *= 2)
-#pragma unroll
-    for (int j = k / 2; j > 0; j /= 2) {
-      const uint64_t o = (uint64_t)__shfl_xor((unsigned long long)v, j, 64);
-      const bool larger = ((lane & j) == 0) == ((lane & k) == 0);   // this lane keeps the larger of the two
-      v = (v > o) == larger ? v : o;
-    }
-  return v;
+  v = sort_step<2, 1>(v);
+  v = sort_step<4, 2>(v);
+  v = sort_step<8, 4>(v);
+  v = sort_step<16, 8>(v);
+  v = sort_step<32, 16>(v);
+  return sort_step<64, 32>(v);
 }
 
 // Sorts key[0..nc) in descending order, nc <= kCand, keys distinct: each wave
@@ -556,14 +642,14 @@ __device__ void sort_desc(uint64_t* key, int nc) {
   __syncthreads();
 }
 
-__global__ __launch_bounds__(kThreads) void sample_choose_kernel(SampleArgs a, Ws ws, int chunks, int per) {
-  __shared__ uint64_t part[kWaves];
-  __shared__ int ipart[kWaves];
-  __shared__ unsigned long long mass[kMaxChunks];
-  __shared__ uint64_t key[kCand];
+// The row's token and logprob, from its border, the listed entries (key, unsorted;
+// more than kCand: not used) and the weight of each chunk's entries in the bins
+// before the border (mass, in LDS; all of it where nothing is cut).  A barrier
+// stands between the writes of key and mass and the call.  part: kWaves + 1.
+__device__ void choose(const SampleArgs& a, int row, const Settings& s, const RowInfo& r, int listed, int chunks,
+                       int per, uint64_t* key, unsigned long long* mass, uint64_t* part, int* ipart) {
   static_assert(kCand == 2 * kThreads, "two listed entries per thread");
-  const int row = blockIdx.x, t = threadIdx.x, wave = t >> 6, lane = t & 63;
-  const RowInfo r = ws.info[row];
+  const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
   const float mx = r.mx;
   if (!(mx > -INFINITY)) {   // nothing to choose from
     if (t == 0) {
@@ -572,19 +658,12 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(SampleArgs a, W
     }
     return;
   }
-  const Settings s = settings(a, row);
   const Binning b{mx, r.c};
   const float* l = a.logits + (int64_t)row * a.ld;
   Cut cut{0u, 0x7FFFFFFF, 0};   // nothing cut: every live entry is ordered above 0
-  const int listed = r.lo == kNone ? 0 : ws.listed[row];
   if (listed <= kCand) {
-    if (t < chunks) mass[t] = r.lo ? ws.hist_mass[((int64_t)row * chunks + t) * kBins + r.lo - 1] : 0;
     if (r.lo != kNone) {
-      // Larger logit first, then lower index: ~index makes "greater is ranked
-      // earlier" one comparison.
       const int nc = listed;
-      for (int i = t; i < nc; i += kThreads) key[i] = ws.cand[(int64_t)row * kCand + i] ^ 0xFFFFFFFFull;
-      __syncthreads();
       sort_desc(key, nc);
       // Thread t holds places 2t and 2t+1; their rank and the weight before
       // them, among the listed entries.
@@ -686,8 +765,7 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(SampleArgs a, W
       for (int e = 0; e < kBatch; ++e)
         if (kept(v[e], i + 64 * e, b, cut)) q += weight(v[e], mx, s.inv_t2);
     }
-#pragma unroll
-    for (int off = 32; off > 0; off /= 2) q += (uint64_t)__shfl_xor((unsigned long long)q, off, 64);
+    q = wave_sum(q);
     __syncthreads();
     if (lane == 0) part[wave] = q;
     __syncthreads();
@@ -710,22 +788,36 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(SampleArgs a, W
   }
   const int i0 = rc.begin + w * part_len, i1 = min(rc.end, i0 + part_len);
   int token = -1;
-  for (int base = i0; base < i1; base += kThreads) {
-    const int i = base + t;
-    const float v = i < i1 ? l[i] : -INFINITY;
-    const uint64_t q = i < i1 && kept(v, i, b, cut) ? weight(v, mx, s.inv_t2) : 0;
-    const uint64_t sum = run + block_scan(q, part);
-    const int hit = block_min(!over && q && (double)sum > want ? i : 0x7FFFFFFF, ipart);
+  constexpr int kEach = 4;   // neighbouring entries per thread
+  for (int base = i0; base < i1; base += kEach * kThreads) {
+    const int first = base + kEach * t;
+    float v[kEach];
+    uint64_t q[kEach], own = 0;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) v[e] = first + e < i1 ? l[first + e] : -INFINITY;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      q[e] = kept(v[e], first + e, b, cut) ? weight(v[e], mx, s.inv_t2) : 0;
+      own += q[e];
+    }
+    uint64_t sum = run + block_scan(own, part);
+    if (t == kThreads - 1) part[kWaves] = sum;   // read behind the barriers below
+    sum -= own;
+    int hit = 0x7FFFFFFF, far = -1;   // the first whose running sum exceeds it, the last with weight
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      sum += q[e];
+      if (q[e] && !over && hit == 0x7FFFFFFF && (double)sum > want) hit = first + e;
+      if (q[e]) far = first + e;
+    }
+    hit = block_min(hit, ipart);
     if (hit != 0x7FFFFFFF) {
       token = hit;
       break;
     }
-    const int far = -block_min(q ? -i : 1, ipart);   // the last one with weight, -1 without
+    far = -block_min(-far, ipart);
     token = far >= 0 ? far : token;
-    __syncthreads();
-    if (t == kThreads - 1) part[0] = sum;
-    __syncthreads();
-    run = part[0];
+    run = part[kWaves];
   }
   if (t == 0) {
     a.tokens[row] = token;
@@ -739,13 +831,73 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(SampleArgs a, W
   }
 }
 
+__global__ __launch_bounds__(kThreads) void sample_choose_kernel(SampleArgs a, Ws ws, int chunks, int per) {
+  __shared__ uint64_t part[kWaves + 1];
+  __shared__ int ipart[kWaves];
+  __shared__ unsigned long long mass[kMaxChunks];
+  __shared__ uint64_t key[kCand];
+  const int row = blockIdx.x, t = threadIdx.x;
+  const RowInfo r = ws.info[row];
+  const int listed = r.lo == kNone ? 0 : ws.listed[row];
+  if (t < chunks) mass[t] = r.lo ? ws.hist_mass[((int64_t)row * chunks + t) * kBins + r.lo - 1] : 0;
+  for (int i = t; i < listed && i < kCand; i += kThreads) key[i] = ws.cand[(int64_t)row * kCand + i];
+  __syncthreads();
+  choose(a, row, settings(a, row), r, listed, chunks, per, key, mass, part, ipart);
+}
+
+// All five steps in one block and one launch, the sums and the list in LDS and
+// the row read again from the L2.
+__global__ __launch_bounds__(kThreads) void sample_row_kernel(SampleArgs a) {
+  __shared__ uint64_t mass[kBins];
+  __shared__ uint32_t cnt[kBins];
+  __shared__ uint64_t key[kCand];
+  __shared__ uint64_t part[kWaves + 1];
+  __shared__ float2 fpart[kWaves];
+  __shared__ int ipart[kWaves];
+  __shared__ unsigned long long whole;
+  __shared__ int count;
+  const int row = blockIdx.x, t = threadIdx.x;
+  const float* l = a.logits + (int64_t)row * a.ld;
+  const Range all{0, a.n};
+  const Settings s = settings(a, row);
+  const bool counts = s.k < a.n;
+  cnt[t] = 0;
+  mass[t] = 0;
+  if (t == 0) count = 0;
+  const float2 st = range_stats(l, all, fpart);   // its barrier covers the clearing
+  const Binning b = binning(st.x, st.y, s.t);
+  {
+    Entries<4> in(l, all);
+    range_hist(in, s, b, counts, cnt, reinterpret_cast<unsigned long long*>(mass));
+  }
+  __syncthreads();
+  const uint64_t mi = block_scan(mass[t], part);
+  const uint32_t ci = counts ? (uint32_t)block_scan(cnt[t], part) : 0;
+  mass[t] = mi;
+  cnt[t] = ci;
+  __syncthreads();
+  const RowInfo r = find_border(s, b, counts, mi, ci, mass, cnt, ipart);
+  if (r.lo != kNone) {
+    Entries<8> in(l, all);
+    range_list(in, r, key, count);
+  }
+  if (t == 0) whole = r.mass_lo;   // all of the row's where nothing is cut
+  __syncthreads();
+  choose(a, row, s, r, count, 1, a.n, key, &whole, part, ipart);
+}
+
 // Chunks for about 512 blocks over all rows (two per CU; 1024: 64x151936 69 ->
-// 73 us), at most 16 per row:
-// the border launch adds them up.
+// 73 us), at most 16 per row: the border launch adds them up.
 struct Plan {
   int per, chunks;
 };
+// One block and launch for a row that is short, or not too long where there is a
+// row for every CU.  Measured, one launch against five (us): 1 x 4000 16 and 24, 1 x
+// 16000 25 and 27, 1 x 32000 37 and 27; 64 x 8000 23 and 38, 64 x 50257 62 and 42;
+// 256 x 16000 31 and 41, 256 x 50257 68 and 74, 256 x 151936 184 and 166.
+constexpr int64_t kShortRow = 20480, kBlockRow = 65536, kManyRows = 256;
 Plan plan(int64_t m, int64_t n) {
+  if (n <= kShortRow || (n <= kBlockRow && m >= kManyRows)) return {(int)n, 1};
   const int64_t tiles = (n + kThreads - 1) / kThreads;
   int64_t want = (512 + m - 1) / m;
   want = want < kMaxChunks ? want : kMaxChunks;
@@ -760,12 +912,17 @@ int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
 
 int64_t sample_workspace_bytes(int64_t m, int64_t n) {
   const Plan p = plan(m, n);
+  if (p.chunks == 1) return 256;   // nothing is kept between launches
   return align256(m * p.chunks * (int64_t)sizeof(float2)) + align256(m * (int64_t)sizeof(RowInfo)) + align256(m * 4) +
          align256(m * p.chunks * kBins * 4) + align256(m * p.chunks * kBins * 8) + align256(m * kCand * 8);
 }
 
 hipError_t launch_sample(const SampleArgs& a, void* workspace, hipStream_t s) {
   const Plan p = plan(a.m, a.n);
+  if (p.chunks == 1) {
+    hipLaunchKernelGGL(sample_row_kernel, dim3((unsigned)a.m), dim3(kThreads), 0, s, a);
+    return hipGetLastError();
+  }
   uint8_t* at = static_cast<uint8_t*>(workspace);
   auto take = [&](int64_t bytes) {
     uint8_t* r = at;

@@ -81,6 +81,40 @@ def test_ties(q3):
     check(q3, l, u, 0.5 + rng.random(8), rng.integers(1, 20000, 8), rng.random(8), 0.3 * rng.random(8))
 
 
+def longer(l, n):
+    """The same rows with masked entries behind them, up to n."""
+    return np.concatenate([l, np.full((len(l), n - l.shape[1]), -INF, np.float32)], 1)
+
+
+@pytest.mark.parametrize("n", [20480, 20481, 65536, 65537, 131072])
+def test_rows_in_one_block_and_in_several(q3, n):
+    # spreads, ties and masks at both sides of the length where a row is split over blocks
+    rng = np.random.default_rng(n)
+    l, u = rows(8, 9000, seed=n)
+    l[1] = np.round(l[1])
+    l[2] = 1.5
+    l[3, rng.random(9000) < 0.9] = -INF
+    l[4, rng.random(9000) < 0.5] = np.nan
+    l[5, [7, 400, 8999]] = INF
+    l[6] = -INF
+    l[7] *= 100
+    long = np.concatenate([longer(l, n), rows(4, n, seed=1)[0]])
+    u = rng.random(12).astype(np.float32)
+    u[3], u[9] = 1.0, 0.0
+    check(q3, long, u)
+    check(q3, long, u, top_k=[1, 50, 3000, 9, 1000, 2, 3, 1, 40, n - 1, n // 2, 5])
+    check(q3, long, u, top_p=rng.random(12))
+    check(q3, long, u, 0.3 + rng.random(12), rng.integers(0, 4000, 12), 0.2 + rng.random(12), 0.1 * rng.random(12))
+    tok = check(q3, long, u, temperature=np.zeros(12))
+    assert tok[6] == -1
+
+
+def test_many_long_rows(q3):
+    for n in (30000, 65536, 65537):
+        l, u = rows(256, n, seed=n)
+        check(q3, l, u, top_k=[0, 30] * 128, top_p=[0.9, 1.0, 0.5, 0.99] * 64)
+
+
 def test_equal_weights_draw_evenly(q3):
     # dyadic sums are exact on both sides: u = i/n picks entry i
     n = 4096
@@ -139,7 +173,7 @@ def test_pitched_rows_outputs_and_workspace(q3):
     b = check(q3, l, u, top_p=[0.9] * 4, workspace=ws)
     assert (a == b).all() and (tok.cpu().numpy() == a).all()
     with pytest.raises(q3.Q3Error):
-        q3.q3_sample(wide[:, :3000], tok.float(), workspace=ws[:256])
+        q3.q3_sample(wide[:, :3000], tok.float(), workspace=ws[:ws.numel() // 2])
     with pytest.raises(q3.Q3Error):
         q3.q3_sample(torch.zeros(1, (1 << 19) + 1, device="cuda"), torch.zeros(1, device="cuda"))
     with pytest.raises(ValueError):
@@ -152,12 +186,13 @@ def test_largest_vocabulary(q3):
     check(q3, np.zeros((2, 1 << 19), np.float32), u, top_p=[0.25, 1.0])
 
 
-def test_captured_and_replayed(q3):
+@pytest.mark.parametrize("n", [4000, 40000])
+def test_captured_and_replayed(q3, n):
     # new logits, numbers and settings under the same graph; other work in between
-    l = torch.randn(5, 40000, device="cuda")
+    l = torch.randn(5, n, device="cuda")
     u = torch.rand(5, device="cuda")
     p = torch.full((5,), 0.9, device="cuda")
-    ws = q3.sample_workspace(5, 40000, "cuda")
+    ws = q3.sample_workspace(5, n, "cuda")
     tok, lp = torch.empty(5, dtype=torch.int32, device="cuda"), torch.empty(5, device="cuda")
     q3.q3_sample(l, u, top_p=p, workspace=ws, tokens=tok, logprobs=lp)
     torch.cuda.synchronize()
@@ -165,7 +200,7 @@ def test_captured_and_replayed(q3):
     with torch.cuda.graph(g):
         q3.q3_sample(l, u, top_p=p, workspace=ws, tokens=tok, logprobs=lp)
     for i in range(4):
-        l.copy_(torch.randn(5, 40000, device="cuda") * (i + 0.5))
+        l.copy_(torch.randn(5, n, device="cuda") * (i + 0.5))
         u.copy_(torch.rand(5, device="cuda"))
         p.fill_(0.5 + 0.15 * i)
         g.replay()
