@@ -80,7 +80,7 @@ def _call(name, device, *args):
     index = device.index
     # The raw handle: a Stream object costs 2 us of host time per call.
     stream = torch._C._cuda_getCurrentRawStream(index)
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         status = fn(*args, stream)
     else:
         with torch.cuda.device(device):
@@ -308,15 +308,15 @@ def q3_residual_norm_backward(r_out: torch.Tensor, pre_weight: torch.Tensor = No
     # The gradients summed over the tokens share one allocation; bf16 rows are
     # pitched so that q3_gemm_backward takes them as they are.
     wide = (n + 7) // 8 * 8
-    sums = torch.empty((3, (n + 3) // 4 * 4), dtype=torch.float32, device=dev)
-    g = ResidualNormGrads(dr=r_out.new_empty((m, n)), dpre_weight=sums[0, :n])
+    sums = torch.empty((3, n), dtype=torch.float32, device=dev).unbind(0)
+    g = ResidualNormGrads(r_out.new_empty((m, n)), sums[0])
     if y is not None:
-        dy = torch.empty((m, wide), dtype=torch.bfloat16, device=dev)
+        dy = r_out.new_empty((m, wide), dtype=torch.bfloat16)
         g.dy = dy if wide == n else dy[:, :n]
     if gate is not None:
-        g.dgate = y.new_empty((m, n)) if gate.dim() == 2 else sums[2, :n]
+        g.dgate = y.new_empty((m, n)) if gate.dim() == 2 else sums[2]
     if post_weight is not None:
-        g.dpost_weight = sums[1, :n]
+        g.dpost_weight = sums[1]
     ws = _ws(workspace, lib().q3_residual_norm_backward_workspace_bytes(m, n), dev)
     grads = Q3ResidualNormGrads(_ptr(dx), _pitch(dx), _ptr(dr_out), _pitch(dr_out), g.dr.data_ptr(), n, _ptr(g.dy),
                                 wide, _ptr(g.dgate), n, _ptr(g.dpost_weight), g.dpre_weight.data_ptr())
