@@ -878,7 +878,7 @@ void wide_kernel(KArgs a) {
   }
   const rsrc_t xr = make_rsrc(a.x, (uint32_t)((a.x_rows - 1) * a.ldx * 2 + (int64_t)a.G * 64));
   const uint32_t ldx_bytes = (uint32_t)(a.ldx * 2);
-  const uint32_t lane16 = 16u * (uint32_t)lane, row_bytes = (uint32_t)a.G * 64u;
+  const uint32_t lane16 = 16u * (uint32_t)lane;
   if (tid < 64) *reinterpret_cast<u32x4*>(lds + zero_base + 16u * tid) = u32x4{0u, 0u, 0u, 0u};
 
   for (int slice = 0; slice < a.m; slice += kSlice) {
@@ -904,8 +904,7 @@ void wide_kernel(KArgs a) {
     auto loads_of = [&](StepData<R>& dst, uint32_t buf, int sn) {
       const bool live = sn < s_end;
       const uint32_t sc = (uint32_t)(live ? sn : s_end - 1);
-      const uint32_t xl = live && 1024u * sc + lane16 < row_bytes ? lane16 : kOob;   // zeros past K
-      return [&, buf, live, sc, xl](auto q) {
+      return [&, buf, live, sc](auto q) {
         constexpr int Q = decltype(q)::value;
         if constexpr (Q < 3 * R) {
           constexpr int r = Q / 3, j = Q % 3;
@@ -919,7 +918,7 @@ void wide_kernel(KArgs a) {
           const int j = wave + kW * (Q - 4 * R);
           __builtin_amdgcn_raw_ptr_buffer_load_lds(
               xr, (__attribute__((address_space(3))) void*)(lds + buf + (uint32_t)j * rstride), 16,
-              j < cnt ? xl : kOob, (uint32_t)(slice + (j < cnt ? j : 0)) * ldx_bytes + 1024u * sc, 0, 0);
+              live && j < cnt ? lane16 : kOob, (uint32_t)(slice + (j < cnt ? j : 0)) * ldx_bytes + 1024u * sc, 0, 0);
         }
       };
     };
@@ -1108,13 +1107,12 @@ void wide_hs_kernel(KArgs a) {
   // lane l takes token 2q + l/32 and the chunk stored at position l%32.  The
   // position-to-chunk map depends on the token's low four bits, which for
   // this wave's loads take two values (j even, j odd).
-  uint32_t xsrc[2], xcol[2];
+  uint32_t xsrc[2];
 #pragma unroll
   for (int par = 0; par < 2; ++par) {
     const uint32_t t = 2u * (uint32_t)(wave + kW * par) + (uint32_t)(lane >> 5);
     const uint32_t c = ((uint32_t)lane & 31u) ^ (t & 15u);
-    xcol[par] = 256u * (c >> 3) + 16u * (c & 7u);
-    xsrc[par] = (uint32_t)(lane >> 5) * ldx_bytes + xcol[par];
+    xsrc[par] = (uint32_t)(lane >> 5) * ldx_bytes + 256u * (c >> 3) + 16u * (c & 7u);
   }
   const uint32_t i7 = (uint32_t)i & 7u;
 
@@ -1139,14 +1137,8 @@ void wide_hs_kernel(KArgs a) {
       const uint32_t sc = (uint32_t)(live ? sn : s_end - 1);
       const uint32_t vc = live ? vcode + 8u * decltype(hc)::value : kOob;
       const uint32_t vs = live ? vscale : kOob;
-      uint32_t xl[2];   // zeros past K
-#pragma unroll
-      for (int par = 0; par < 2; ++par) {
-        const uint32_t h = 128u * decltype(hc)::value;
-        xl[par] = live && 1024u * sc + h + xcol[par] < (uint32_t)a.G * 64u ? xsrc[par] + h : kOob;
-      }
       using Half = decltype(hc);
-      return [&, buf, sc, vc, vs, xl](auto q) {
+      return [&, buf, live, sc, vc, vs](auto q) {
         constexpr uint32_t H = Half::value;
         // The first half-step reads the first 8 bytes of every 16-byte piece
         // and the second the rest, half a step later.  Non-temporal loads in
@@ -1173,7 +1165,7 @@ void wide_hs_kernel(KArgs a) {
           const int t = 2 * qi + (lane >> 5);
           __builtin_amdgcn_raw_ptr_buffer_load_lds(
               xr, (__attribute__((address_space(3))) void*)(lds + buf + (uint32_t)qi * 1024u), 16,
-              t < cnt ? xl[jq & 1] : kOob,
+              live && t < cnt ? xsrc[jq & 1] + 128u * H : kOob,
               (uint32_t)(slice + (2 * qi < cnt ? 2 * qi : 0)) * ldx_bytes + 1024u * sc, 0, 0);
         }
       };
