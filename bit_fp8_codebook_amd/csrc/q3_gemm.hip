@@ -5,8 +5,9 @@
 //   dx[m][k] = sum_n dy[m][n] w[n][k]         (q3_gemm_backward)
 //   h[m][i]  = act(x . w[i]) * (x . w[I + i]) (q3_glu)
 //
-// Up to 64 tokens a product is bound by the packed weights, and q3_linear.hip's
-// kernels read them once.  For more tokens it is bound by the matrix cores, and
+// Few tokens are bound by the packed weights and their dequantisation, and
+// q3_linear.hip's kernels read them once for up to 64 or 128 tokens.  Many are
+// bound by the matrix cores, and
 // dequantising inside the product would repeat the vector work for every block
 // of tokens; so the matrix is widened once, exactly, to bf16 in the caller's
 // workspace (for the gradient: transposed) and all three run on one kernel:
@@ -522,17 +523,34 @@ int64_t padded_k(int64_t k) { return (k + 127) / 128 * 128; }
 int64_t padded_n(int64_t n) { return (n + 63) / 64 * 64; }
 constexpr int64_t kSmallM = 64;
 
-// Whether m tokens go through the packed planes 64 at a time: widening costs as
-// much as a few such passes over a tall matrix, and on a short one a pass does
-// not fill the chip.  Measured at K = 4096, passes against widening (us): 4096
-// rows, 128 tokens 31 and 26; 11008, 128 33 and 46; 14336, 192 55 and 61, 256 74
-// and 65; 18432, 192 91 and 90, 256 121 and 88; 28672, 384 139 and 154, 512 192
-// and 152; 40000, 448 273 and 271, 512 310 and 272; 65536, 512 347 and 335; 151936,
-// 512 681 and 782, 768 1007 and 996.  K = 8192: 28672, 384 241 and 295; 57344, 512
-// 593 and 583.
-bool in_passes(int64_t n, int64_t m) {
-  const int64_t passes = (m + kSmallM - 1) / kSmallM, most = n / 4700;
-  return passes <= (most < 7 ? most : 7) || passes == 1;
+// Tokens that go through the packed planes at a time, and in how many passes at
+// most; more are multiplied with the widened matrix.  On whole 512-k steps a pass
+// takes 128: a product's K is split until the chip is full, so passes pay in
+// proportion to the matrix; a gated pass takes the same time up to 32768 rows
+// (a pair of tiles per SIMD), and widening a time that grows with them.  Elsewhere
+// a pass takes 64, which fills the chip on tall matrices only.  Measured, passes
+// and widening (us), at K = 4096 where not said:
+//   products  4096 rows, 128 tokens 22 and 26, 256 43 and 33; 4096 x 14336, 256 59
+//             and 65, 300 78 and 73; 8192 x 8192, 384 87 and 96; 11008, 256 57 and
+//             54; 14336, 256 59 and 64, 384 89 and 73; 28672, 384 120 and 153, 512
+//             160 and 155; 100000, 384 468 and 580
+//   gated     1024 x 1024, 128 tokens 15 and 18; 16384 rows, 128 39 and 64, 256 78
+//             and 66; 22016, 384 118 and 144; 28672, 384 118 and 165, 512 158 and
+//             160; 57344 x 8192, 384 433 and 576
+//   by 64     11008, 128 34 and 46; 14336, 192 55 and 61, 256 70 and 64; 18432, 256
+//             121 and 88; 28672, 384 141 and 153; 65536, 512 347 and 335
+// and 128 a pass against 64: 28672, 128 40 and 46; 8192 x 8192, 128 30 and 53.
+struct Passes {
+  int64_t tokens, most;
+};
+Passes passes_of(int64_t n, int64_t k, bool glu) {
+  auto clamp = [](int64_t v, int64_t hi) { return v < 1 ? 1 : (v > hi ? hi : v); };
+  if (k % 512 == 0) return {128, glu ? (n >= 20000 ? 3 : 1) : clamp(n * k / 22000000, 3)};
+  return {kSmallM, clamp(n / 4700, 7)};
+}
+bool in_passes(int64_t n, int64_t k, int64_t m, bool glu) {
+  const Passes p = passes_of(n, k, glu);
+  return m <= p.tokens * p.most;
 }
 
 hipError_t launch_widen(const PlaneView& w, uint16_t* out, hipStream_t s) {
@@ -577,10 +595,15 @@ __global__ __launch_bounds__(256) void glu_back_kernel(const float* __restrict__
 }  // namespace
 
 int64_t gemm_workspace_bytes(int64_t n, int64_t k, int64_t m) {
-  if (in_passes(n, m)) {
-    const int64_t full = m >= kSmallM ? gemm_small_m_workspace_bytes(n, k, kSmallM) : 0;
-    const int64_t last = m % kSmallM ? gemm_small_m_workspace_bytes(n, k, m % kSmallM) : 0;
-    return full > last ? full : last;
+  if (in_passes(n, k, m, false)) {
+    int64_t most = 0;
+    const int64_t step = passes_of(n, k, false).tokens;
+    for (int64_t c : {m < step ? m : step, m % step}) {
+      if (c == 0) continue;
+      const int64_t b = c > kSmallM ? gemm_mid_workspace_bytes(n, k, c) : gemm_small_m_workspace_bytes(n, k, c);
+      most = most > b ? most : b;
+    }
+    return most;
   }
   return align256(n * padded_k(k) * 2) + align256(split_bytes(m, n, k));
 }
@@ -589,11 +612,12 @@ hipError_t launch_gemm(const PlaneView& w, const uint16_t* x, int64_t m, int64_t
                        hipStream_t s) {
   const int64_t k = (int64_t)w.groups * 32;
   if (w.n == 0) return hipSuccess;
-  if (in_passes(w.n, m)) {
-    const int64_t bytes = ws ? gemm_workspace_bytes(w.n, k, m) : 0;
-    for (int64_t i = 0; i < m; i += kSmallM) {
-      const int64_t c = m - i < kSmallM ? m - i : kSmallM;
-      const hipError_t e = launch_gemm_small_m(w, x + i * ldx, c, ldx, y + i * ldy, ldy, ws, bytes, s);
+  if (in_passes(w.n, k, m, false)) {
+    const int64_t bytes = ws ? gemm_workspace_bytes(w.n, k, m) : 0, step = passes_of(w.n, k, false).tokens;
+    for (int64_t i = 0; i < m; i += step) {
+      const int64_t c = m - i < step ? m - i : step;
+      const hipError_t e = c > kSmallM ? launch_gemm_mid(w, x + i * ldx, c, ldx, y + i * ldy, ldy, ws, s)
+                                       : launch_gemm_small_m(w, x + i * ldx, c, ldx, y + i * ldy, ldy, ws, bytes, s);
       if (e != hipSuccess) return e;
     }
     return hipSuccess;
@@ -659,17 +683,21 @@ hipError_t launch_gemm_backward(const PlaneView& w, const uint16_t* dy, int64_t 
 }
 
 int64_t glu_workspace_bytes(int64_t n_gu, int64_t k, int64_t m) {
-  return in_passes(n_gu, m) ? 0 : align256(n_gu * padded_k(k) * 2);
+  return in_passes(n_gu, k, m, true) ? 0 : align256(n_gu * padded_k(k) * 2);
 }
 
 hipError_t launch_glu(const PlaneView& gate_up, const uint16_t* x, int64_t m, int64_t ldx, int32_t act, uint16_t* h,
                       int64_t ldh, float* pre, int64_t ld_pre, void* ws, hipStream_t s) {
   if (gate_up.n == 0) return hipSuccess;
-  if (in_passes(gate_up.n, m)) {
-    for (int64_t i = 0; i < m; i += kSmallM) {
-      const int64_t c = m - i < kSmallM ? m - i : kSmallM;
-      const hipError_t e = launch_glu_small_m(gate_up, x + i * ldx, c, ldx, act, h + i * ldh, ldh,
-                                              pre ? pre + i * ld_pre : nullptr, ld_pre, s);
+  const int64_t k = (int64_t)gate_up.groups * 32;
+  if (in_passes(gate_up.n, k, m, true)) {
+    const int64_t step = passes_of(gate_up.n, k, true).tokens;
+    for (int64_t i = 0; i < m; i += step) {
+      const int64_t c = m - i < step ? m - i : step;
+      float* p = pre ? pre + i * ld_pre : nullptr;
+      const hipError_t e =
+          c > kSmallM ? launch_glu_mid(gate_up, x + i * ldx, c, ldx, act, h + i * ldh, ldh, p, ld_pre, s)
+                      : launch_glu_small_m(gate_up, x + i * ldx, c, ldx, act, h + i * ldh, ldh, p, ld_pre, s);
       if (e != hipSuccess) return e;
     }
     return hipSuccess;
@@ -681,10 +709,10 @@ hipError_t launch_glu(const PlaneView& gate_up, const uint16_t* x, int64_t m, in
   g.a = x;
   g.lda = ldx;
   g.b = wide;
-  g.ldb = padded_k((int64_t)gate_up.groups * 32);
+  g.ldb = padded_k(k);
   g.m = m;
   g.n = gate_up.n / 2;
-  g.k = (int64_t)gate_up.groups * 32;
+  g.k = k;
   g.h = h;
   g.ldh = ldh;
   g.pre = pre;

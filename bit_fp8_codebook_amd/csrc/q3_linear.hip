@@ -1020,11 +1020,30 @@ constexpr int kKeepPolicy = 1;               // work-group scope (sc0), no non-t
 // Chunk CH = 4 tt + e of a half-step: B operands of the NT column tiles, then
 // the chunk's dequantisation and 4 MFMAs for each row tile.  xrow: the lane's
 // token row in the buffer plus 16 * ((8 kb) ^ (i & 8)); i7 = i & 7.
+// The column tiles' B operands of chunk CH.
+template <int NT>
+__device__ __forceinline__ void wide_hs_read(bf16x8 (&b)[NT], int ch, uint32_t xrow, uint32_t i7, const uint8_t* lds) {
+  const uint32_t xa = xrow + 16u * ((uint32_t)ch ^ i7);
+#pragma unroll
+  for (int c = 0; c < NT; ++c)
+    b[c] = *reinterpret_cast<const bf16x8*>(lds + xa + (uint32_t)c * 16u * kHalfTokenBytes);
+}
+
+// The wave's weights of chunk CH.
+template <int R, int CH>
+__device__ __forceinline__ void wide_hs_weights(bf16x8 (&w)[R], const HalfStep<R>& d, const RowCb (&cb)[R]) {
+  constexpr int tt = CH / 4, e = CH % 4;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const float sc = e8m0_to_f32((d.sc[r] >> (8 * tt)) & 0xFFu);
+    w[r] = dequant_chunk<e>(d.w[r][0][tt], d.w[r][1][tt], d.w[r][2][tt], sc, cb[r].lo, cb[r].hi);
+  }
+}
+
 template <int NT, int R, int kLoads, int CH, typename Issue>
 __device__ __forceinline__ void wide_hs_chunk(const HalfStep<R>& d, const RowCb (&cb)[R], uint32_t xrow, uint32_t i7,
                                             const uint8_t* lds, f32x4 (&acc)[R][NT], Issue& issue) {
   if constexpr (CH < 8) {
-    constexpr int tt = CH / 4, e = CH % 4;
     // The next half-step's loads go out an eighth per chunk (issued all at
     // once, or in the first half of the chunks, the wave stalls on them: 5-10%
     // slower), and stay in their chunk: left alone, the scheduler sinks them
@@ -1032,11 +1051,9 @@ __device__ __forceinline__ void wide_hs_chunk(const HalfStep<R>& d, const RowCb 
     constexpr int q0 = CH * kLoads / 8, q1 = (CH + 1) * kLoads / 8;
     issue_range<q0, q1>(issue);
     __builtin_amdgcn_sched_barrier(0);
-    const uint32_t xa = xrow + 16u * ((uint32_t)CH ^ i7);
     bf16x8 b[NT];
-#pragma unroll
-    for (int c = 0; c < NT; ++c)
-      b[c] = *reinterpret_cast<const bf16x8*>(lds + xa + (uint32_t)c * 16u * kHalfTokenBytes);
+    wide_hs_read<NT>(b, CH, xrow, i7, lds);
+    constexpr int tt = CH / 4, e = CH % 4;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const float sc = e8m0_to_f32((d.sc[r] >> (8 * tt)) & 0xFFu);
@@ -1049,10 +1066,50 @@ __device__ __forceinline__ void wide_hs_chunk(const HalfStep<R>& d, const RowCb 
   }
 }
 
+// The same with one wave per SIMD: the next chunk's B operands are read and its
+// weights dequantised between this one's products, two vector instructions
+// behind each (28672 x 4096 at 128 tokens 43.7 -> 40.1 us; three 42.8, five 41.5;
+// the loads in the first four, two or one chunks 41.7, 42.9 and 47.3).
+template <int NT, int R, int kLoads, int CH, typename Issue>
+__device__ __forceinline__ void wide_hs_ahead(const HalfStep<R>& d, const RowCb (&cb)[R], uint32_t xrow, uint32_t i7,
+                                              const uint8_t* lds, f32x4 (&acc)[R][NT], const bf16x8 (&b)[NT],
+                                              const bf16x8 (&w)[R], Issue& issue) {
+  if constexpr (CH < 8) {
+    constexpr int q0 = CH * kLoads / 8, q1 = (CH + 1) * kLoads / 8;
+    issue_range<q0, q1>(issue);
+    __builtin_amdgcn_sched_barrier(0);
+    bf16x8 bn[NT], wn[R];
+    if constexpr (CH < 7) {
+      wide_hs_read<NT>(bn, CH + 1, xrow, i7, lds);
+      __builtin_amdgcn_sched_barrier(0);
+      wide_hs_weights<R, CH + 1>(wn, d, cb);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int c = 0; c < NT; ++c)
+        acc[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[r], b[c], acc[r][c], 0, 0, 0);
+#pragma unroll
+    for (int q = 0; q < R * NT; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);         // a product
+      __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);   // vector instructions
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    wide_hs_ahead<NT, R, kLoads, CH + 1>(d, cb, xrow, i7, lds, acc, bn, wn, issue);
+  }
+}
+
 template <int NT, int R, int kLoads, typename Issue>
 __device__ __forceinline__ void wide_hs_half(const HalfStep<R>& d, const RowCb (&cb)[R], uint32_t xrow, uint32_t i7,
                                            const uint8_t* lds, f32x4 (&acc)[R][NT], Issue&& issue) {
-  wide_hs_chunk<NT, R, kLoads, 0>(d, cb, xrow, i7, lds, acc, issue);
+  if constexpr (NT > 4) {
+    bf16x8 b[NT], w[R];
+    wide_hs_read<NT>(b, 0, xrow, i7, lds);
+    wide_hs_weights<R, 0>(w, d, cb);
+    wide_hs_ahead<NT, R, kLoads, 0>(d, cb, xrow, i7, lds, acc, b, w, issue);
+  } else {
+    wide_hs_chunk<NT, R, kLoads, 0>(d, cb, xrow, i7, lds, acc, issue);
+  }
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -1061,11 +1118,17 @@ __device__ __forceinline__ void wide_hs_half(const HalfStep<R>& d, const RowCb (
 
 constexpr int kWideHsWaves = 4;
 
+
 size_t wide_hs_bytes(int slice) { return 2u * (size_t)slice * kHalfTokenBytes; }
 
-template <int NT, int R>
-__global__ __launch_bounds__(64 * kWideHsWaves) __attribute__((amdgpu_waves_per_eu(2)))
+// Six or eight column tiles (65..128 tokens) take the same steps with one block
+// per CU: a weight is then dequantised once for twice the tokens, which is most
+// of what a pass of 64 issues (28672 x 4096 at 128 tokens: two passes of 64 46 us).
+// kGlu (R = 2): the wave's row tiles are gate tile q and up tile q.
+template <int NT, int R, bool kGlu>
+__global__ __launch_bounds__(64 * kWideHsWaves) __attribute__((amdgpu_waves_per_eu(NT > 4 ? 1 : 2)))
 void wide_hs_kernel(KArgs a) {
+  static_assert(!kGlu || R == 2, "one gate and one up tile");
   constexpr int kW = kWideHsWaves, kSlice = 16 * NT;
   constexpr uint32_t buf_bytes = (uint32_t)kSlice * kHalfTokenBytes;
   static_assert(kSlice % (2 * kW) == 0, "two tokens per activation load, spread evenly over the waves");
@@ -1078,6 +1141,7 @@ void wide_hs_kernel(KArgs a) {
   const uint32_t gp = (uint32_t)a.G;   // a multiple of 16 here
   const int64_t tiles = (a.n + 15) / 16;
   const int64_t tile0 = ((int64_t)blockIdx.x * kW + wave) * R;
+  const int64_t pair = (int64_t)blockIdx.x * kW + wave;   // kGlu
   const rsrc_t code = make_rsrc(a.code, (uint32_t)(tiles * 192 * gp));
   const rsrc_t scale = make_rsrc(a.scale, (uint32_t)(tiles * 16 * gp));
   const int steps = (int)(gp / 16);
@@ -1092,10 +1156,11 @@ void wide_hs_kernel(KArgs a) {
   RowCb cb[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int64_t T = tile0 + r < tiles ? tile0 + r : tiles - 1;
+    const int64_t want = !kGlu ? tile0 + r : (pair < a.half_tiles ? pair + r * (int64_t)a.half_tiles : tiles);
+    const int64_t T = want < tiles ? want : tiles - 1;
     tcode[r] = (uint32_t)T * (192u * gp);
     tscale[r] = (uint32_t)T * (16u * gp);
-    const int64_t row = (tile0 + r) * 16 + i;
+    const int64_t row = want * 16 + i;
     const u32x2 c2 = bload64(cbr, row < a.n ? (uint32_t)row * 8u : kOob);
     cb[r].lo = c2.x;
     cb[r].hi = c2.y;
@@ -1194,6 +1259,10 @@ void wide_hs_kernel(KArgs a) {
     for (int c = 0; c < NT; ++c) {
       const int j = 16 * c + i;
       if (j < cnt) {
+        if constexpr (kGlu) {
+          if (pair < a.half_tiles) store_glu(a, slice + j, pair * 16 + 4 * kb, acc[0][c], acc[1][c]);
+          continue;
+        }
         float* yr = ybase + (int64_t)(slice + j) * a.ldy;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -1255,16 +1324,16 @@ hipError_t launch_wide(const KArgs& a, unsigned splits, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int NT, int R>
+template <int NT, int R, bool kGlu = false>
 hipError_t launch_wide_hs(const KArgs& a, unsigned splits, hipStream_t s) {
   constexpr int kRowsPerBlock = R * kWideHsWaves;
   const size_t shm = wide_hs_bytes(16 * NT);
   static LdsAllowance seen;
-  const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(wide_hs_kernel<NT, R>), shm, seen);
+  const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(wide_hs_kernel<NT, R, kGlu>), shm, seen);
   if (e != hipSuccess) return e;
   const int64_t tiles = (a.n + 15) / 16;
   const dim3 grid((unsigned)((tiles + kRowsPerBlock - 1) / kRowsPerBlock), 1, splits);
-  hipLaunchKernelGGL((wide_hs_kernel<NT, R>), grid, dim3(64 * kWideHsWaves), shm, s, a);
+  hipLaunchKernelGGL((wide_hs_kernel<NT, R, kGlu>), grid, dim3(64 * kWideHsWaves), shm, s, a);
   return hipGetLastError();
 }
 
@@ -1536,6 +1605,23 @@ SmallMPlan plan_small_m(int64_t n, int groups, int64_t m) {
   return pl;
 }
 
+hipError_t launch_split_reduce(const float* part, int splits, int64_t m, int64_t n, float* y, int64_t ldy,
+                               hipStream_t s) {
+  const int64_t threads = m * ((n + 3) / 4);
+  const int vec = ((uintptr_t)part % 16 == 0) && (n % 4 == 0) && ((uintptr_t)y % 16 == 0) && (ldy % 4 == 0);
+  const dim3 grid((unsigned)((threads + 255) / 256));
+  switch (splits) {
+    case 2: hipLaunchKernelGGL(split_reduce_kernel<2>, grid, dim3(256), 0, s, part, m, n, y, ldy, vec); break;
+    case 4: hipLaunchKernelGGL(split_reduce_kernel<4>, grid, dim3(256), 0, s, part, m, n, y, ldy, vec); break;
+    case 8: hipLaunchKernelGGL(split_reduce_kernel<8>, grid, dim3(256), 0, s, part, m, n, y, ldy, vec); break;
+    case kMaxSplits:
+      hipLaunchKernelGGL(split_reduce_kernel<kMaxSplits>, grid, dim3(256), 0, s, part, m, n, y, ldy, vec);
+      break;
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
 }  // namespace
 
 int64_t gemm_small_m_workspace_bytes(int64_t n, int64_t k, int64_t m) {
@@ -1580,20 +1666,45 @@ hipError_t launch_gemm_small_m(const PlaneView& w, const uint16_t* x, int64_t m,
   else if (m <= 48) e = launch_cfg<3, kDense, false>(a, (int)m, 1, s, pl.wide_rows, pl.splits, pl.halfstep);
   else e = launch_cfg<4, kDense, false>(a, (int)m, 1, s, pl.wide_rows, pl.splits, pl.halfstep);
   if (e != hipSuccess || pl.splits == 1) return e;
-  const int64_t threads = m * ((w.n + 3) / 4);
-  const int vec = ((uintptr_t)ws % 16 == 0) && (w.n % 4 == 0) && ((uintptr_t)y % 16 == 0) && (ldy % 4 == 0);
-  const dim3 grid((unsigned)((threads + 255) / 256));
-  const float* part = static_cast<const float*>(ws);
-  switch (pl.splits) {
-    case 2: hipLaunchKernelGGL(split_reduce_kernel<2>, grid, dim3(256), 0, s, part, m, w.n, y, ldy, vec); break;
-    case 4: hipLaunchKernelGGL(split_reduce_kernel<4>, grid, dim3(256), 0, s, part, m, w.n, y, ldy, vec); break;
-    case 8: hipLaunchKernelGGL(split_reduce_kernel<8>, grid, dim3(256), 0, s, part, m, w.n, y, ldy, vec); break;
-    case kMaxSplits:
-      hipLaunchKernelGGL(split_reduce_kernel<kMaxSplits>, grid, dim3(256), 0, s, part, m, w.n, y, ldy, vec);
-      break;
-    default: return hipErrorInvalidValue;
+  return launch_split_reduce(static_cast<const float*>(ws), pl.splits, m, w.n, y, ldy, s);
+}
+
+// 65..128 tokens on whole steps: two row tiles per wave (a gate and an up tile),
+// K split over blocks as long as there is a CU for each (at 128 tokens, up to 128,
+// 256 and 512 blocks: 4096 x 14336 42, 31 and 40 us, 14336 x 4096 43, 32 and 39).
+int64_t gemm_mid_splits(int64_t n, int groups) {
+  const int64_t blocks = ((n + 15) / 16 + 2 * kWideHsWaves - 1) / (2 * kWideHsWaves);
+  const int steps = groups / 16;
+  int splits = 1;
+  while (splits < kMaxSplits && blocks * splits * 2 <= 256 && steps >= 2 * splits) splits *= 2;
+  return splits;
+}
+
+int64_t gemm_mid_workspace_bytes(int64_t n, int64_t k, int64_t m) {
+  const int64_t splits = gemm_mid_splits(n, (int)(k / 32));
+  return splits > 1 ? splits * m * n * 4 : 0;
+}
+
+hipError_t launch_gemm_mid(const PlaneView& w, const uint16_t* x, int64_t m, int64_t ldx, float* y, int64_t ldy,
+                           void* ws, hipStream_t s) {
+  KArgs a = base_args(w);
+  a.x = x;
+  a.ldx = ldx;
+  a.y = y;
+  a.ldy = ldy;
+  a.m = (int)m;
+  a.x_rows = m;
+  a.vec_y = ((uintptr_t)y % 16 == 0) && (ldy % 4 == 0);
+  const int splits = (int)gemm_mid_splits(w.n, w.groups);
+  if (splits > 1) {
+    a.y = static_cast<float*>(ws);
+    a.ldy = w.n;
+    a.split_stride = m * w.n;
+    a.vec_y = ((uintptr_t)ws % 16 == 0) && (w.n % 4 == 0);
   }
-  return hipGetLastError();
+  const hipError_t e = m <= 96 ? launch_wide_hs<6, 2>(a, splits, s) : launch_wide_hs<8, 2>(a, splits, s);
+  if (e != hipSuccess || splits == 1) return e;
+  return launch_split_reduce(static_cast<const float*>(ws), splits, m, w.n, y, ldy, s);
 }
 
 namespace {
@@ -1632,9 +1743,8 @@ hipError_t launch_glu_nt(KArgs a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_glu_small_m(const PlaneView& gate_up, const uint16_t* x, int64_t m, int64_t ldx, int32_t act,
-                              uint16_t* h, int64_t ldh, float* pre, int64_t ld_pre, hipStream_t s) {
-  if (gate_up.n == 0) return hipSuccess;
+static KArgs glu_args(const PlaneView& gate_up, const uint16_t* x, int64_t m, int64_t ldx, int32_t act, uint16_t* h,
+                      int64_t ldh, float* pre, int64_t ld_pre) {
   KArgs a = base_args(gate_up);
   a.x = x;
   a.ldx = ldx;
@@ -1646,10 +1756,23 @@ hipError_t launch_glu_small_m(const PlaneView& gate_up, const uint16_t* x, int64
   a.act = act;
   a.pre = pre;
   a.ld_pre = ld_pre;
+  return a;
+}
+
+hipError_t launch_glu_small_m(const PlaneView& gate_up, const uint16_t* x, int64_t m, int64_t ldx, int32_t act,
+                              uint16_t* h, int64_t ldh, float* pre, int64_t ld_pre, hipStream_t s) {
+  if (gate_up.n == 0) return hipSuccess;
+  const KArgs a = glu_args(gate_up, x, m, ldx, act, h, ldh, pre, ld_pre);
   if (m <= 16) return launch_glu_nt<1>(a, s);
   if (m <= 32) return launch_glu_nt<2>(a, s);
   if (m <= 48) return launch_glu_nt<3>(a, s);
   return launch_glu_nt<4>(a, s);
+}
+
+hipError_t launch_glu_mid(const PlaneView& gate_up, const uint16_t* x, int64_t m, int64_t ldx, int32_t act,
+                          uint16_t* h, int64_t ldh, float* pre, int64_t ld_pre, hipStream_t s) {
+  const KArgs a = glu_args(gate_up, x, m, ldx, act, h, ldh, pre, ld_pre);
+  return m <= 96 ? launch_wide_hs<6, 2, true>(a, 1, s) : launch_wide_hs<8, 2, true>(a, 1, s);
 }
 
 hipError_t launch_head2_scores(const PlaneView& w, const uint16_t* x, int64_t m, int64_t ldx, float* y, int64_t ldy,

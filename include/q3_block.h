@@ -38,8 +38,8 @@ typedef enum q3_act { Q3_ACT_SILU = 0, Q3_ACT_GELU_TANH = 1 } q3_act;
 
 /* y[m][n] = x[m][:] . w[n][:], m >= 1: q3_gemm_small_m for up to 64 tokens, and
  * for more the matrix dequantised exactly to bf16 in the workspace, multiplied
- * on the matrix cores with fp32 accumulation (or, where that is faster, 64
- * tokens at a time straight from the packed planes).  x bf16 [m][ldx],
+ * on the matrix cores with fp32 accumulation (or, where that is faster, 64 or
+ * 128 tokens at a time straight from the packed planes).  x bf16 [m][ldx],
  * ldx % 8 == 0, 16-byte aligned, 256 of its rows below 2 GiB; y fp32 [m][ldy];
  * m < 2^31; n and k up to 2^21 here and in what follows.
  * workspace: 256-byte aligned, at least q3_gemm_workspace_bytes(n, k, m) bytes

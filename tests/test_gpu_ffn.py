@@ -96,6 +96,34 @@ def test_gemm_tall_matrix_in_passes(q3, n, m):
     check_product(q3.q3_gemm(w, x), h64(x), w64)
 
 
+@pytest.mark.parametrize("n,k", [(16, 512), (45, 1024), (300, 1536), (1000, 4096), (4100, 2560), (9000, 512)])
+def test_gemm_of_65_to_128_tokens(q3, n, k):
+    # whole steps of K, split over blocks (evenly or not) or not; the last pass of more tokens
+    layer = synth.make_layer(n, k, seed=n)
+    w, w64 = pack_layer(q3, layer), weights(layer)
+    for m in (65, 80, 96, 97, 112, 127, 128, 129, 200):
+        x = tokens(m, k, m, pitch=1)
+        y = torch.full((m, n + 3), 5.0, device="cuda")
+        check_product(q3.q3_gemm(w, x, y=y[:, :n]), h64(x), w64)
+        assert (y[:, n:] == 5).all()
+        need = q3.q3_gemm_workspace_bytes(n, k, m)
+        ws = torch.full((need + 256,), 255, dtype=torch.uint8, device="cuda")
+        assert torch.equal(q3.q3_gemm(w, x, workspace=ws[:need]), q3.q3_gemm(w, x)) and (ws[need:] == 255).all()
+        bad = x.clone()
+        bad[3] = float("nan")
+        got, rows = q3.q3_gemm(w, bad), [i for i in range(m) if i != 3]
+        assert torch.equal(got[rows], q3.q3_gemm(w, x)[rows]) and got[3].isnan().all()
+
+
+@pytest.mark.parametrize("inter,k", [(32, 512), (96, 1024), (160, 2560), (10016, 512)])
+def test_glu_of_65_to_128_tokens(q3, inter, k):
+    w, w64 = glu_case(q3, inter, k, seed=inter)
+    for m in (65, 96, 97, 128, 129, 260):
+        h = torch.full((m, inter + 8), 5.0, dtype=torch.bfloat16, device="cuda")
+        check_glu(q3, w, w64, tokens(m, k, m, pitch=1), "gelu", h=h[:, :inter])
+        assert (h[:, inter:] == 5).all()
+
+
 @pytest.mark.parametrize("inter,m", [(4640, 70), (4640, 128), (4640, 129), (9248, 250), (4704, 70), (4704, 128),
                                      (4704, 129), (9408, 250)])
 def test_glu_tall_matrix_in_passes(q3, inter, m):
