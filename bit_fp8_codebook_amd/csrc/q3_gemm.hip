@@ -539,7 +539,7 @@ constexpr int64_t kSmallM = 64;
 //             160; 57344 x 8192, 384 433 and 576
 //   by 64     11008, 128 34 and 46; 14336, 192 55 and 61, 256 70 and 64; 18432, 256
 //             121 and 88; 28672, 384 141 and 153; 65536, 512 347 and 335
-// and 128 a pass against 64: 28672, 128 40 and 46; 8192 x 8192, 128 30 and 53.
+// and 128 a pass against 64: 28672, 128 40 and 47; 8192 x 8192, 128 30 and 53.
 struct Passes {
   int64_t tokens, most;
 };
