@@ -27,10 +27,12 @@
 //
 // What bounds it: for few rows the chain of some twenty block-wide sums and
 // minima, about 0.5 us each with their two barriers, and the launches (1 x 1000
-// 15 us, 1 x 32000 28 us); for many the hist pass's 64-bit exponential for every
-// entry and its second evaluation where the draw falls (64 x 151936 61 us, of
-// which hist 20, choose 20; 4 copies of the sums against lanes that meet at a
+// 15 us, 1 x 32000 27 us); for many the hist pass's 64-bit exponential for every
+// entry and its second evaluation where the draw falls (64 x 151936 60 us, of
+// which hist 19, choose 19; 4 copies of the sums against lanes that meet at a
 // bin change nothing).  The row is read from memory once, then from cache.
+#include <type_traits>
+
 #include "q3_device.h"
 #include "q3_internal.h"
 
@@ -642,6 +644,25 @@ __device__ void sort_desc(uint64_t* key, int nc) {
   __syncthreads();
 }
 
+// Among the lanes' weights, in lane order, the first whose running sum from
+// `run` on exceeds `want`, or the last with weight; and the sum before it.
+struct Pick {
+  int at;
+  bool hit;
+  uint64_t run;
+};
+__device__ __forceinline__ Pick pick(uint64_t q, uint64_t run, double want) {
+  const uint64_t sum = run + wave_scan(q);
+  const uint64_t hit = __ballot(q && (double)sum > want), any = __ballot(q != 0);
+  Pick p;
+  p.hit = hit != 0;
+  p.at = hit ? __builtin_ctzll(hit) : (any ? 63 - __builtin_clzll(any) : 0);
+  const uint64_t before = sum - q;
+  p.run = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(before >> 32), p.at) << 32 |
+          (uint32_t)__builtin_amdgcn_readlane((int)before, p.at);
+  return p;
+}
+
 // The row's token and logprob, from its border, the listed entries (key, unsorted;
 // more than kCand: not used) and the weight of each chunk's entries in the bins
 // before the border (mass, in LDS; all of it where nothing is cut).  A barrier
@@ -727,31 +748,16 @@ __device__ void choose(const SampleArgs& a, int row, const Settings& s, const Ro
     }
   }
   __syncthreads();
-  uint64_t total = 0;
-  for (int c = 0; c < chunks; ++c) total += mass[c];
   float u = a.u[row];
   if (!(u > 0.f)) u = 0.f;
-  const double want = (double)u * (double)total;
   // The chunk, then the wave's part of it, then the entry whose running sum
-  // exceeds u times the total; for u >= 1 the last one with weight.
-  uint64_t run = 0;
-  int c = 0, last = 0;
-  uint64_t last_run = 0;
-  for (c = 0; c < chunks; ++c) {
-    const uint64_t q = mass[c];
-    if (q && (double)(run + q) > want) break;
-    if (q) {
-      last = c;
-      last_run = run;
-    }
-    run += q;
-  }
-  const bool over = c == chunks;
-  if (over) {
-    c = last;
-    run = last_run;
-  }
-  const Range rc = chunk_range(c, per, a.n);
+  // exceeds u times the total; for u >= 1 the last one with weight.  Every wave
+  // finds them for itself where the values fit its lanes.
+  const uint64_t total = wave_sum(lane < chunks ? (uint64_t)mass[lane] : 0);
+  const double want = (double)u * (double)total;
+  const Pick pc = pick(lane < chunks ? (uint64_t)mass[lane] : 0, 0, want);
+  const bool over = !pc.hit;
+  const Range rc = chunk_range(pc.at, per, a.n);
   const int part_len = ((rc.end - rc.begin + kWaves - 1) / kWaves + 63) & ~63;
   {
     constexpr int kBatch = 10;   // loads ahead of their use
@@ -770,55 +776,53 @@ __device__ void choose(const SampleArgs& a, int row, const Settings& s, const Ro
     if (lane == 0) part[wave] = q;
     __syncthreads();
   }
-  int w = 0;
-  last = 0;
-  last_run = run;
-  for (w = 0; w < kWaves; ++w) {
-    const uint64_t q = part[w];
-    if (!over && q && (double)(run + q) > want) break;
-    if (q) {
-      last = w;
-      last_run = run;
-    }
-    run += q;
-  }
-  if (w == kWaves) {
-    w = last;
-    run = last_run;
-  }
-  const int i0 = rc.begin + w * part_len, i1 = min(rc.end, i0 + part_len);
+  const Pick pw = pick(lane < kWaves ? part[lane] : 0, pc.run, over ? INFINITY : want);
+  const int i0 = rc.begin + pw.at * part_len, i1 = min(rc.end, i0 + part_len);
   int token = -1;
   constexpr int kEach = 4;   // neighbouring entries per thread
-  for (int base = i0; base < i1; base += kEach * kThreads) {
-    const int first = base + kEach * t;
-    float v[kEach];
-    uint64_t q[kEach], own = 0;
+  // kBlock: over the block's threads, else by each wave over its lanes.
+  auto draw = [&](auto block) {
+    constexpr bool kBlock = decltype(block)::value;
+    constexpr int kWide = kBlock ? kThreads : 64;
+    const int id = kBlock ? t : lane;
+    uint64_t run = pw.run;
+    for (int base = i0; base < i1; base += kEach * kWide) {
+      const int first = base + kEach * id;
+      float v[kEach];
+      uint64_t q[kEach], own = 0;
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) v[e] = first + e < i1 ? l[first + e] : -INFINITY;
+      for (int e = 0; e < kEach; ++e) v[e] = first + e < i1 ? l[first + e] : -INFINITY;
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-      q[e] = kept(v[e], first + e, b, cut) ? weight(v[e], mx, s.inv_t2) : 0;
-      own += q[e];
-    }
-    uint64_t sum = run + block_scan(own, part);
-    if (t == kThreads - 1) part[kWaves] = sum;   // read behind the barriers below
-    sum -= own;
-    int hit = 0x7FFFFFFF, far = -1;   // the first whose running sum exceeds it, the last with weight
+      for (int e = 0; e < kEach; ++e) {
+        q[e] = kept(v[e], first + e, b, cut) ? weight(v[e], mx, s.inv_t2) : 0;
+        own += q[e];
+      }
+      uint64_t sum = run + (kBlock ? block_scan(own, part) : wave_scan(own));
+      if constexpr (kBlock) {
+        if (t == kThreads - 1) part[kWaves] = sum;   // read behind the barriers below
+      } else {
+        run = last_lane(sum);
+      }
+      sum -= own;
+      int hit = 0x7FFFFFFF, far = -1;   // the first whose running sum exceeds it, the last with weight
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-      sum += q[e];
-      if (q[e] && !over && hit == 0x7FFFFFFF && (double)sum > want) hit = first + e;
-      if (q[e]) far = first + e;
+      for (int e = 0; e < kEach; ++e) {
+        sum += q[e];
+        if (q[e] && !over && hit == 0x7FFFFFFF && (double)sum > want) hit = first + e;
+        if (q[e]) far = first + e;
+      }
+      hit = kBlock ? block_min(hit, ipart) : wave_min(hit);
+      if (hit != 0x7FFFFFFF) {
+        token = hit;
+        break;
+      }
+      far = kBlock ? -block_min(-far, ipart) : -wave_min(-far);
+      token = far >= 0 ? far : token;
+      if constexpr (kBlock) run = part[kWaves];
     }
-    hit = block_min(hit, ipart);
-    if (hit != 0x7FFFFFFF) {
-      token = hit;
-      break;
-    }
-    far = -block_min(-far, ipart);
-    token = far >= 0 ? far : token;
-    run = part[kWaves];
-  }
+  };
+  if (part_len <= 2 * kEach * 64) draw(std::false_type{});
+  else draw(std::true_type{});
   if (t == 0) {
     a.tokens[row] = token;
     if (a.logprobs && token < 0) {   // only if the logits changed under the call
