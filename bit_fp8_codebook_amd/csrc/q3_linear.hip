@@ -103,7 +103,6 @@ struct KArgs {
   int sk;         // K split over the waves of a block (full-K mode)
   const int32_t* ids;
   int pairs_total, topk, x_by_slot;
-  uint32_t x_lds;  // LDS bytes of a token's row staged whole: whole steps and kRowPad
   int slice_cap;   // expert passes in full-K mode: token rows the LDS staging holds (<= 16, even)
   int num_experts;
   // kSwiGLU: tiles in the gate half; output terms h[2*pair + term][I]
@@ -557,33 +556,42 @@ void linear_kernel(KArgs a) {
     };
     // Lane addresses of token slots at the step's start in a row-per-token x
     // layout of the given row stride, for buffer base `base` (absent tokens of
-    // matrix-core mode go to `zero`, a 1 KB zero block, and stay there).
-    auto run = [&](const StepData<R, kWd>& d, uint32_t base, uint32_t rstride, uint32_t zero, uint32_t adv) {
+    // matrix-core mode go to `zero`, a 1 KB zero block, and stay there).  Lanes
+    // with no groups in the step (`here` false: past a partial last step's quads)
+    // have the next token's row in that place, whose infinities and NaN must not
+    // meet their zero weights: on the vector ALUs, where the block holds exactly
+    // NT tokens, they sit the step out; in matrix-core mode they read the zero
+    // block.  (Rows staged up to a whole step instead take up to 768 bytes more of
+    // LDS a token where K ends inside one: 4096 x 4864 at 14 tokens 7.5 -> 10.5 us,
+    // streamed; 8192 x 544 at 32 4.7 -> 5.5, two blocks a CU instead of three.)
+    auto run = [&](const StepData<R, kWd>& d, uint32_t base, uint32_t rstride, uint32_t zero, uint32_t adv,
+                   bool here) {
       if constexpr (kDot) {
-        uint32_t xa[NT];
+        if (here) {
+          uint32_t xa[NT];
+          const uint32_t at = base + adv + 256u * kb;
 #pragma unroll
-        for (int m = 0; m < NT; ++m) xa[m] = (m < cnt ? base + m * rstride + adv : zero) + 256u * kb;
-        dot_step<NT, R>(d, rt, xa, lds, dacc);
+          for (int m = 0; m < NT; ++m) xa[m] = at + m * rstride;
+          dot_step<NT, R>(d, rt, xa, lds, dacc);
+        }
       } else {
         uint32_t xb[NT];
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
           const int j = 16 * c + i;
-          xb[c] = (j < cnt ? base + j * rstride + adv : zero) + 256u * kb;
+          xb[c] = (here && j < cnt ? base + j * rstride + adv : zero) + 256u * kb;
         }
         mfma_step<NT, R>(d, rt, xb, lds, acc);
       }
     };
 
     if constexpr (kMode == kShared) {
-      // Stage all activations: row j holds token j's K values and zeros up to a
-      // whole number of steps (lanes past a partial last step's quads read there
-      // with zero weights, which another token's infinities and NaN must not
-      // meet); a 1 KB zero block follows.  The
+      // Stage all activations: row j holds token j's K values (zero past K up to
+      // whole quads, and in the row's pad); a 1 KB zero block follows.  The
       // first batch of activation loads goes out before the weight loads:
       // loads complete in issue order, so activations queued behind a step of
       // weights would hold up every wave of the block at the barrier below.
-      const uint32_t rstride = a.x_lds;
+      const uint32_t rstride = gp * 64u + kRowPad;
       const uint32_t zero_base = (uint32_t)cnt * rstride;
       const int cpr = (int)(rstride / 16);
       const int nchunk = cnt * cpr + 64;   // rows are contiguous, then the zero block
@@ -617,12 +625,12 @@ void linear_kernel(KArgs a) {
       for (int s = s0; s < s1; s += 2) {
         load_step(p, rt, last_ok, s + 1, s1, B);
         __builtin_amdgcn_sched_barrier(0);
-        run(A, 0u, rstride, zero_base, 1024u * s);
+        run(A, 0u, rstride, zero_base, 1024u * s, s < p.full_steps || last_ok);
         __builtin_amdgcn_sched_barrier(0);
         if (s + 1 >= s1) break;
         load_step(p, rt, last_ok, s + 2, s1, A);
         __builtin_amdgcn_sched_barrier(0);
-        run(B, 0u, rstride, zero_base, 1024u * (s + 1));
+        run(B, 0u, rstride, zero_base, 1024u * (s + 1), s + 1 < p.full_steps || last_ok);
         __builtin_amdgcn_sched_barrier(0);
       }
     } else {
@@ -669,7 +677,7 @@ void linear_kernel(KArgs a) {
         fetch(s + 1, xr);
         load_step(p, rt, last_ok, s + 1, s1, B);
         __builtin_amdgcn_sched_barrier(0);
-        run(A, 0u, rstride, zero_base, 0u);
+        run(A, 0u, rstride, zero_base, 0u, true);
         __builtin_amdgcn_sched_barrier(0);
         put(1, xr);   // buffer 1 was last read at step s-1
         __syncthreads();
@@ -677,7 +685,7 @@ void linear_kernel(KArgs a) {
         fetch(s + 2, xr);
         load_step(p, rt, last_ok, s + 2, s1, A);
         __builtin_amdgcn_sched_barrier(0);
-        run(B, buf_bytes, rstride, zero_base, 0u);
+        run(B, buf_bytes, rstride, zero_base, 0u, true);
         __builtin_amdgcn_sched_barrier(0);
         put(0, xr);
         __syncthreads();
@@ -1282,10 +1290,9 @@ void wide_hs_kernel(KArgs a) {
 
 // ---- host side ------------------------------------------------------------------
 
-uint32_t staged_row_bytes(int groups) { return (uint32_t)((groups + 15) / 16) * 1024u + kRowPad; }
-
 size_t full_k_bytes(int tokens, int groups) {
-  return (size_t)tokens * staged_row_bytes(groups) + 1024;
+  const size_t gp = (size_t)((groups + 3) & ~3);
+  return (size_t)tokens * (gp * 64 + kRowPad) + 1024;
 }
 
 size_t stream_bytes(int slice) { return 2u * slice * (1024u + kRowPad) + 1024u; }
@@ -1530,7 +1537,6 @@ KArgs base_args(const PlaneView& w) {
   a.cb = w.cb;
   a.n = w.n;
   a.G = w.groups;
-  a.x_lds = staged_row_bytes(w.groups);
   return a;
 }
 
