@@ -397,13 +397,28 @@ hipError_t pick(int32_t r_type, bool vec, int n, F&& f) {
 
 }  // namespace
 
+// A launch takes less than 2^32 threads: 2^26 - 4 rows of up to 512 columns, 2^22 - 1
+// of more than 4096.  More rows go in several.
 hipError_t launch_residual_norm(const NormArgs& a, int32_t r_type, bool vec, hipStream_t s) {
   return pick<false>(r_type, vec, a.n, [&](auto e, auto v, auto t, auto el) {
+    using E = decltype(e);
     constexpr int T = decltype(t)::value;
-    const unsigned blocks = (unsigned)((a.m + rows_per_block<T>() - 1) / rows_per_block<T>());
-    hipLaunchKernelGGL((residual_norm_kernel<decltype(e), decltype(v)::value, T, decltype(el)::value>), dim3(blocks),
-                       dim3(block_threads<T>()), 0, s, a);
-    return hipGetLastError();
+    constexpr int64_t most = 0xFFFFFFFFll / block_threads<T>() * rows_per_block<T>();
+    for (int64_t at = 0; at < a.m; at += most) {
+      NormArgs b = a;
+      b.m = a.m - at < most ? a.m - at : most;
+      if (b.y) b.y += at * a.ldy;
+      if (b.gate) b.gate += at * a.ld_gate;
+      b.r = static_cast<const E*>(a.r) + at * a.ldr;
+      if (b.r_out) b.r_out = static_cast<E*>(a.r_out) + at * a.ldr_out;
+      if (b.x) b.x += at * a.ldx;
+      const unsigned blocks = (unsigned)((b.m + rows_per_block<T>() - 1) / rows_per_block<T>());
+      hipLaunchKernelGGL((residual_norm_kernel<E, decltype(v)::value, T, decltype(el)::value>), dim3(blocks),
+                         dim3(block_threads<T>()), 0, s, b);
+      const hipError_t err = hipGetLastError();
+      if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
   });
 }
 
