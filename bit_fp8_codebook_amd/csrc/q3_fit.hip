@@ -281,8 +281,16 @@ hipError_t launch_fit(const float* w, int64_t ldw, int64_t n, int64_t k, uint8_t
   static LdsAllowance seen;
   const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(fit_kernel<kNarrow>), shm, seen);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(fit_kernel<kNarrow>, dim3((unsigned)n), dim3(kFitThreads), shm, s, w, ldw, k, cb);
-  return hipGetLastError();
+  // A launch takes less than 2^32 threads, 2^24 - 1 rows; more rows go in several.
+  constexpr int64_t most = 0xFFFFFFFFll / kFitThreads;
+  for (int64_t r = 0; r < n; r += most) {
+    const int64_t rows = n - r < most ? n - r : most;
+    hipLaunchKernelGGL(fit_kernel<kNarrow>, dim3((unsigned)rows), dim3(kFitThreads), shm, s, w + r * ldw, ldw, k,
+                       cb + r * 8);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
 }
 
 }  // namespace
