@@ -157,7 +157,8 @@ Q3_API q3_status q3_glu_backward(const float* pre, int64_t ld_pre, const float* 
   if (ld_pre < 2 * inter || ld_dh < inter || ld_dpre < 2 * inter) return Q3_ERR_INVALID_ARG;
   if (ld_pre % 4 || ld_dh % 4 || ld_dpre % 8 || !aligned(pre, 16) || !aligned(dh, 16) || !aligned(dpre, 16))
     return Q3_ERR_MISALIGNED;
-  if (m * (inter / 4) > (int64_t(0x7FFFFFFF) * 256)) return Q3_ERR_UNSUPPORTED_SHAPE;
+  // One thread per four outputs, and a launch takes less than 2^32 (in blocks of 256).
+  if (m * (inter / 4) > int64_t(0xFFFFFF00)) return Q3_ERR_UNSUPPORTED_SHAPE;
   q3_status st = check_device();
   if (st != Q3_OK) return st;
   return from_hip(q3::launch_glu_backward(pre, ld_pre, dh, ld_dh, act, m, inter, dpre, ld_dpre,

@@ -427,7 +427,7 @@ hipError_t launch_gemm_one(GemmArgs g, int splits, hipStream_t s) {
       allow_dynamic_lds(reinterpret_cast<const void*>(gemm_kernel<TM, TN, kEpi>), shm, seen);
   if (e != hipSuccess) return e;
   const int64_t tm = (g.m + BM - 1) / BM, tn = (g.n + kOut - 1) / kOut;
-  if (tm * tn > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (tm * tn > 0xFFFFFF) return hipErrorInvalidValue;   // 2^32 threads; outputs of that size fit no card
   g.tiles_m = (int)tm;
   g.tiles_n = (int)tn;
   hipLaunchKernelGGL((gemm_kernel<TM, TN, kEpi>), dim3((unsigned)(tm * tn), (unsigned)splits),
@@ -727,7 +727,7 @@ hipError_t launch_glu(const PlaneView& gate_up, const uint16_t* x, int64_t m, in
 hipError_t launch_glu_backward(const float* pre, int64_t ld_pre, const float* dh, int64_t ld_dh, int32_t act,
                                int64_t m, int64_t inter, uint16_t* dpre, int64_t ld_dpre, hipStream_t s) {
   const int64_t quads = m * (inter / 4), blocks = (quads + 255) / 256;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (blocks > 0xFFFFFF) return hipErrorInvalidValue;   // 2^32 threads
   if (quads == 0) return hipSuccess;
   hipLaunchKernelGGL(glu_back_kernel, dim3((unsigned)blocks), dim3(256), 0, s, pre, ld_pre, dh, ld_dh, act, quads,
                      inter, dpre, ld_dpre);

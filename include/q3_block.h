@@ -75,7 +75,8 @@ Q3_API q3_status q3_glu(const q3_matrix* gate_up, const uint16_t* x, int64_t m, 
  * dpre[m][I + i] = dh act(g), for pre as q3_glu wrote it and dh fp32 [m][ld_dh]
  * (q3_gemm_backward of the down projection).  dpre bf16 [m][ld_dpre], so that
  * q3_gemm_backward(gate_up, dpre) is the gradient of x.  All rows 16-byte
- * aligned (ld_pre % 4, ld_dh % 4, ld_dpre % 8 == 0), inter % 32 == 0. */
+ * aligned (ld_pre % 4, ld_dh % 4, ld_dpre % 8 == 0), inter % 32 == 0,
+ * m * inter <= 2^34 - 1024 (one launch). */
 Q3_API q3_status q3_glu_backward(const float* pre, int64_t ld_pre, const float* dh, int64_t ld_dh, int32_t act,
                                  int64_t m, int64_t inter, uint16_t* dpre, int64_t ld_dpre, void* stream);
 
