@@ -265,22 +265,33 @@ def _norm_args(r, pre_weight, y, post_weight, gate):
     return m, n, dev, ld_gate
 
 
+def _next_x(x, want_x, weight, weight_name, r):
+    """The bfloat16 output x as given or new, or None where it is not wanted."""
+    if not want_x:
+        if x is not None or weight is not None:
+            raise ValueError(f"want_x=False takes neither x nor {weight_name}")
+        return None
+    shape = r.shape
+    return r.new_empty(shape, dtype=torch.bfloat16) if x is None else _rows(x, shape, torch.bfloat16, r.device, "x")
+
+
 def q3_residual_norm(r: torch.Tensor, pre_weight: torch.Tensor = None, y: torch.Tensor = None,
                      post_weight: torch.Tensor = None, gate: torch.Tensor = None, scale: float = 1.0,
-                     eps: float = 1e-6, r_out: torch.Tensor = None, x: torch.Tensor = None):
+                     eps: float = 1e-6, r_out: torch.Tensor = None, x: torch.Tensor = None, want_x: bool = True):
     """r' = r + scale * gate * norm(y; post_weight) and x = norm(r'; pre_weight)
-    -> (r', x): r' in r's type, x bfloat16.  y None: r' is r itself.  post_weight
-    None: y is not normed.  gate float32 [m][n], or [n] for all tokens.  r_out may
-    be r."""
+    -> (r', x): r' in r's type, x bfloat16 (None, and not computed, with want_x
+    False).  y None: r' is r itself.  post_weight None: y is not normed.  gate
+    float32 [m][n], or [n] for all tokens.  r_out may be r."""
     m, n, dev, ld_gate = _norm_args(r, pre_weight, y, post_weight, gate)
     if r_out is not None:
         _rows(r_out, (m, n), r.dtype, dev, "r_out")
     elif y is not None:
         r_out = r.new_empty((m, n))
-    x = r.new_empty((m, n), dtype=torch.bfloat16) if x is None else _rows(x, (m, n), torch.bfloat16, dev, "x")
+    x = _next_x(x, want_x, pre_weight, "pre_weight", r)
+    if x is None and r_out is None:
+        raise ValueError("want_x=False without y or r_out: nothing to compute")
     _call("q3_residual_norm", dev, _ptr(y), _pitch(y), _ptr(post_weight), _ptr(gate), ld_gate, scale, r.data_ptr(),
-          _pitch(r), _ptr(r_out), _pitch(r_out), _R_TYPES[r.dtype], _ptr(pre_weight), x.data_ptr(), _pitch(x), eps, m,
-          n)
+          _pitch(r), _ptr(r_out), _pitch(r_out), _R_TYPES[r.dtype], _ptr(pre_weight), _ptr(x), _pitch(x), eps, m, n)
     return (r if r_out is None else r_out), x
 
 
@@ -335,10 +346,11 @@ def q3_ffn_workspace_bytes(n_gu: int, k: int, m: int) -> int:
 def q3_ffn(gate_up: PackedMatrix, down: PackedMatrix, r: torch.Tensor, pre_weight: torch.Tensor = None,
            post_weight: torch.Tensor = None, gate: torch.Tensor = None, scale: float = 1.0,
            next_weight: torch.Tensor = None, act: str = "silu", eps: float = 1e-6, r_out: torch.Tensor = None,
-           x: torch.Tensor = None, workspace: torch.Tensor = None):
+           x: torch.Tensor = None, workspace: torch.Tensor = None, want_x: bool = True):
     """r' = r + scale * gate * norm(down . h; post_weight), h the gated block of
     norm(r; pre_weight), and x = norm(r'; next_weight) -> (r', x), as the separate
-    calls give them.  r_out may be r."""
+    calls give them; with want_x False x is None and not computed.  r_out may be r.
+    For inference: neither h's pre-activations nor the down product are kept."""
     code = _act(act)
     # y, the down product, is the call's own: r's shape stands for it in the checks
     m, n, dev, _ = _norm_args(r, pre_weight, None, None, None)
@@ -351,11 +363,11 @@ def q3_ffn(gate_up: PackedMatrix, down: PackedMatrix, r: torch.Tensor, pre_weigh
         _rows(gate, (n,) if gate.dim() == 1 else (m, n), torch.float32, dev, "gate")
         ld_gate = _pitch(gate) if gate.dim() == 2 else 0
     r_out = r.new_empty((m, n)) if r_out is None else _rows(r_out, (m, n), r.dtype, dev, "r_out")
-    x = r.new_empty((m, n), dtype=torch.bfloat16) if x is None else _rows(x, (m, n), torch.bfloat16, dev, "x")
+    x = _next_x(x, want_x, next_weight, "next_weight", r)
     ws = _ws(workspace, lib().q3_ffn_workspace_bytes(gate_up.n, n, m), dev)
     norms = Q3FfnNorms(_ptr(pre_weight), _ptr(post_weight), _ptr(next_weight), _ptr(gate), ld_gate, scale, eps)
     _call("q3_ffn", dev, _matrix(gate_up, dev), _matrix(down, dev), code, ctypes.byref(norms), r.data_ptr(), _pitch(r),
-          r_out.data_ptr(), _pitch(r_out), _R_TYPES[r.dtype], x.data_ptr(), _pitch(x), m, *_ws_args(ws))
+          r_out.data_ptr(), _pitch(r_out), _R_TYPES[r.dtype], _ptr(x), _pitch(x), m, *_ws_args(ws))
     return r_out, x
 
 
