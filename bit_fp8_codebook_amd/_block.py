@@ -5,6 +5,10 @@ many tokens, the gated feed-forward block, residual norms (each with the
 gradients of its inputs) and sampling.  Every function forwards to the C entry
 point of the same name; outputs and workspaces that are not given are allocated
 here.  A call runs on the current stream of its tensors' device.
+
+No call is recorded by autograd: results carry no graph, also where an input
+requires a gradient.  The backward calls give the gradients and are chained by
+hand (or in the backward of a torch.autograd.Function).
 """
 from __future__ import annotations
 
@@ -168,7 +172,8 @@ def q3_gemm_workspace_bytes(n: int, k: int, m: int) -> int:
 
 
 def q3_gemm(w: PackedMatrix, x: torch.Tensor, y: torch.Tensor = None, workspace: torch.Tensor = None) -> torch.Tensor:
-    """y[m][n] = x[m] . w[n] for any number of tokens (x bfloat16, y float32)."""
+    """y[m][n] = x[m] . w[n] for any number of tokens (x bfloat16, y float32).
+    Not recorded by autograd: q3_gemm_backward gives x's gradient."""
     _tokens(x, w.k, "x")
     m, dev = x.shape[0], x.device
     y = torch.empty((m, w.n), dtype=torch.float32, device=dev) if y is None else \
@@ -206,7 +211,8 @@ def q3_glu(gate_up: PackedMatrix, x: torch.Tensor, act: str = "silu", save_pre: 
            pre: torch.Tensor = None, workspace: torch.Tensor = None):
     """h = act(x . gate) * (x . up) in bfloat16 [m][I] for gate_up = [gate I rows;
     up I rows]; with save_pre (or pre given) -> (h, pre), the pre-activations
-    [g; u] float32 [m][2I] that q3_glu_backward takes."""
+    [g; u] float32 [m][2I] that q3_glu_backward takes.  Not recorded by autograd:
+    q3_glu_backward, then q3_gemm_backward give x's gradient."""
     _tokens(x, gate_up.k, "x")
     code = _act(act)
     m, dev, inter = x.shape[0], x.device, gate_up.n // 2
@@ -281,7 +287,8 @@ def q3_residual_norm(r: torch.Tensor, pre_weight: torch.Tensor = None, y: torch.
     """r' = r + scale * gate * norm(y; post_weight) and x = norm(r'; pre_weight)
     -> (r', x): r' in r's type, x bfloat16 (None, and not computed, with want_x
     False).  y None: r' is r itself.  post_weight None: y is not normed.  gate
-    float32 [m][n], or [n] for all tokens.  r_out may be r."""
+    float32 [m][n], or [n] for all tokens.  r_out may be r.  Not recorded by
+    autograd: q3_residual_norm_backward gives the gradients."""
     m, n, dev, ld_gate = _norm_args(r, pre_weight, y, post_weight, gate)
     if r_out is not None:
         _rows(r_out, (m, n), r.dtype, dev, "r_out")
@@ -350,7 +357,8 @@ def q3_ffn(gate_up: PackedMatrix, down: PackedMatrix, r: torch.Tensor, pre_weigh
     """r' = r + scale * gate * norm(down . h; post_weight), h the gated block of
     norm(r; pre_weight), and x = norm(r'; next_weight) -> (r', x), as the separate
     calls give them; with want_x False x is None and not computed.  r_out may be r.
-    For inference: neither h's pre-activations nor the down product are kept."""
+    For inference: neither h's pre-activations nor the down product are kept, and
+    the call is not recorded by autograd; training takes the separate calls."""
     code = _act(act)
     # y, the down product, is the call's own: r's shape stands for it in the checks
     m, n, dev, _ = _norm_args(r, pre_weight, None, None, None)
