@@ -9,7 +9,8 @@ namespace q3 {
 
 // Both activations have the form z / (1 + e^-v): silu with v = z, the tanh form
 // of GELU with v = 2 sqrt(2/pi) (z + 0.044715 z^3), since 1/2 (1 + tanh(v/2)) =
-// 1 / (1 + e^-v).  No cancellation for negative z; v = -inf gives -0.
+// 1 / (1 + e^-v).  No cancellation for negative z; a finite z far enough out for
+// e^-v to overflow gives -0 (z = -inf itself is NaN, as z times 0 is).
 constexpr float kGelu2 = 1.5957691216057308f;   // 2 sqrt(2/pi)
 constexpr float kGelu3 = 0.044715f;
 

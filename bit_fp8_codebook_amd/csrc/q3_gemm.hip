@@ -7,11 +7,11 @@
 //
 // Few tokens are bound by the packed weights and their dequantisation, and
 // q3_linear.hip's kernels read them once for up to 64 or 128 tokens.  Many are
-// bound by the matrix cores, and
-// dequantising inside the product would repeat the vector work for every block
-// of tokens; so the matrix is widened once, exactly, to bf16 in the caller's
-// workspace (for the gradient: transposed) and all three run on one kernel:
-// C = A B^T with both operands bf16 and contiguous along the summed axis.
+// bound by the matrix cores, and dequantising inside the product would repeat the
+// vector work for every block of tokens; so the matrix is widened once, exactly, to
+// bf16 in the caller's workspace (for the gradient: transposed) and all three run
+// on one kernel: C = A B^T with both operands bf16 and contiguous along the summed
+// axis.
 #include <type_traits>
 
 #include "q3_act.h"

@@ -190,13 +190,14 @@ hipError_t launch_glu(const PlaneView& gate_up, const uint16_t* x, int64_t m, in
                       int64_t ldh, float* pre, int64_t ld_pre, void* ws, hipStream_t s);
 hipError_t launch_glu_backward(const float* pre, int64_t ld_pre, const float* dh, int64_t ld_dh, int32_t act,
                                int64_t m, int64_t inter, uint16_t* dpre, int64_t ld_dpre, hipStream_t s);
-// The dense gated product of up to 64 tokens, straight from the packed planes (q3_linear.hip).
-// 65..128 tokens on whole 512-k steps (groups % 16 == 0), straight from the planes.
+// Straight from the packed planes (q3_linear.hip): 65..128 tokens on whole 512-k
+// steps (groups % 16 == 0), plain and gated.
 int64_t gemm_mid_workspace_bytes(int64_t n, int64_t k, int64_t m);
 hipError_t launch_gemm_mid(const PlaneView& w, const uint16_t* x, int64_t m, int64_t ldx, float* y, int64_t ldy,
                            void* ws, hipStream_t s);
 hipError_t launch_glu_mid(const PlaneView& gate_up, const uint16_t* x, int64_t m, int64_t ldx, int32_t act,
                           uint16_t* h, int64_t ldh, float* pre, int64_t ld_pre, hipStream_t s);
+// The gated product of up to 64 tokens.
 hipError_t launch_glu_small_m(const PlaneView& gate_up, const uint16_t* x, int64_t m, int64_t ldx, int32_t act,
                               uint16_t* h, int64_t ldh, float* pre, int64_t ld_pre, hipStream_t s);
 

@@ -1025,10 +1025,8 @@ struct RowCb {
 constexpr uint32_t kHalfTokenBytes = 512;   // one token's activations of one half-step
 constexpr int kKeepPolicy = 1;               // work-group scope (sc0), no non-temporal hint
 
-// Chunk CH = 4 tt + e of a half-step: B operands of the NT column tiles, then
-// the chunk's dequantisation and 4 MFMAs for each row tile.  xrow: the lane's
-// token row in the buffer plus 16 * ((8 kb) ^ (i & 8)); i7 = i & 7.
-// The column tiles' B operands of chunk CH.
+// The column tiles' B operands of chunk CH = 4 tt + e of a half-step.  xrow: the
+// lane's token row in the buffer plus 16 * ((8 kb) ^ (i & 8)); i7 = i & 7.
 template <int NT>
 __device__ __forceinline__ void wide_hs_read(bf16x8 (&b)[NT], int ch, uint32_t xrow, uint32_t i7, const uint8_t* lds) {
   const uint32_t xa = xrow + 16u * ((uint32_t)ch ^ i7);
@@ -1037,17 +1035,16 @@ __device__ __forceinline__ void wide_hs_read(bf16x8 (&b)[NT], int ch, uint32_t x
     b[c] = *reinterpret_cast<const bf16x8*>(lds + xa + (uint32_t)c * 16u * kHalfTokenBytes);
 }
 
-// The wave's weights of chunk CH.
+// Row tile r's weights of chunk CH.
 template <int R, int CH>
-__device__ __forceinline__ void wide_hs_weights(bf16x8 (&w)[R], const HalfStep<R>& d, const RowCb (&cb)[R]) {
+__device__ __forceinline__ bf16x8 wide_hs_weight(const HalfStep<R>& d, const RowCb (&cb)[R], int r) {
   constexpr int tt = CH / 4, e = CH % 4;
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const float sc = e8m0_to_f32((d.sc[r] >> (8 * tt)) & 0xFFu);
-    w[r] = dequant_chunk<e>(d.w[r][0][tt], d.w[r][1][tt], d.w[r][2][tt], sc, cb[r].lo, cb[r].hi);
-  }
+  const float sc = e8m0_to_f32((d.sc[r] >> (8 * tt)) & 0xFFu);
+  return dequant_chunk<e>(d.w[r][0][tt], d.w[r][1][tt], d.w[r][2][tt], sc, cb[r].lo, cb[r].hi);
 }
 
+// Chunk CH: its B operands, then the dequantisation and the MFMAs of one row tile
+// after the other.
 template <int NT, int R, int kLoads, int CH, typename Issue>
 __device__ __forceinline__ void wide_hs_chunk(const HalfStep<R>& d, const RowCb (&cb)[R], uint32_t xrow, uint32_t i7,
                                             const uint8_t* lds, f32x4 (&acc)[R][NT], Issue& issue) {
@@ -1061,11 +1058,9 @@ __device__ __forceinline__ void wide_hs_chunk(const HalfStep<R>& d, const RowCb 
     __builtin_amdgcn_sched_barrier(0);
     bf16x8 b[NT];
     wide_hs_read<NT>(b, CH, xrow, i7, lds);
-    constexpr int tt = CH / 4, e = CH % 4;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const float sc = e8m0_to_f32((d.sc[r] >> (8 * tt)) & 0xFFu);
-      const bf16x8 a = dequant_chunk<e>(d.w[r][0][tt], d.w[r][1][tt], d.w[r][2][tt], sc, cb[r].lo, cb[r].hi);
+      const bf16x8 a = wide_hs_weight<R, CH>(d, cb, r);
 #pragma unroll
       for (int c = 0; c < NT; ++c) acc[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[c], acc[r][c], 0, 0, 0);
     }
@@ -1090,7 +1085,8 @@ __device__ __forceinline__ void wide_hs_ahead(const HalfStep<R>& d, const RowCb 
     if constexpr (CH < 7) {
       wide_hs_read<NT>(bn, CH + 1, xrow, i7, lds);
       __builtin_amdgcn_sched_barrier(0);
-      wide_hs_weights<R, CH + 1>(wn, d, cb);
+#pragma unroll
+      for (int r = 0; r < R; ++r) wn[r] = wide_hs_weight<R, CH + 1>(d, cb, r);
     }
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -1113,7 +1109,8 @@ __device__ __forceinline__ void wide_hs_half(const HalfStep<R>& d, const RowCb (
   if constexpr (NT > 4) {
     bf16x8 b[NT], w[R];
     wide_hs_read<NT>(b, 0, xrow, i7, lds);
-    wide_hs_weights<R, 0>(w, d, cb);
+#pragma unroll
+    for (int r = 0; r < R; ++r) w[r] = wide_hs_weight<R, 0>(d, cb, r);
     wide_hs_ahead<NT, R, kLoads, 0>(d, cb, xrow, i7, lds, acc, b, w, issue);
   } else {
     wide_hs_chunk<NT, R, kLoads, 0>(d, cb, xrow, i7, lds, acc, issue);
@@ -1125,7 +1122,6 @@ __device__ __forceinline__ void wide_hs_half(const HalfStep<R>& d, const RowCb (
 }
 
 constexpr int kWideHsWaves = 4;
-
 
 size_t wide_hs_bytes(int slice) { return 2u * (size_t)slice * kHalfTokenBytes; }
 
