@@ -272,13 +272,12 @@ def _norm_args(r, pre_weight, y, post_weight, gate):
 
 
 def _next_x(x, want_x, weight, weight_name, r):
-    """The bfloat16 output x as given or new, or None where it is not wanted."""
-    if not want_x:
-        if x is not None or weight is not None:
-            raise ValueError(f"want_x=False takes neither x nor {weight_name}")
-        return None
-    shape = r.shape
-    return r.new_empty(shape, dtype=torch.bfloat16) if x is None else _rows(x, shape, torch.bfloat16, r.device, "x")
+    """The caller's bfloat16 output x, or None where it is not wanted."""
+    if want_x:
+        return _rows(x, r.shape, torch.bfloat16, r.device, "x")
+    if x is not None or weight is not None:
+        raise ValueError(f"want_x=False takes neither x nor {weight_name}")
+    return None
 
 
 def q3_residual_norm(r: torch.Tensor, pre_weight: torch.Tensor = None, y: torch.Tensor = None,
@@ -294,7 +293,10 @@ def q3_residual_norm(r: torch.Tensor, pre_weight: torch.Tensor = None, y: torch.
         _rows(r_out, (m, n), r.dtype, dev, "r_out")
     elif y is not None:
         r_out = r.new_empty((m, n))
-    x = _next_x(x, want_x, pre_weight, "pre_weight", r)
+    if want_x and x is None:
+        x = r.new_empty((m, n), dtype=torch.bfloat16)
+    else:
+        x = _next_x(x, want_x, pre_weight, "pre_weight", r)
     if x is None and r_out is None:
         raise ValueError("want_x=False without y or r_out: nothing to compute")
     _call("q3_residual_norm", dev, _ptr(y), _pitch(y), _ptr(post_weight), _ptr(gate), ld_gate, scale, r.data_ptr(),
@@ -371,7 +373,10 @@ def q3_ffn(gate_up: PackedMatrix, down: PackedMatrix, r: torch.Tensor, pre_weigh
         _rows(gate, (n,) if gate.dim() == 1 else (m, n), torch.float32, dev, "gate")
         ld_gate = _pitch(gate) if gate.dim() == 2 else 0
     r_out = r.new_empty((m, n)) if r_out is None else _rows(r_out, (m, n), r.dtype, dev, "r_out")
-    x = _next_x(x, want_x, next_weight, "next_weight", r)
+    if want_x and x is None:
+        x = r.new_empty((m, n), dtype=torch.bfloat16)
+    else:
+        x = _next_x(x, want_x, next_weight, "next_weight", r)
     ws = _ws(workspace, lib().q3_ffn_workspace_bytes(gate_up.n, n, m), dev)
     norms = Q3FfnNorms(_ptr(pre_weight), _ptr(post_weight), _ptr(next_weight), _ptr(gate), ld_gate, scale, eps)
     _call("q3_ffn", dev, _matrix(gate_up, dev), _matrix(down, dev), code, ctypes.byref(norms), r.data_ptr(), _pitch(r),
