@@ -16,12 +16,15 @@
 // row belongs to a group of T threads, the smallest of 64..1024 with 8 T >= n;
 // up to 512 columns that is one wave, so a 256-thread block takes four rows and
 // no reduction crosses a wave.  The backward pass sums its weight gradients over
-// tokens in LDS: a fixed number of groups walks the rows, each leaves one partial
-// row per gradient, and a second launch adds those in group order (no atomics, so
-// the same call gives the same bits).  All statistics and sums are fp32.
+// tokens in LDS, or past 12288 columns, where three rows of sums do not fit, in the
+// partial rows themselves: a fixed number of groups walks the rows, each leaves one
+// partial row per gradient, and a second launch adds those in group order (no
+// atomics, so the same call gives the same bits).  All statistics and sums are fp32.
 // Measured: 8192 x 8192 fp32 forward 213 us (5.7 TB/s), backward 379 + 5 us (5.3
 // TB/s); 2047 x 5120 bf16 backward 41 + 6 us, of which the partial rows are a
-// quarter of the bytes; 1 x 4096 forward 2.8 us.
+// quarter of the bytes; 1 x 4096 forward 2.8 us.  4096 rows backward, fp32: 12288
+// columns 192 us (5.8 TB/s), 12292 454, 16384 522 (2.8 TB/s: the sums move with
+// every row).
 #include <type_traits>
 
 #include "q3_device.h"
