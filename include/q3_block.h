@@ -61,8 +61,9 @@ Q3_API q3_status q3_gemm_backward(const q3_matrix* w, const uint16_t* dy, int64_
 /* h[m][i] = act(g) * u with g = x[m] . w[i], u = x[m] . w[I + i], both products,
  * the activation and the product in one kernel (behind a pass that widens the
  * matrix where the workspace is not 0 bytes): gate_up is a packed matrix of
- * n = 2I rows [gate rows 0..I-1; up rows I..2I-1], I % 32 == 0.  x bf16 [m][ldx] as in q3_gemm; h bf16 [m][ldh],
- * ldh >= I, ldh % 8 == 0, 16-byte aligned (so it is the down product's x).
+ * n = 2I rows [gate rows 0..I-1; up rows I..2I-1], I % 32 == 0.
+ * x bf16 [m][ldx] as in q3_gemm; h bf16 [m][ldh], ldh >= I, ldh % 8 == 0,
+ * 16-byte aligned (so it is the down product's x).
  * pre (may be NULL): fp32 [m][ld_pre], the pre-activations [g; u] for the
  * backward pass, ld_pre >= 2I, ld_pre % 4 == 0, 16-byte aligned.
  * workspace: 256-byte aligned, q3_glu_workspace_bytes(2I, k, m) bytes (0
