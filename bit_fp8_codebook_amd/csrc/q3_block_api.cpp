@@ -11,7 +11,6 @@ using namespace q3::check;
 namespace {
 
 constexpr int64_t kMaxK = int64_t(1) << 21;   // rows and columns: 256 widened rows stay below 2 GiB
-constexpr int64_t kMaxM = int64_t(1) << 31;   // exclusive
 
 // A packed matrix and bf16 token rows of `cols` columns in front of it.  A
 // kernel addresses up to 256 rows through one 32-bit buffer resource.
@@ -26,12 +25,6 @@ q3_status check_product(const q3_matrix* w, const uint16_t* x, int64_t m, int64_
   return Q3_OK;
 }
 
-q3_status check_workspace(const void* ws, int64_t bytes, int64_t need) {
-  if (need > 0 && (!ws || bytes < need)) return Q3_ERR_INVALID_ARG;
-  if (!aligned(ws, 256)) return Q3_ERR_MISALIGNED;
-  return Q3_OK;
-}
-
 bool bad_shape(int64_t n, int64_t k, int64_t m) {
   return n < 1 || n > kMaxK || k < 32 || k % 32 || k > kMaxK || m < 1 || m >= kMaxM;
 }
@@ -39,7 +32,6 @@ bool bad_shape(int64_t n, int64_t k, int64_t m) {
 bool bad_act(int32_t act) { return act != Q3_ACT_SILU && act != Q3_ACT_GELU_TANH; }
 
 constexpr int64_t kMaxNorm = 16384;
-int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
 
 // What both directions of the residual norm share.
 q3_status check_norm(const float* y, int64_t ldy, const float* post_weight, const float* gate, int64_t ld_gate,

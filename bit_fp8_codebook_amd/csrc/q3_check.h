@@ -14,6 +14,9 @@ namespace q3::check {
 inline constexpr int64_t kGroup = 32;
 inline constexpr int64_t kMaxPlaneBytes = (int64_t(1) << 31) - (int64_t(1) << 24);   // per plane, and for x
 
+inline constexpr int64_t kMaxM = int64_t(1) << 31;   // token rows, exclusive
+
+inline int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
 inline int64_t padded_groups(int64_t k) { return (k / kGroup + 3) / 4 * 4; }
 inline int64_t tiles_of(int64_t n) { return (n + 15) / 16; }
 inline int64_t code_plane_bytes(int64_t n, int64_t k) { return tiles_of(n) * 192 * padded_groups(k); }
@@ -21,6 +24,12 @@ inline int64_t scale_plane_bytes(int64_t n, int64_t k) { return tiles_of(n) * 16
 inline int64_t code_plane_bytes2(int64_t n, int64_t k) { return tiles_of(n) * 128 * padded_groups(k); }
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+inline q3_status check_workspace(const void* ws, int64_t bytes, int64_t need) {
+  if (need > 0 && (!ws || bytes < need)) return Q3_ERR_INVALID_ARG;
+  if (!aligned(ws, 256)) return Q3_ERR_MISALIGNED;
+  return Q3_OK;
+}
 
 inline q3_status check_shape(int64_t n, int64_t k) {
   if (n < 0) return Q3_ERR_INVALID_ARG;

@@ -201,6 +201,125 @@ hipError_t launch_glu_mid(const PlaneView& gate_up, const uint16_t* x, int64_t m
 hipError_t launch_glu_small_m(const PlaneView& gate_up, const uint16_t* x, int64_t m, int64_t ldx, int32_t act,
                               uint16_t* h, int64_t ldh, float* pre, int64_t ld_pre, hipStream_t s);
 
+// The attention sublayer: a layer's paged cache and the new tokens of a batch, as
+// the kernels take them.
+struct CacheView {
+  uint16_t* k;
+  uint16_t* v;
+  int64_t pages;
+  int64_t page_stride;   // elements
+  int32_t shift;         // log2 of the page size
+  int32_t heads;
+  int32_t d;
+};
+struct BatchView {
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const int32_t* table;
+  int64_t ld_table;
+  int64_t table_pages;
+  int32_t sequences;     // 0: no batch
+};
+
+// Head norms and rotation (q3_rope.hip).
+struct RopeArgs {
+  const float* qkv;
+  int64_t ld;
+  int32_t hq, hk, d, rot, interleaved;
+  float eps;
+  const float* wq;
+  const float* wk;
+  const float* freq;
+  const int32_t* positions;
+  uint16_t* q;
+  int64_t ldq;
+  uint16_t* k;      // rows, or null: the cache
+  int64_t ldk;
+  uint16_t* v;
+  int64_t ldv;
+  CacheView cache;
+  BatchView batch;
+  int64_t m;
+  int64_t first;    // the launch's first row
+};
+hipError_t launch_qk_norm_rope(const RopeArgs& a, hipStream_t s);
+
+struct RopeBackArgs {
+  const float* qkv;
+  int64_t ld;
+  int32_t hq, hk, d, rot, interleaved;
+  float eps;
+  const float* wq;
+  const float* wk;
+  const float* freq;
+  const int32_t* positions;
+  const void* dq;   // null: zero
+  int64_t ld_dq;
+  const void* dk;
+  int64_t ld_dk;
+  const void* dv;
+  int64_t ld_dv;
+  uint16_t* dqkv;
+  int64_t ld_out;
+  float* part;      // [groups][2][d]; null: no weight gradients
+  float* dwq;
+  float* dwk;
+  int64_t m;
+  int64_t groups;
+};
+int64_t rope_back_groups(int64_t m);
+hipError_t launch_qk_norm_rope_back(const RopeBackArgs& a, int32_t d_type, hipStream_t s);
+
+// Attention over a paged cache (q3_attend.hip).
+struct AttendArgs {
+  const uint16_t* q;
+  int64_t ldq;
+  uint16_t* out;
+  int64_t ldo;
+  float* lse;
+  int32_t hq;
+  float scale;
+  int32_t window;   // 0: off
+  CacheView cache;
+  BatchView batch;
+  int64_t m;
+};
+int64_t attend_workspace_bytes(int64_t m, int64_t sequences, int32_t hq, int32_t hk, int32_t d);
+hipError_t launch_attend(const AttendArgs& a, void* ws, hipStream_t s);
+
+// Log probabilities (q3_logprobs.hip).
+constexpr int kMaxTop = 32;
+struct LogprobArgs {
+  const float* logits;
+  int64_t ld;
+  int64_t m;
+  int n;
+  const int32_t* targets;
+  float inv_t;
+  int top;
+  float* logprobs;
+  float* entropy;
+  int32_t* top_ids;
+  float* top_logprobs;
+  float* stats;
+};
+int64_t logprobs_workspace_bytes(int64_t m, int64_t n, int32_t top);
+hipError_t launch_logprobs(const LogprobArgs& a, void* ws, hipStream_t s);
+struct LogprobBackArgs {
+  const float* logits;
+  int64_t ld;
+  int64_t m;
+  int n;
+  const int32_t* targets;
+  float inv_t;
+  const float* stats;
+  const float* dlogprobs;
+  const float* dentropy;
+  void* dlogits;
+  int64_t ld_d;
+};
+hipError_t launch_logprobs_back(const LogprobBackArgs& a, int32_t d_type, hipStream_t s);
+
 // Dynamic LDS above 64 KB must be allowed per kernel on each device.  One
 // LdsAllowance per kernel (a zero-initialised static) remembers, per device,
 // the largest size already allowed, so later launches cost one atomic load.

@@ -1,0 +1,411 @@
+// Log probabilities of given tokens, entropy and top alternatives of rows of
+// logits, and their gradient.
+//
+// With c = 1 / temperature, M = max l, e_j = exp(c (l_j - M)):
+//   S = sum e,  T = sum e c (l - M)
+//   ln p_j = c (l_j - M) - ln S,  H = ln S - T / S
+//   dl_j = c (g ([j == t] - p_j) - h p_j (ln p_j + H))
+//
+// Bound by memory: the forward reads each logit once.  A block holds 8192 of a
+// row's logits in registers at a time and keeps the running M, S and T of every
+// thread (rescaled where M grows).  Differences to M are formed before they are
+// scaled, so large logits lose nothing.  Rows are split over blocks where there
+// are few; a second launch joins the parts in order.
+//
+// Top alternatives: each wave keeps the best `top` entries it has seen, sorted,
+// one per lane.  An entry is one 64-bit key, the logit's order in the high word
+// and the inverted index in the low one, so that a plain comparison ranks and no
+// two are equal.  Of 1024 new entries only those above the list's last matter.
+// Where there are many (the list is still empty), the list's size-th largest of
+// the 64 lanes' maxima is a bound that at least that many entries reach; what
+// passes is packed into lanes, sorted with the list and cut.
+#include "q3_device.h"
+#include "../../include/q3_block.h"
+#include "q3_internal.h"
+
+namespace q3 {
+namespace {
+
+constexpr int kThreads = 512, kWaves = kThreads / 64;
+constexpr int kEach = 16;                     // logits of a thread
+constexpr int kChunk = kThreads * kEach;      // of a block
+constexpr float kLog2e = 1.4426950408889634f;
+
+typedef unsigned long long Key;
+
+__device__ __forceinline__ Key key_of(float l, uint32_t index) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, l + 0.f);   // -0 as 0
+  const uint32_t up = b & 0x80000000u ? ~b : b | 0x80000000u;
+  return (Key)up << 32 | (uint32_t)~index;
+}
+__device__ __forceinline__ float logit_of(Key k) {
+  const uint32_t up = (uint32_t)(k >> 32);
+  return __builtin_bit_cast(float, up & 0x80000000u ? up & 0x7FFFFFFFu : ~up);
+}
+__device__ __forceinline__ Key max_key(Key a, Key b) { return a > b ? a : b; }
+__device__ __forceinline__ Key min_key(Key a, Key b) { return a < b ? a : b; }
+
+// The wave's 64 keys in descending lane order.
+__device__ __forceinline__ Key sort_wave(Key k, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 64; size *= 2) {
+#pragma unroll
+    for (int step = size / 2; step > 0; step /= 2) {
+      const Key o = __shfl_xor(k, step, 64);
+      const bool down = (lane & size) == 0 || size == 64;     // this run descends
+      const bool first = (lane & step) == 0;
+      k = down == first ? max_key(k, o) : min_key(k, o);
+    }
+  }
+  return k;
+}
+// Two descending lists of 32, `k` in lanes 0..31 of each: the best 32 of both,
+// descending, in lanes 0..31.
+__device__ __forceinline__ Key merge_best(Key mine, Key other, int lane) {
+  const Key back = __shfl(other, 31 - (lane & 31), 64);
+  Key k = max_key(mine, back);   // the larger halves of a bitonic sequence
+#pragma unroll
+  for (int step = 16; step > 0; step /= 2) {
+    const Key o = __shfl_xor(k, step, 64);
+    k = (lane & step) == 0 ? max_key(k, o) : min_key(k, o);
+  }
+  return k;
+}
+
+struct Sums {
+  float m, s, t;   // largest logit (raw), sum of weights, sum of weights * c (l - m)
+};
+__device__ __forceinline__ Sums empty_sums() { return {-INFINITY, 0.f, 0.f}; }
+// Sums under a larger maximum.
+__device__ __forceinline__ void rise(Sums& a, float m, float c) {
+  if (!(m > a.m)) return;
+  if (a.m > -INFINITY) {
+    const float d = (a.m - m) * c, f = exp2f(d * kLog2e);
+    a.t = f > 0.f ? f * (a.t + d * a.s) : 0.f;
+    a.s *= f;
+  }
+  a.m = m;
+}
+__device__ __forceinline__ Sums join(Sums a, Sums b, float c) {
+  const float m = fmaxf(a.m, b.m);
+  rise(a, m, c);
+  rise(b, m, c);
+  return {m, a.s + b.s, a.t + b.t};
+}
+__device__ __forceinline__ Sums join_wave(Sums a, float c) {
+#pragma unroll
+  for (int off = 1; off < 64; off *= 2) {
+    const Sums o = {__shfl_xor(a.m, off, 64), __shfl_xor(a.s, off, 64), __shfl_xor(a.t, off, 64)};
+    a = join(a, o, c);
+  }
+  return a;
+}
+
+// What a block found of its part of a row.
+struct Part {
+  float m, s, t, unused;
+};
+
+// Logits j..j+3 of a row of n; those past its end are 0.  `whole`: none is.
+__device__ __forceinline__ f32x4 load4(rsrc_t row, const float* p, int j, int n, bool whole) {
+  if (whole || j + 4 <= n)
+    return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(row, 4u * (uint32_t)j, 0, 0));
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (j + i < n) v[i] = p[j + i];
+  return v;
+}
+
+// The answers of a row from all its logits' sums.
+__device__ __forceinline__ void finish(const LogprobArgs& a, int64_t row, Sums r, float target) {
+  const bool some = r.m > -INFINITY;
+  const float ln = some ? logf(r.s) : 0.f;
+  const float h = some ? ln - r.t / r.s : 0.f;
+  const int t = a.targets[row];
+  float lp = 0.f;
+  if (t >= 0 && t < a.n) {
+    const float d = target == r.m ? 0.f : (target - r.m) * a.inv_t;   // +inf
+    lp = some && target > -INFINITY ? d - ln : -INFINITY;
+  }
+  a.logprobs[row] = lp;
+  if (a.entropy) a.entropy[row] = h;
+  if (a.stats) reinterpret_cast<f32x4*>(a.stats)[row] = f32x4{r.m, ln, h, 0.f};
+}
+// Lane j < top writes place j.
+__device__ __forceinline__ void finish_top(const LogprobArgs& a, int64_t row, Sums r, Key k, int lane) {
+  if (lane >= a.top) return;
+  const float l = logit_of(k), ln = logf(r.s);
+  const float d = l == r.m ? 0.f : (l - r.m) * a.inv_t;
+  a.top_ids[row * a.top + lane] = k ? (int32_t)~(uint32_t)k : -1;
+  a.top_logprobs[row * a.top + lane] = k ? d - ln : -INFINITY;
+}
+
+// Block (part, row): the logits [part * per, (part + 1) * per) of the row, per a
+// multiple of kChunk.
+template <bool kTop>
+__global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a, int per, Part* parts, Key* lists) {
+  __shared__ Sums red[kWaves];
+  __shared__ Key best[kWaves][32];
+  __shared__ Key packed[kWaves][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t row = blockIdx.y;
+  const int from = blockIdx.x * per, to = min(a.n, from + per);
+  const float* logits = a.logits + row * a.ld;
+  const rsrc_t src = make_rsrc(logits, (uint32_t)a.n * 4u);
+  Sums sums = empty_sums();
+  Key list = 0, last = 0;   // the wave's best, descending by lane; the one in place top - 1
+  const float c2 = a.inv_t * kLog2e;
+  for (int at = from; at < to; at += kChunk) {
+    float l[kEach];
+    const int first = at + 4 * (int)threadIdx.x;   // four consecutive ones every 4 * kThreads
+#pragma unroll
+    for (int q = 0; q < kEach / 4; ++q) {
+      const f32x4 v = load4(src, logits, first + q * 4 * kThreads, a.n, at + kChunk <= a.n);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) l[4 * q + i] = v[i];
+    }
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int j = first + (i / 4) * 4 * kThreads + i % 4;
+      if (!(l[i] == l[i]) || j >= to) l[i] = -INFINITY;   // NaN is masked
+      m = fmaxf(m, l[i]);
+    }
+    rise(sums, m, a.inv_t);
+    if (sums.m > -INFINITY) {
+      const float top = sums.m;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const float d = l[i] == top ? 0.f : l[i] - top;   // +inf
+        const float e = exp2f(d * c2);
+        sums.s += e;
+        sums.t += e > 0.f ? e * (d * a.inv_t) : 0.f;
+      }
+    }
+    if constexpr (kTop) {
+      // Entries above the list's last one, by value (an equal one has a higher index).
+      const uint32_t floor_up = (uint32_t)(last >> 32);
+      Key mine = 0;   // the lane's best
+      int above = 0;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int j = first + (i / 4) * 4 * kThreads + i % 4;
+        const Key k = l[i] > -INFINITY ? key_of(l[i], j) : 0;
+        mine = max_key(mine, k);
+        above += (uint32_t)(k >> 32) > floor_up;
+      }
+      if (__ballot(above > 0) == 0) continue;
+      int count = above;
+#pragma unroll
+      for (int off = 1; off < 64; off *= 2) count += __shfl_xor(count, off, 64);
+      Key bound = last;
+      if (count > 32) bound = max_key(bound, __shfl(sort_wave(mine, lane), a.top - 1, 64));
+      // Pack what reaches the bound.
+      int n = 0;
+      bool fits = true;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int j = first + (i / 4) * 4 * kThreads + i % 4;
+        const Key k = l[i] > -INFINITY ? key_of(l[i], j) : 0;
+        const bool in = k >= bound && k > last;
+        const uint64_t who = __ballot(in);
+        const int place = n + __popcll(who & ((1ull << lane) - 1));
+        if (in && place < 64) packed[wave][place] = k;
+        n += __popcll(who);
+      }
+      fits = n <= 32;
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      if (fits) {
+        // The list in lanes 0..31, the new ones behind it.
+        Key k = __shfl(list, lane & 31, 64);
+        if (lane >= 32) k = lane - 32 < n ? packed[wave][lane - 32] : 0;
+        list = sort_wave(k, lane);
+      } else {
+        // Many that reach it: one at a time, best first.  The bound stays below
+        // every entry that belongs to the list, so `top` steps are enough.
+        Key below = ~0ull;   // the last one taken
+        for (int step = 0; step < a.top; ++step) {
+          Key k = 0;
+#pragma unroll
+          for (int i = 0; i < kEach; ++i) {
+            const int j = first + (i / 4) * 4 * kThreads + i % 4;
+            const Key c = l[i] > -INFINITY ? key_of(l[i], j) : 0;
+            if (c < below) k = max_key(k, c);
+          }
+#pragma unroll
+          for (int off = 1; off < 64; off *= 2) k = max_key(k, __shfl_xor(k, off, 64));
+          if (k <= __shfl(list, a.top - 1, 64)) break;
+          const int place = __popcll(__ballot(list > k));
+          const Key up = __shfl_up(list, 1, 64);
+          list = lane < place ? list : lane == place ? k : up;
+          below = k;
+        }
+      }
+      if (lane >= a.top) list = 0;
+      last = __shfl(list, a.top - 1, 64);
+      __builtin_amdgcn_wave_barrier();   // the next chunk packs behind these reads
+    }
+  }
+
+  sums = join_wave(sums, a.inv_t);
+  if (lane == 0) red[wave] = sums;
+  if (kTop && lane < 32) best[wave][lane] = list;
+  __syncthreads();
+  if (wave != 0) return;
+  sums = join_wave(lane < kWaves ? red[lane] : empty_sums(), a.inv_t);
+  if constexpr (kTop) {
+    list = best[0][lane & 31];
+    for (int w = 1; w < kWaves; ++w) list = merge_best(list, best[w][lane & 31], lane);
+  }
+  const int t = a.targets[row];
+  if (!parts) {
+    if (lane == 0) finish(a, row, sums, t >= 0 && t < a.n ? a.logits[row * a.ld + t] : 0.f);
+    if (kTop) finish_top(a, row, sums, list, lane);
+    return;
+  }
+  const int64_t slot = row * gridDim.x + blockIdx.x;
+  if (lane == 0) parts[slot] = {sums.m, sums.s, sums.t, 0.f};
+  if (kTop && lane < a.top) lists[slot * a.top + lane] = list;
+}
+
+// A wave per row joins its parts in order.
+template <bool kTop>
+__global__ __launch_bounds__(256) void logprobs_join_kernel(LogprobArgs a, int count, const Part* parts,
+                                                            const Key* lists) {
+  const int lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (row >= a.m) return;   // whole waves
+  Sums sums = empty_sums();
+  for (int i = lane; i < count; i += 64) {
+    const Part p = parts[row * count + i];
+    sums = join(sums, {p.m, p.s, p.t}, a.inv_t);
+  }
+  sums = join_wave(sums, a.inv_t);
+  const int t = a.targets[row];
+  if (lane == 0) finish(a, row, sums, t >= 0 && t < a.n ? a.logits[row * a.ld + t] : 0.f);
+  if constexpr (kTop) {
+    Key list = 0;
+    for (int i = 0; i < count; ++i) {
+      const int j = lane & 31;
+      list = merge_best(list, j < a.top ? lists[(row * count + i) * a.top + j] : 0, lane);
+    }
+    finish_top(a, row, sums, list, lane);
+  }
+}
+
+// Four consecutive gradients a thread.
+template <typename E>
+__global__ __launch_bounds__(256) void logprobs_back_kernel(LogprobBackArgs a, int vec) {
+  const int64_t row = blockIdx.y;
+  const int j = 4 * (blockIdx.x * 256 + threadIdx.x);
+  if (j >= a.n) return;
+  const f32x4 st = reinterpret_cast<const f32x4*>(a.stats)[row];
+  const int t = a.targets && a.dlogprobs ? a.targets[row] : -1;
+  const float g = t >= 0 && t < a.n ? a.dlogprobs[row] : 0.f;
+  const float h = a.dentropy ? a.dentropy[row] : 0.f;
+  const rsrc_t src = make_rsrc(a.logits + row * a.ld, (uint32_t)a.n * 4u);
+  const f32x4 v = load4(src, a.logits + row * a.ld, j, a.n, false);
+  const bool finite = st.x < INFINITY;   // in a row with +inf only those entries count
+  float o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float l = v[i];
+    const float lp = (l == st.x ? 0.f : (l - st.x) * a.inv_t) - st.y;
+    const float p = l > -INFINITY ? exp2f(lp * kLog2e) : 0.f;
+    const float d = (j + i == t ? g : 0.f) - p * (g + h * (lp + st.z));
+    o[i] = p > 0.f ? a.inv_t * d : finite && j + i == t && l > -INFINITY ? a.inv_t * g : 0.f;
+  }
+  E* to = static_cast<E*>(a.dlogits) + row * a.ld_d + j;
+  if (vec && j + 4 <= a.n) {
+    if constexpr (sizeof(E) == 4) {
+      *reinterpret_cast<f32x4*>(to) = f32x4{o[0], o[1], o[2], o[3]};
+    } else {
+      const bf16x2 x = {static_cast<__bf16>(o[0]), static_cast<__bf16>(o[1])};
+      const bf16x2 y = {static_cast<__bf16>(o[2]), static_cast<__bf16>(o[3])};
+      *reinterpret_cast<u32x2*>(to) = u32x2{__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y)};
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (j + i >= a.n) break;
+      if constexpr (sizeof(E) == 4) to[i] = o[i];
+      else to[i] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(o[i]));
+    }
+  }
+}
+
+// Parts of a row: blocks for the whole chip where rows are few, whole chunks each.
+int parts_of(int64_t m, int64_t n) {
+  const int64_t chunks = (n + kChunk - 1) / kChunk, want = (1024 + m - 1) / m;
+  const int64_t each = (chunks + want - 1) / want;
+  return (int)((chunks + each - 1) / each);
+}
+
+}  // namespace
+
+int64_t logprobs_workspace_bytes(int64_t m, int64_t n, int32_t top) {
+  const int64_t parts = parts_of(m, n);
+  return parts == 1 ? 0 : m * parts * ((int64_t)sizeof(Part) + 8 * top);
+}
+
+hipError_t launch_logprobs(const LogprobArgs& args, void* ws, hipStream_t s) {
+  const int parts = parts_of(args.m, args.n);
+  const int chunks = (args.n + kChunk - 1) / kChunk;
+  const int per = (chunks + parts - 1) / parts * kChunk;
+  Part* p = parts > 1 ? static_cast<Part*>(ws) : nullptr;
+  Key* lists = p ? reinterpret_cast<Key*>(p + args.m * parts) : nullptr;
+  // Rows of one launch: the grid's height (parts is 1 where there are more).
+  constexpr int64_t most = 65535;
+  for (int64_t at = 0; at < args.m; at += most) {
+    LogprobArgs a = args;
+    a.m = args.m - at < most ? args.m - at : most;
+    a.logits += at * args.ld;
+    a.targets += at;
+    a.logprobs += at;
+    if (a.entropy) a.entropy += at;
+    if (a.stats) a.stats += 4 * at;
+    if (a.top) {
+      a.top_ids += at * a.top;
+      a.top_logprobs += at * a.top;
+    }
+    const dim3 grid((unsigned)parts, (unsigned)a.m);
+    if (a.top) hipLaunchKernelGGL(logprobs_kernel<true>, grid, dim3(kThreads), 0, s, a, per, p, lists);
+    else hipLaunchKernelGGL(logprobs_kernel<false>, grid, dim3(kThreads), 0, s, a, per, p, lists);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (!p) return hipSuccess;
+  const dim3 join((unsigned)((args.m + 3) / 4));
+  if (args.top) hipLaunchKernelGGL(logprobs_join_kernel<true>, join, dim3(256), 0, s, args, parts, p, lists);
+  else hipLaunchKernelGGL(logprobs_join_kernel<false>, join, dim3(256), 0, s, args, parts, p, lists);
+  return hipGetLastError();
+}
+
+hipError_t launch_logprobs_back(const LogprobBackArgs& args, int32_t d_type, hipStream_t s) {
+  const int e = d_type == Q3_BF16 ? 2 : 4;
+  const int vec = args.ld_d % 4 == 0 && reinterpret_cast<uintptr_t>(args.dlogits) % (4 * e) == 0;
+  const int64_t blocks = (args.n + 1023) / 1024;
+  // Rows of one launch: the grid's height, and less than 2^32 threads.
+  const int64_t most = 65535 < 0xFFFFFFFFll / (256 * blocks) ? 65535 : 0xFFFFFFFFll / (256 * blocks);
+  for (int64_t at = 0; at < args.m; at += most) {
+    LogprobBackArgs a = args;
+    a.m = args.m - at < most ? args.m - at : most;
+    a.logits += at * args.ld;
+    if (a.targets) a.targets += at;
+    a.stats += 4 * at;
+    if (a.dlogprobs) a.dlogprobs += at;
+    if (a.dentropy) a.dentropy += at;
+    a.dlogits = static_cast<char*>(args.dlogits) + at * args.ld_d * e;
+    const dim3 grid((unsigned)blocks, (unsigned)a.m);
+    if (d_type == Q3_BF16) hipLaunchKernelGGL(logprobs_back_kernel<uint16_t>, grid, dim3(256), 0, s, a, vec);
+    else hipLaunchKernelGGL(logprobs_back_kernel<float>, grid, dim3(256), 0, s, a, vec);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
+}
+
+}  // namespace q3

@@ -3,7 +3,9 @@
  * and behind the last one (MI355X, gfx950): the gated feed-forward block and
  * products of many tokens on packed weights with the gradients of their inputs,
  * the residual norms that turn a product's fp32 outputs into the next product's
- * bf16 activations, and the choice of a token from the vocabulary logits.
+ * bf16 activations, the attention sublayer's norms, rotation and attention over a
+ * paged cache, the choice of a token from the vocabulary logits, and the log
+ * probabilities of given ones with their gradient.
  *
  * The conventions are q3.h's: device pointers, caller-owned buffers, no
  * allocation, asynchronous on `stream`, arguments validated on the host before
@@ -162,6 +164,120 @@ Q3_API q3_status q3_ffn(const q3_matrix* gate_up, const q3_matrix* down, int32_t
                         const void* r, int64_t ldr, void* r_out, int64_t ldr_out, int32_t r_type, uint16_t* x_next,
                         int64_t ldx_next, int64_t m, void* workspace, int64_t workspace_bytes, void* stream);
 
+/* ---- Attention sublayer --------------------------------------------------------- */
+
+/* A layer's keys and values in pages: bf16 [pages][heads][page_size][head_dim],
+ * the pages of each page_stride elements apart.  page_size: a power of two up to
+ * 1024; head_dim: a multiple of 16 up to 256; heads up to 1024; pages >= 1;
+ * page_stride >= heads * page_size * head_dim, % 8 == 0; k and v 16-byte aligned. */
+typedef struct q3_paged_cache {
+  void* k;
+  void* v;
+  int64_t pages;
+  int64_t page_stride;
+  int32_t page_size;
+  int32_t heads;
+  int32_t head_dim;
+} q3_paged_cache;
+
+/* New tokens of several sequences: those of sequence s are rows q_start[s] up to
+ * q_start[s + 1] of a call's m rows, and stand at the end of its kv_len[s]
+ * positions (the new ones included): row i at position
+ * kv_len[s] - (q_start[s + 1] - i).  Position p of sequence s lives in page
+ * page_table[s][p / page_size].  All three are device memory, int32; q_start
+ * ascends from 0 ([sequences + 1]), rows from its last entry on belong to no
+ * sequence.  1 <= sequences <= 65535; 1 <= table_pages <= ld_table, the pages a
+ * table row names.
+ * Entries are checked on the device: a position that is negative or past the
+ * table, or whose page is outside [0, pages), is not there -- it is not written,
+ * and attention does not see it. */
+typedef struct q3_paged_batch {
+  int64_t sequences;
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const int32_t* page_table;
+  int64_t ld_table;
+  int64_t table_pages;
+} q3_paged_batch;
+
+/* The heads of a qkv product's rows [heads_q | heads_kv | heads_kv] of head_dim
+ * (queries, keys, values), the norms and the rotation of the first two:
+ *   x = head * weight * rsqrt(mean(head^2) + eps)     (weight NULL: x = head)
+ *   angle_j = position * inv_freq[j],  j < rotated / 2
+ *   (x_a, x_b) <- (x_a cos - x_b sin, x_b cos + x_a sin)
+ * with (a, b) = (j, j + rotated/2), or (2j, 2j + 1) where interleaved; values
+ * from `rotated` on stay.  Angles are formed and reduced in 64 bits.
+ * inv_freq fp32 [rotated / 2] (may be NULL where rotated is 0); weights fp32
+ * [head_dim]; heads_q, heads_kv 1..1024; head_dim as in a cache; rotated even,
+ * 0..head_dim. */
+typedef struct q3_head_norms {
+  int32_t heads_q;
+  int32_t heads_kv;
+  int32_t head_dim;
+  int32_t rotated;
+  int32_t interleaved;
+  float eps;
+  const float* q_weight;
+  const float* k_weight;
+  const float* inv_freq;
+} q3_head_norms;
+
+/* qkv fp32 [m][ld], ld % 4 == 0, 16-byte aligned, m < 2^31 -> q bf16
+ * [m][ldq]; k and v either to a cache (cache and batch given, k and v NULL) or as
+ * bf16 rows [m][ldk], [m][ldv] (cache and batch NULL).  bf16 rows: pitch % 8 ==
+ * 0, 16-byte aligned.  positions int32 [m] (device), or NULL: the batch's.  With
+ * a batch the cache's positions are the batch's also where positions is given,
+ * and rows that belong to no sequence are not read and their q not written. */
+Q3_API q3_status q3_qk_norm_rope(const q3_head_norms* heads, const float* qkv, int64_t ld, const int32_t* positions,
+                                 uint16_t* q, int64_t ldq, uint16_t* k, int64_t ldk, uint16_t* v, int64_t ldv,
+                                 const q3_paged_cache* cache, const q3_paged_batch* batch, int64_t m, void* stream);
+
+/* Its backward pass, from the kept qkv rows: dq, dk, dv (each may be NULL:
+ * zero) of d_type (Q3_F32 or Q3_BF16; pitch in elements and 16-byte aligned as
+ * above, fp32 rows % 4) -> dqkv bf16 [m][ld_dqkv] (what q3_gemm_backward takes)
+ * and dq_weight, dk_weight fp32 [head_dim], summed over tokens and heads in a
+ * fixed order (may be NULL; NULL where the weight is).  positions as above, given
+ * where rotated is not 0.  workspace: 256-byte aligned,
+ * q3_qk_norm_rope_backward_workspace_bytes(m, head_dim) bytes. */
+typedef struct q3_qkv_grads {
+  int32_t d_type;
+  const void* dq;
+  int64_t ld_dq;
+  const void* dk;
+  int64_t ld_dk;
+  const void* dv;
+  int64_t ld_dv;
+  uint16_t* dqkv;
+  int64_t ld_dqkv;
+  float* dq_weight;
+  float* dk_weight;
+} q3_qkv_grads;
+Q3_API int64_t q3_qk_norm_rope_backward_workspace_bytes(int64_t m, int32_t head_dim);
+Q3_API q3_status q3_qk_norm_rope_backward(const q3_head_norms* heads, const float* qkv, int64_t ld,
+                                          const int32_t* positions, int64_t m, const q3_qkv_grads* grads,
+                                          void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Attention of the batch's new tokens over the cache (their own keys and values
+ * are in it): a token at position p sees the cache's positions j <= p, with
+ * window > 0 only j > p - window.  Query head h reads the cache's head
+ * h / (heads_q / heads), heads_q a multiple of the cache's heads, up to 1024.
+ *   S_j = scale q . k_j,  o = sum_j softmax(S)_j v_j,  lse = ln sum_j e^(S_j)
+ * q bf16 [m][ldq], out bf16 [m][ldo], heads_q * head_dim columns, pitch % 8 == 0,
+ * 16-byte aligned; lse fp32 [m][heads_q] or NULL.  A token that sees nothing gets
+ * zeros and lse -inf; rows that belong to no sequence are left as they are.
+ * What a token does not see cannot reach its row, whatever it holds (infinities
+ * and NaN too).  Scores, sums and products are fp32; the weights e^(S - max)
+ * enter the second product as bf16.  scale: finite, normal (its size at least
+ * 2^-126).  1 <= m < 2^24, m * heads_q < 2^30, sequences * heads < 2^23.
+ * workspace: 256-byte aligned, q3_paged_attention_workspace_bytes(m, sequences,
+ * heads_q, heads, head_dim) bytes. */
+Q3_API int64_t q3_paged_attention_workspace_bytes(int64_t m, int64_t sequences, int32_t heads_q, int32_t heads,
+                                                  int32_t head_dim);
+Q3_API q3_status q3_paged_attention(const uint16_t* q, int64_t ldq, int32_t heads_q, const q3_paged_cache* cache,
+                                    const q3_paged_batch* batch, float scale, int32_t window, uint16_t* out,
+                                    int64_t ldo, float* lse, int64_t m, void* workspace, int64_t workspace_bytes,
+                                    void* stream);
+
 /* ---- Sampling ----------------------------------------------------------------- */
 
 /* One token per row of logits (the vocabulary product's fp32 outputs), from a
@@ -189,6 +305,41 @@ Q3_API int64_t q3_sample_workspace_bytes(int64_t m, int64_t n);
 Q3_API q3_status q3_sample(const float* logits, int64_t m, int64_t n, int64_t ld, const float* temperature,
                            const int32_t* top_k, const float* top_p, const float* min_p, const float* u,
                            void* workspace, int64_t workspace_bytes, int32_t* tokens, float* logprobs, void* stream);
+
+/* ---- Log probabilities ----------------------------------------------------------- */
+
+/* Scores of given tokens under rows of logits (the vocabulary product's fp32
+ * outputs), with z = logits / temperature and p = softmax(z):
+ *   logprobs[i] = ln p[targets[i]]; a target outside [0, n) is none: 0
+ *   entropy[i]  = -sum p ln p                            (may be NULL)
+ *   top_ids, top_logprobs [m][top]: the entries with the largest logits, larger
+ *     first, equal ones by lower index (top 0..32, both NULL where it is 0)
+ *   stats fp32 [m][4]: the largest logit, ln sum e^(z - max z), entropy, 0 (may be
+ *     NULL): what the backward pass takes; 16-byte aligned
+ * Masks as in q3_sample: -inf and NaN have no weight (logprob -inf, never in
+ * top), if some logits are +inf only those count; a row with nothing else gives
+ * logprob -inf (0 without a target) and entropy 0.  Unfilled places of top hold -1 and -inf.
+ * logits fp32 [m][ld], 1 <= n <= 2^19, 1 <= m < 2^24; targets int32 [m], device;
+ * temperature > 0, it and its reciprocal finite.  workspace: 256-byte aligned,
+ * q3_logprobs_workspace_bytes(m, n, top) bytes. */
+Q3_API int64_t q3_logprobs_workspace_bytes(int64_t m, int64_t n, int32_t top);
+Q3_API q3_status q3_logprobs(const float* logits, int64_t m, int64_t n, int64_t ld, const int32_t* targets,
+                             float temperature, int32_t top, float* logprobs, float* entropy, int32_t* top_ids,
+                             float* top_logprobs, float* stats, void* workspace, int64_t workspace_bytes,
+                             void* stream);
+
+/* The gradient of the logits, from the logits and the kept stats:
+ *   dlogits[i][j] = (dlogprobs[i] ([j == target] - p_j)
+ *                    - dentropy[i] p_j (ln p_j + entropy[i])) / temperature
+ * and 0 at masked entries.  dlogprobs, dentropy fp32 [m] (each may be NULL:
+ * zero); targets may be NULL where dlogprobs is.  dlogits of d_type (Q3_BF16,
+ * what q3_gemm_backward takes, or Q3_F32) [m][ld_d]; elements are naturally
+ * aligned, rows aligned to four elements move in vectors; fp32 dlogits may be
+ * the logits themselves (same pitch). */
+Q3_API q3_status q3_logprobs_backward(const float* logits, int64_t m, int64_t n, int64_t ld, const int32_t* targets,
+                                      float temperature, const float* stats, const float* dlogprobs,
+                                      const float* dentropy, void* dlogits, int64_t ld_d, int32_t d_type,
+                                      void* stream);
 
 #ifdef __cplusplus
 }
