@@ -79,7 +79,7 @@ __device__ __forceinline__ int below_window(const AttendArgs& a, int position) {
   return low > -1 ? (int)low : -1;
 }
 struct Span {
-  int lo, hi;
+  int lo, hi;   // hi == lo: nothing
 };
 __device__ __forceinline__ Span span_of(const AttendArgs& a, const Tile& t, int r0, int r1, int group) {
   const int64_t held = a.batch.table_pages << a.cache.shift;
@@ -91,31 +91,127 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, const Tile& t, int 
   return {(int)lo, (int)hi};
 }
 
-// ---- tiles of 128 rows ----------------------------------------------------------
+// ---- keys and values on their way to LDS ------------------------------------------
 
-constexpr int kWideRows = 128, kStep = 64, kWideThreads = 256;
-
-// Where chunk c (16 bytes) of key row `key` stands among the row's chunks in LDS.
+// A tile of keys or values in LDS: rows of DT values (the head's, padded with zeros
+// to one of the lengths that the kernels are made for), in chunks of 16 bytes.
 // Keys are read 16 bytes a lane from 16 consecutive rows, values 8 bytes a lane
-// from 4 rows and 64 consecutive bytes of each: either way the lanes of a step
-// fall on all banks.
-template <int DP>
-__device__ __forceinline__ uint32_t place_k(uint32_t key) {
-  return DP == 64 ? (key >> 1) & 7u : key & 15u;
+// from 4 rows and 64 consecutive bytes of each; place_k and place_v say which bits
+// of a chunk's number are turned over in which row, so that the lanes of a step
+// fall on all 64 banks either way.
+template <int DT>
+struct Layout {
+  static constexpr int chunks = DT / 8;
+  static constexpr uint32_t row = DT * 2;
+  static __device__ __forceinline__ uint32_t place_k(uint32_t key) {
+    if constexpr (chunks % 16 == 0) return key & 15u;
+    else if constexpr (chunks % 8 == 0) return (key >> 1) & 7u;
+    else return (key >> 2) & 3u;
+  }
+  static __device__ __forceinline__ uint32_t place_v(uint32_t key) {
+    if constexpr (chunks % 16 == 0) return 4u * (key & 3u);
+    else if constexpr (chunks % 8 == 0) return 4u * ((key >> 1) & 1u);
+    else return 0u;
+  }
+};
+
+__device__ const u32x4 kZeros = {0u, 0u, 0u, 0u};   // what stands behind a head's last value
+
+// One wave's 1 KB from memory to LDS: lane l's 16 bytes land at dst + 16 l.  As
+// assembly, because the compiler would make every transposing LDS read wait for
+// all of them; the kernels wait for the ones they need.
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)p);   // the low half of a generic address
 }
-template <int DP>
-__device__ __forceinline__ uint32_t place_v(uint32_t key) {
-  return DP == 64 ? 4u * ((key >> 1) & 1u) : 4u * (key & 3u);
+__device__ __forceinline__ void load_lds(const void* base, uint32_t offset, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst), "v"(offset), "s"(base) : "memory");
+}
+__device__ __forceinline__ void load_lds(const void* p, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(dst), "v"(p) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_loads() {   // until at most N are under way
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void reads_done() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// The pages of a run of positions, checked once and kept in LDS (-1: not there),
+// so that no load of a table stands between two of the cache.
+constexpr int kListed = 2048;
+struct Pages {
+  int* id;
+  int first;   // the page number that id[0] stands for
+};
+__device__ __forceinline__ void list_pages(const AttendArgs& a, const Tile& t, int key0, int key1, Pages& pages,
+                                           int thread, int threads) {
+  pages.first = key0 >> a.cache.shift;
+  const int count = key1 > key0 ? ((key1 - 1) >> a.cache.shift) - pages.first + 1 : 0;
+  for (int i = thread; i < count && i < kListed; i += threads)
+    pages.id[i] = (int)find_page(a.batch, a.cache, t.sequence, (int64_t)(pages.first + i) << a.cache.shift);
+}
+// Keys that a list takes, a multiple of `step`.
+__device__ __forceinline__ int listed_keys(const AttendArgs& a, int step) {
+  const int64_t n = (int64_t)(kListed - 1) << a.cache.shift;
+  return (int)(n < (1 << 30) ? n : 1 << 30) / step * step;
 }
 
-// A partial result's slot: unscaled sums [rows][DP], then maximum and sum of each row.
-template <int DP>
-constexpr int64_t slot_floats(int rows) { return (int64_t)rows * (DP + 2); }
+// What a wave needs to bring KEYS consecutive keys (or values) of a head: for each
+// load, which key and chunk the lane takes.
+template <int DT, int KEYS>
+struct Loader {
+  using L = Layout<DT>;
+  static constexpr int count = KEYS * L::chunks / 64;
+  uint32_t off[2][count];   // bytes from the first key's row, heads of DT values: keys, values
 
-// Parts that a tile's steps go to: at most `splits`.
-__device__ __forceinline__ int parts_of(int steps, int splits) { return steps < splits ? (steps > 0 ? steps : 1) : splits; }
+  static __device__ __forceinline__ uint32_t key_of(int i, int lane) { return (uint32_t)(64 * i + lane) / L::chunks; }
+  // `at`: the number of the first key's row in its LDS tile.
+  static __device__ __forceinline__ uint32_t chunk_of(int i, int lane, int at, int which) {
+    const uint32_t key = at + key_of(i, lane), c = (uint32_t)(64 * i + lane) % L::chunks;
+    return c ^ (which ? L::place_v(key) : L::place_k(key));
+  }
+  __device__ __forceinline__ void init(int lane, int at) {
+#pragma unroll
+    for (int i = 0; i < count; ++i)
+#pragma unroll
+      for (int w = 0; w < 2; ++w) off[w][i] = (key_of(i, lane) * DT + 8 * chunk_of(i, lane, at, w)) * 2;
+  }
+  // Positions key0.. of `head` (key0 a multiple of KEYS); which: 0 keys, 1 values.
+  __device__ __forceinline__ void issue(const AttendArgs& a, const Pages& pages, int head, int key0, int at, int which,
+                                        uint32_t dst, int lane) const {
+    const int shift = a.cache.shift, mask = (1 << shift) - 1, d = a.cache.d;
+    const uint16_t* base = which ? a.cache.v : a.cache.k;
+    if (d == DT && (1 << shift) >= KEYS) {   // one page, whole rows
+      int id = __builtin_amdgcn_readfirstlane(pages.id[(key0 >> shift) - pages.first]);
+      id = id < 0 ? 0 : id;                  // read, but never used
+      const uint16_t* from = base + (int64_t)id * a.cache.page_stride + (((int64_t)head << shift) + (key0 & mask)) * DT;
+#pragma unroll
+      for (int i = 0; i < count; ++i) load_lds(from, off[which][i], dst + 1024u * i);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < count; ++i) {
+      const int key = key0 + (int)key_of(i, lane);
+      int id = pages.id[(key >> shift) - pages.first];
+      id = id < 0 ? 0 : id;
+      const uint32_t c = chunk_of(i, lane, at, which);
+      const uint16_t* p = base + (int64_t)id * a.cache.page_stride + (((int64_t)head << shift) + (key & mask)) * d + 8 * c;
+      load_lds(8 * c < (uint32_t)d ? (const void*)p : (const void*)&kZeros, dst + 1024u * i);
+    }
+  }
+};
 
-// The same value of the lane's row in the wave's other half.
+// ---- the products of one wave -------------------------------------------------------
+
+// A bit for each of the `keys` positions from key0 on that is there.
+__device__ __forceinline__ uint64_t there_of(const AttendArgs& a, const Pages& pages, int key0, int hi, int keys,
+                                             int lane) {
+  const int key = key0 + lane;
+  const bool in = lane < keys && key < hi;
+  return __ballot(in && pages.id[in ? (key >> a.cache.shift) - pages.first : 0] >= 0);
+}
+
+// The lane's other half: the same row's value there.
 __device__ __forceinline__ float other_half(float v) {
   const uint32_t u = __builtin_bit_cast(uint32_t, v);
   const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
@@ -133,24 +229,273 @@ __device__ __forceinline__ uint32_t finite2(uint32_t u) {
   return u;
 }
 
-// Four waves with 32 rows each, 64 keys at a time through two LDS buffers.  The
-// products are formed transposed, S^T = K Q^T and O^T = V^T P^T: a lane then
-// holds half of the scores of one row, so that maxima and sums stay in the lane
-// but for one exchange, and what it holds of P^T is the second product's operand
-// as it is, the keys of a fragment being taken in the order in which the first
-// product leaves them.
-template <int DP, bool kExact>
-__global__ __launch_bounds__(kWideThreads, DP > 128 ? 1 : 2)
+// Values that are not there, or that some row of the tile does not see, must not
+// reach a product: weights of 0 would turn infinities and NaN there into NaN.  The
+// absent ones become zeros, and so does what is not finite, which add_unseen adds
+// again for the rows that see it.  KEYS rows from `v` on, a bit of `there` each;
+// returns whether this lane took something out.
+template <int DT, int KEYS>
+__device__ __forceinline__ int clean_values(uint8_t* v, uint32_t there, int lane) {
+  int bad = 0;
+#pragma unroll
+  for (int i = 0; i < KEYS * Layout<DT>::chunks / 64; ++i) {
+    u32x4* p = reinterpret_cast<u32x4*>(v + 1024 * i + 16 * lane);
+    u32x4 u = *p;
+    if (!((there >> ((uint32_t)(64 * i + lane) / Layout<DT>::chunks)) & 1)) {
+      u = u32x4{0u, 0u, 0u, 0u};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t f = finite2(u[e]);
+        bad |= f != u[e];
+        u[e] = f;
+      }
+    }
+    *p = u;
+  }
+  return bad;
+}
+
+// A wave's rows and its running sums: NT tiles of 32 rows, in each the lane's row
+// is lane % 32.  The products are formed transposed, S^T = K Q^T and O^T = V^T P^T:
+// a lane then holds half of the scores of its row (key 8 (i / 4) + 4 half + i % 4 of
+// 32 in register i), so maxima and sums stay in the lane but for one exchange, and
+// what it holds of P^T is the second product's operand as it is, the keys of a
+// fragment being taken in the order in which the first product leaves them.
+template <int DT, int NT>
+struct Wave {
+  bf16x8 q[NT][DT / 16];
+  f32x16 o[NT][DT / 32];
+  float top[NT], sum[NT];
+  int position[NT], low[NT];   // the row sees low < key <= position
+  float c;                     // |scale| log2(e)
+  uint32_t value[DT / 32];     // byte of the lane's first transposing read, for each 32 values
+
+  __device__ __forceinline__ void init(const AttendArgs& a, const Tile& t, int head, int group, int first, int live,
+                                       int lane) {
+    c = fabsf(a.scale) * kLog2e;
+    const int half = lane >> 5, d = a.cache.d;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int row = first + 32 * n + (lane & 31);
+      const bool mine = row < live;
+      const int r = t.first + (mine ? row : 0);
+      const int64_t token = t.start + r / group;
+      const int qhead = head * group + r % group;
+      position[n] = position_of(t, r, group);
+      low[n] = below_window(a, position[n]);
+#pragma unroll
+      for (int k = 0; k < DT / 16; ++k) {
+        u32x4 u = {0u, 0u, 0u, 0u};
+        if (mine && 16 * k < d)
+          u = *reinterpret_cast<const u32x4*>(a.q + token * a.ldq + (int64_t)qhead * d + 16 * k + 8 * half);
+        if (a.scale < 0.f) u ^= 0x80008000u;   // the maximum is taken before scaling
+        q[n][k] = __builtin_bit_cast(bf16x8, u);
+      }
+#pragma unroll
+      for (int i = 0; i < DT / 32; ++i) o[n][i] = f32x16{};
+      top[n] = -INFINITY;
+      sum[n] = 0.f;
+    }
+    // A transposing read gives each lane one column of four rows: of 16 lanes, lane
+    // i asks for row i / 4 and its bytes 8 (i % 4).. of 32.
+    const uint32_t key = 4 * half + ((lane & 15) >> 2);
+#pragma unroll
+    for (int i = 0; i < DT / 32; ++i) {
+      const uint32_t chunk = 4 * i + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+      value[i] = key * Layout<DT>::row + 16u * (chunk ^ Layout<DT>::place_v(key)) + 8u * (lane & 1);
+    }
+  }
+
+  // Scores of 32 NB keys from the tile at `k` (rows of its LDS tile from `at` on).
+  template <int NB>
+  __device__ __forceinline__ void scores(const uint8_t* k, f32x16 (&sc)[NT][NB], int lane) const {
+    const int half = lane >> 5;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) sc[n][b] = f32x16{};
+#pragma unroll
+    for (int j = 0; j < DT / 16; ++j)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const uint32_t key = 32 * b + (lane & 31);
+        const bf16x8 f = *reinterpret_cast<const bf16x8*>(k + key * Layout<DT>::row +
+                                                          16u * ((2 * j + half) ^ Layout<DT>::place_k(key)));
+#pragma unroll
+        for (int n = 0; n < NT; ++n) sc[n][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[n][j], sc[n][b], 0, 0, 0);
+      }
+  }
+  // -inf for what the row does not see: a bit per key, widened to a word each, so
+  // that no comparison is kept per register.
+  template <int NB>
+  __device__ __forceinline__ void mask(f32x16 (&sc)[NT][NB], uint64_t there, int key0, int lane) const {
+    const int half = lane >> 5;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int up = position[n] - (key0 + 32 * b) + 1, down = low[n] - (key0 + 32 * b) + 1;   // seen: [down, up)
+        uint32_t seen = (uint32_t)(there >> (32 * b));
+        seen &= up >= 32 ? ~0u : up <= 0 ? 0u : (1u << up) - 1u;
+        seen &= down <= 0 ? ~0u : down >= 32 ? 0u : ~0u << down;
+        seen >>= 4 * half;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t keep = (uint32_t)__builtin_amdgcn_sbfe((int)seen, 8 * (i / 4) + i % 4, 1);
+          const float x = sc[n][b][i];
+          sc[n][b][i] = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, x) & keep) | (0xFF800000u & ~keep));
+        }
+      }
+  }
+  // Scores to weights, as bf16 operands of 16 keys each (what the second product
+  // takes: a weight is then off by half a step, 2^-8 of itself, as the result is
+  // once more.  The sum is that of the unrounded ones).  A second term for what the
+  // rounding leaves would cost the narrow kernel nothing, but turns an infinite
+  // value into NaN.
+  template <int NB>
+  __device__ __forceinline__ void weigh(const f32x16 (&sc)[NT][NB], bf16x8 (&p)[NT][2 * NB]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float high = sc[n][0][0];
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) high = fmaxf(high, sc[n][b][i]);
+      high = fmaxf(top[n], fmaxf(high, other_half(high)) * c);
+      const float base = high == -INFINITY ? 0.f : high;
+      if (__any(high > top[n])) {
+        const float f = __builtin_amdgcn_exp2f(top[n] - base);
+        sum[n] *= f;
+#pragma unroll
+        for (int i = 0; i < DT / 32; ++i) o[n][i] *= f;
+        top[n] = high;
+      }
+#pragma unroll
+      for (int b = 0; b < 2 * NB; ++b) {
+        u32x4 u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = __builtin_amdgcn_exp2f(fmaf(sc[n][b / 2][8 * (b % 2) + 2 * i], c, -base));
+          const float y = __builtin_amdgcn_exp2f(fmaf(sc[n][b / 2][8 * (b % 2) + 2 * i + 1], c, -base));
+          sum[n] += x + y;
+          u[i] = pack_bf16(x, y);
+        }
+        p[n][b] = __builtin_bit_cast(bf16x8, u);
+      }
+    }
+  }
+  // O^T += V^T P^T for 32 NB values from the tile at `v`.
+  template <int NB>
+  __device__ __forceinline__ void values(const uint8_t* v, const bf16x8 (&p)[NT][2 * NB]) {
+#pragma unroll
+    for (int b = 0; b < 2 * NB; ++b)
+#pragma unroll
+      for (int i = 0; i < DT / 32; ++i) {
+        union {
+          s16x4 part[2];
+          bf16x8 all;
+        } f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          f.part[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (__attribute__((address_space(3))) s16x4*)(v + value[i] + (16 * b + 8 * e) * Layout<DT>::row));
+#pragma unroll
+        for (int n = 0; n < NT; ++n) o[n][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.all, p[n][b], o[n][i], 0, 0, 0);
+      }
+  }
+  // Values that clean_values took out, for the rows that see them (a weight times
+  // an infinity or NaN is that again).
+  __device__ __forceinline__ void add_unseen(const AttendArgs& a, const Pages& pages, uint64_t there, int head, int key0,
+                                             int keys, int lane) {
+    const int half = lane >> 5, shift = a.cache.shift, d = a.cache.d;
+    for (int k = 0; k < keys; ++k) {
+      const int key = key0 + k;
+      if (!((there >> k) & 1)) continue;
+      const uint16_t* from = a.cache.v + (int64_t)pages.id[(key >> shift) - pages.first] * a.cache.page_stride +
+                             (((int64_t)head << shift) + (key & ((1 << shift) - 1))) * d;
+#pragma unroll
+      for (int i = 0; i < DT / 32; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int e = 32 * i + 8 * j + 4 * half;
+          u32x2 u = {0u, 0u};
+          if (e < d) u = *reinterpret_cast<const u32x2*>(from + e);
+#pragma unroll
+          for (int l = 0; l < 4; ++l) {
+            const uint32_t pair = l < 2 ? u.x : u.y;
+            const float x = __builtin_bit_cast(float, l & 1 ? pair & 0xFFFF0000u : pair << 16);
+            const float add = fabsf(x) < INFINITY ? 0.f : x;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) o[n][i][4 * j + l] += key <= position[n] && key > low[n] ? add : 0.f;
+          }
+          __builtin_amdgcn_sched_barrier(0);   // rare: one load at a time, no registers for more
+        }
+    }
+  }
+};
+
+// A partial result's slot: unscaled sums [rows][DT], then maximum and sum of each row.
+template <int DT>
+constexpr int64_t slot_floats(int rows) { return (int64_t)rows * (DT + 2); }
+
+__device__ __forceinline__ float lse_of(float top, float sum) {
+  return sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+__device__ __forceinline__ void store4(const AttendArgs& a, int64_t token, int qhead, int e, f32x4 v) {
+  *reinterpret_cast<u32x2*>(a.out + token * a.ldo + (int64_t)qhead * a.cache.d + e) =
+      u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+}
+
+// Row `row` (of `rows`) of a tile from its `count` partial results slot(0).., in
+// order, by 32 lanes of which this is l.
+template <int DT, typename Slot>
+__device__ __forceinline__ void join_row(const AttendArgs& a, const Tile& t, int head, int group, Slot&& slot, int count,
+                                         int rows, int row, int l) {
+  float top = -INFINITY, sum = 0.f;
+  for (int z = 0; z < count; ++z) top = fmaxf(top, slot(z)[rows * DT + 2 * row]);
+  f32x4 o[(DT + 127) / 128] = {};
+  for (int z = 0; z < count; ++z) {
+    const float* p = slot(z);
+    const float m = p[rows * DT + 2 * row];
+    const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
+    sum += f * p[rows * DT + 2 * row + 1];
+#pragma unroll
+    for (int i = 0; i < (DT + 127) / 128; ++i)
+      if (128 * i + 4 * l < DT) o[i] += f * *reinterpret_cast<const f32x4*>(p + row * DT + 128 * i + 4 * l);
+  }
+  const int r = t.first + row;
+  const int64_t token = t.start + r / group;
+  const int qhead = head * group + r % group;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int i = 0; i < (DT + 127) / 128; ++i)
+    if (128 * i + 4 * l < a.cache.d) store4(a, token, qhead, 128 * i + 4 * l, o[i] * inv);
+  if (a.lse && l == 0) a.lse[token * a.hq + qhead] = lse_of(top, sum);
+}
+
+// ---- many rows: tiles of 128 -----------------------------------------------------------
+
+constexpr int kWideRows = 128, kStep = 64, kThreads = 256;
+
+// Parts that a tile's steps go to: at most `splits`.
+__device__ __forceinline__ int parts_of(int steps, int splits) {
+  return steps < splits ? (steps > 0 ? steps : 1) : splits;
+}
+__device__ __forceinline__ int steps_of(const Span& span) {
+  return (span.hi - (span.lo & ~(kStep - 1)) + kStep - 1) / kStep;
+}
+
+// Four waves with 32 rows each share 64 keys at a time through two LDS buffers.
+template <int DT>
+__global__ __launch_bounds__(kThreads, DT > 128 ? 1 : 2)
 void attend_wide_kernel(AttendArgs a, int splits, float* parts) {
-  constexpr int CH = DP / 8;                         // chunks of a key row
-  constexpr uint32_t kRow = DP * 2, kTileBytes = kStep * kRow, kBuf = 2 * kTileBytes;
-  constexpr int kLoads = CH / 4;                     // of a wave: 16 keys
-  constexpr int kKeysPerLoad = 64 / CH;
+  constexpr uint32_t kTile = kStep * Layout<DT>::row, kBuf = 2 * kTile;
   extern __shared__ __align__(16) uint8_t lds[];
-  __shared__ uint32_t held[2][4];                    // each wave's 16 keys: a bit for each that is there
+  __shared__ int list[kListed];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int hk = a.cache.heads, group = a.hq / hk, d = a.cache.d;
+  const int hk = a.cache.heads, group = a.hq / hk;
 
   // Contiguous runs of (head, tile) to each XCD: tiles that read the same keys share an L2.
   const int64_t tiles = tiles_of(a.m, a.batch.sequences, group, kWideRows);
@@ -164,317 +509,491 @@ void attend_wide_kernel(AttendArgs a, int splits, float* parts) {
   if (t.sequence == a.batch.sequences) return;
   const int live = t.rows - t.first < kWideRows ? t.rows - t.first : kWideRows;
   const Span span = span_of(a, t, t.first, t.first + live, group);
-  const int begin = span.lo & ~(kStep - 1);
-  const int steps = (span.hi - begin + kStep - 1) / kStep;
+  const int begin = span.lo & ~(kStep - 1), steps = steps_of(span);
   const int count = parts_of(steps, splits);
   if (z >= count) return;
   const int s0 = (int)((int64_t)steps * z / count), s1 = (int)((int64_t)steps * (z + 1) / count);
 
-  // This lane's row, and its query in registers.
-  const int row = 32 * wave + (lane & 31), half = lane >> 5;
-  const bool mine = row < live;
-  const int r = t.first + (mine ? row : 0);
-  const int token = t.start + r / group, qhead = head * group + r % group;
-  const int position = position_of(t, r, group), low = below_window(a, position);
-  const float c = fabsf(a.scale) * kLog2e;
-  bf16x8 q[DP / 16];
-#pragma unroll
-  for (int k = 0; k < DP / 16; ++k) {
-    u32x4 u = {0u, 0u, 0u, 0u};
-    if (mine && (kExact || 16 * k < d))
-      u = *reinterpret_cast<const u32x4*>(a.q + (int64_t)token * a.ldq + (int64_t)qhead * d + 16 * k + 8 * half);
-    if (a.scale < 0.f) u ^= 0x80008000u;             // the maximum is taken before scaling
-    q[k] = __builtin_bit_cast(bf16x8, u);
-  }
-
-  // The page of one of the wave's 16 keys of a step (lane l: key l % 16), -1 where it is not there.
-  auto page_of = [&](int s) {
-    const int key = begin + s * kStep + 16 * wave + (lane & 15);
-    return s < s1 && key < span.hi ? (int)find_page(a.batch, a.cache, t.sequence, key) : -1;
-  };
-  const int mask = (1 << a.cache.shift) - 1;
-  auto issue = [&](int s, int page) {
-    uint8_t* buf = lds + (s & 1) * kBuf + wave * 16 * kRow;
-    const uint32_t there = (uint32_t)__ballot(page >= 0) & 0xFFFFu;
-    if (lane == 0) held[s & 1][wave] = there;
-    const int key0 = begin + s * kStep + 16 * wave;
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int k = i * kKeysPerLoad + lane / CH;    // of the wave's 16
-      const uint32_t key = 16 * wave + k, at = lane % CH;
-      int p = __shfl(page, k, 64);
-      p = p < 0 ? 0 : p;                             // read, but never used
-      const int64_t from = (int64_t)p * a.cache.page_stride + (((int64_t)head << a.cache.shift) + ((key0 + k) & mask)) * d;
-      uint32_t ck = at ^ place_k<DP>(key), cv = at ^ place_v<DP>(key);
-      if (!kExact) {
-        ck = 8 * ck < (uint32_t)d ? ck : 0;
-        cv = 8 * cv < (uint32_t)d ? cv : 0;
-      }
-      __builtin_amdgcn_global_load_lds(
-          (const __attribute__((address_space(1))) void*)(a.cache.k + from + 8 * ck),
-          (__attribute__((address_space(3))) void*)(buf + i * 1024), 16, 0, 0);
-      __builtin_amdgcn_global_load_lds(
-          (const __attribute__((address_space(1))) void*)(a.cache.v + from + 8 * cv),
-          (__attribute__((address_space(3))) void*)(buf + kTileBytes + i * 1024), 16, 0, 0);
-    }
-  };
-
-  f32x16 o[DP / 32];
-#pragma unroll
-  for (int i = 0; i < DP / 32; ++i) o[i] = f32x16{};
-  float top = -INFINITY, sum = 0.f;
-
+  Wave<DT, 1> w;
+  w.init(a, t, head, group, 32 * wave, live, lane);
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // the compiler waits for nothing of it inside the loop
   const int first_position = position_of(t, t.first, group);   // of the tile's rows
   const int last_low = below_window(a, position_of(t, t.first + live - 1, group));
-  int page = page_of(s0);
-  if (s0 < s1) issue(s0, page);
-  page = page_of(s0 + 1);
-  for (int s = s0; s < s1; ++s) {
-    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this step's loads and the next one's pages
-    __syncthreads();
-    if (s + 1 < s1) issue(s + 1, page);
-    page = page_of(s + 2);
-    uint8_t* buf = lds + (s & 1) * kBuf;
-    const int key0 = begin + s * kStep;
-    uint64_t there = 0;
+  Loader<DT, 16> loader;
+  loader.init(lane, 16 * wave);
+  Pages pages{list, 0};
+  const uint32_t base = lds_offset(lds) + wave * 16 * Layout<DT>::row;
+  auto issue = [&](int s) {
+    const int key0 = begin + s * kStep + 16 * wave;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) there |= (uint64_t)held[s & 1][w] << (16 * w);
-    const bool whole = ~there == 0 && key0 + kStep - 1 <= first_position &&
-                       key0 > last_low;
-    int bad = 0;
-    if (!whole) {
-      // Values that are not there, or that some row does not see, must not reach
-      // a product: weights of 0 would turn infinities and NaN there into NaN.
-      // What is not finite is taken out here and added again below for the rows
-      // that see it.
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int k = i * kKeysPerLoad + lane / CH;
-        u32x4* p = reinterpret_cast<u32x4*>(buf + kTileBytes + wave * 16 * kRow + i * 1024 + lane * 16);
-        u32x4 v = *p;
-        if (!((held[s & 1][wave] >> k) & 1)) {
-          v = u32x4{0u, 0u, 0u, 0u};
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t f = finite2(v[e]);
-            bad |= f != v[e];
-            v[e] = f;
-          }
-        }
-        *p = v;
-      }
-      bad = __syncthreads_or(bad);
-    }
-    if (32 * wave >= live) continue;
+    for (int which = 0; which < 2; ++which)
+      loader.issue(a, pages, head, key0, 16 * wave, which, base + (s & 1) * kBuf + which * kTile, lane);
+  };
 
-    // S^T: keys of 32-key block b, 8 (i / 4) + 4 half + i % 4, of this lane's row.
-    f32x16 sc[2] = {f32x16{}, f32x16{}};
-#pragma unroll
-    for (int k = 0; k < DP / 16; ++k) {
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        if (!kExact && 16 * k >= d) continue;
-        const uint32_t key = 32 * b + (lane & 31);
-        const bf16x8 f = *reinterpret_cast<const bf16x8*>(buf + key * kRow + 16u * ((2 * k + half) ^ place_k<DP>(key)));
-        sc[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[k], sc[b], 0, 0, 0);
+  const int run = listed_keys(a, kStep) / kStep;
+  for (int w0 = s0; w0 < s1; w0 += run) {
+    const int w1 = s1 - w0 < run ? s1 : w0 + run;
+    meet();   // the list and the buffers are free
+    list_pages(a, t, begin + w0 * kStep, begin + w1 * kStep, pages, threadIdx.x, kThreads);
+    meet();
+    issue(w0);
+    for (int s = w0; s < w1; ++s) {
+      wait_loads<0>();
+      meet();   // everyone's loads of this step are in, and everyone has left the step before
+      if (s + 1 < w1) issue(s + 1);
+      uint8_t* buf = lds + (s & 1) * kBuf;
+      const int key0 = begin + s * kStep;
+      const uint64_t there = there_of(a, pages, key0, span.hi, kStep, lane);
+      const bool whole = ~there == 0 && key0 + kStep - 1 <= first_position && key0 > last_low;
+      int bad = 0;
+      if (!whole) {
+        bad = clean_values<DT, 16>(buf + kTile + wave * 16 * Layout<DT>::row, (uint32_t)(there >> (16 * wave)), lane);
+        bad = __syncthreads_or(bad);
       }
-    }
-    if (!whole) {
-      const uint64_t seen = there >> (4 * half);
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int k = 32 * b + 8 * (i / 4) + i % 4, key = key0 + k + 4 * half;
-          const bool sees = ((seen >> k) & 1) && key <= position && key > low;
-          sc[b][i] = sees ? sc[b][i] : -INFINITY;
-        }
-    }
-    float high = sc[0][0];
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) high = fmaxf(high, sc[b][i]);
-    high = fmaxf(top, fmaxf(high, other_half(high)) * c);
-    const float base = high == -INFINITY ? 0.f : high;
-    if (__any(high > top)) {
-      const float f = __builtin_amdgcn_exp2f(top - base);
-      sum *= f;
-#pragma unroll
-      for (int i = 0; i < DP / 32; ++i) o[i] *= f;
-      top = high;
-    }
-    bf16x8 p[4];
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      u32x4 u;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float x = __builtin_amdgcn_exp2f(fmaf(sc[b / 2][8 * (b % 2) + 2 * i], c, -base));
-        const float y = __builtin_amdgcn_exp2f(fmaf(sc[b / 2][8 * (b % 2) + 2 * i + 1], c, -base));
-        sum += x + y;
-        u[i] = pack_bf16(x, y);
-      }
-      p[b] = __builtin_bit_cast(bf16x8, u);
-    }
-    // O^T += V^T P^T.  A transposing read gives each lane one column of four
-    // rows: lanes 16 g + i ask for row i / 4 of four, 8 bytes i % 4 of 32.
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-#pragma unroll
-      for (int n = 0; n < DP / 32; ++n) {
-        if (!kExact && 32 * n >= d) continue;
-        union {
-          s16x4 part[2];
-          bf16x8 all;
-        } v;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t key = 16 * b + 8 * e + 4 * half + ((lane & 15) >> 2);
-          const uint32_t chunk = 4 * n + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-          v.part[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(
-              buf + kTileBytes + key * kRow + 16u * (chunk ^ place_v<DP>(key)) + 8u * (lane & 1)));
-        }
-        o[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v.all, p[b], o[n], 0, 0, 0);
-      }
-    }
-    if (bad) {
-      for (int k = 0; k < kStep; ++k) {
-        const int key = key0 + k;
-        if (!((there >> k) & 1)) continue;
-        const bool sees = mine && key <= position && key > low;
-        const int64_t from = find_page(a.batch, a.cache, t.sequence, key) * a.cache.page_stride +
-                             (((int64_t)head << a.cache.shift) + (key & mask)) * d;
-#pragma unroll
-        for (int n = 0; n < DP / 32; ++n)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int e = 32 * n + 8 * (i / 4) + 4 * half + i % 4;
-            if (!kExact && e >= d) continue;
-            const float v = __builtin_bit_cast(float, (uint32_t)a.cache.v[from + e] << 16);
-            if (sees && !(fabsf(v) < INFINITY)) o[n][i] += v;
-          }
-      }
+      if (32 * wave >= live) continue;
+      f32x16 sc[1][2];
+      w.scores(buf, sc, lane);
+      if (!whole) w.mask(sc, there, key0, lane);
+      bf16x8 p[1][4];
+      w.template weigh<2>(sc, p);
+      w.template values<2>(buf + kTile, p);
+      if (bad) w.add_unseen(a, pages, there, head, key0, kStep, lane);
     }
   }
 
-  sum += other_half(sum);
-  if (!mine) return;
-  if (count == 1) {
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    uint16_t* to = a.out + (int64_t)token * a.ldo + (int64_t)qhead * d;
-#pragma unroll
-    for (int n = 0; n < DP / 32; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e = 32 * n + 8 * i + 4 * half;
-        if (!kExact && e >= d) continue;
-        *reinterpret_cast<u32x2*>(to + e) = u32x2{pack_bf16(o[n][4 * i] * inv, o[n][4 * i + 1] * inv),
-                                                  pack_bf16(o[n][4 * i + 2] * inv, o[n][4 * i + 3] * inv)};
-      }
-    if (a.lse && half == 0) a.lse[(int64_t)token * a.hq + qhead] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-    return;
-  }
-  float* slot = parts + ((tile * hk + head) * splits + z) * slot_floats<DP>(kWideRows);
-#pragma unroll
-  for (int n = 0; n < DP / 32; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<f32x4*>(slot + row * DP + 32 * n + 8 * i + 4 * half) =
-          f32x4{o[n][4 * i], o[n][4 * i + 1], o[n][4 * i + 2], o[n][4 * i + 3]};
-  if (half == 0) {
-    slot[kWideRows * DP + 2 * row] = top;
-    slot[kWideRows * DP + 2 * row + 1] = sum;
-  }
-}
-
-// The parts of a tile's rows, in order: eight rows a block, 32 lanes a row.
-template <int DP>
-__global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int splits, const float* parts) {
-  const int lane = threadIdx.x & 63;
-  const int hk = a.cache.heads, group = a.hq / hk, d = a.cache.d;
-  const int64_t tile = blockIdx.x / hk;
-  const int head = blockIdx.x % hk;
-  const Tile t = find_tile(a, tile, group, kWideRows, lane);
-  if (t.sequence == a.batch.sequences) return;
-  const int live = t.rows - t.first < kWideRows ? t.rows - t.first : kWideRows;
-  const Span span = span_of(a, t, t.first, t.first + live, group);
-  const int count = parts_of((span.hi - (span.lo & ~(kStep - 1)) + kStep - 1) / kStep, splits);
-  const int row = blockIdx.y * 8 + threadIdx.x / 32, l = threadIdx.x % 32;
-  if (count == 1 || row >= live) return;
-  const float* slot = parts + (tile * hk + head) * splits * slot_floats<DP>(kWideRows);
-  float top = -INFINITY, sum = 0.f;
-  for (int z = 0; z < count; ++z) top = fmaxf(top, slot[z * slot_floats<DP>(kWideRows) + kWideRows * DP + 2 * row]);
-  f32x4 o[(DP + 127) / 128] = {};
-  for (int z = 0; z < count; ++z) {
-    const float* p = slot + z * slot_floats<DP>(kWideRows);
-    const float m = p[kWideRows * DP + 2 * row];
-    const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
-    sum += f * p[kWideRows * DP + 2 * row + 1];
-#pragma unroll
-    for (int i = 0; i < (DP + 127) / 128; ++i)
-      if (128 * i + 4 * l < DP) o[i] += f * *reinterpret_cast<const f32x4*>(p + row * DP + 128 * i + 4 * l);
-  }
+  const int row = 32 * wave + (lane & 31), half = lane >> 5;
+  const float sum = w.sum[0] + other_half(w.sum[0]);
+  if (row >= live) return;
   const int r = t.first + row;
   const int64_t token = t.start + r / group;
   const int qhead = head * group + r % group;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  if (count == 1) {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-  for (int i = 0; i < (DP + 127) / 128; ++i) {
-    const int e = 128 * i + 4 * l;
-    if (e < d)
-      *reinterpret_cast<u32x2*>(a.out + token * a.ldo + (int64_t)qhead * d + e) =
-          u32x2{pack_bf16(o[i][0] * inv, o[i][1] * inv), pack_bf16(o[i][2] * inv, o[i][3] * inv)};
+    for (int n = 0; n < DT / 32; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e = 32 * n + 8 * i + 4 * half;
+        const f32x16& o = w.o[0][n];
+        if (e < a.cache.d)
+          store4(a, token, qhead, e, f32x4{o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]} * inv);
+      }
+    if (a.lse && half == 0) a.lse[token * a.hq + qhead] = lse_of(w.top[0], sum);
+    return;
   }
-  if (a.lse && l == 0) a.lse[token * a.hq + qhead] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+  float* slot = parts + ((tile * hk + head) * splits + z) * slot_floats<DT>(kWideRows);
+#pragma unroll
+  for (int n = 0; n < DT / 32; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x16& o = w.o[0][n];
+      *reinterpret_cast<f32x4*>(slot + row * DT + 32 * n + 8 * i + 4 * half) =
+          f32x4{o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]};
+    }
+  if (half == 0) {
+    slot[kWideRows * DT + 2 * row] = w.top[0];
+    slot[kWideRows * DT + 2 * row + 1] = sum;
+  }
 }
 
-int padded(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
+// The parts of a tile's rows: eight rows a block, 32 lanes a row.
+template <int DT>
+__global__ __launch_bounds__(kThreads) void attend_wide_join_kernel(AttendArgs a, int splits, const float* parts) {
+  const int hk = a.cache.heads, group = a.hq / hk;
+  const int64_t tile = blockIdx.x / hk;
+  const int head = blockIdx.x % hk;
+  const Tile t = find_tile(a, tile, group, kWideRows, threadIdx.x & 63);
+  if (t.sequence == a.batch.sequences) return;
+  const int live = t.rows - t.first < kWideRows ? t.rows - t.first : kWideRows;
+  const int count = parts_of(steps_of(span_of(a, t, t.first, t.first + live, group)), splits);
+  const int row = blockIdx.y * 8 + threadIdx.x / 32;
+  if (count == 1 || row >= live) return;
+  const float* first = parts + (tile * hk + head) * splits * slot_floats<DT>(kWideRows);
+  join_row<DT>(a, t, head, group, [&](int z) { return first + z * slot_floats<DT>(kWideRows); }, count, kWideRows, row,
+               threadIdx.x % 32);
+}
 
-// Splits of the keys: until every CU has two blocks.
-int splits_of(int64_t m, int64_t sequences, int hq, int hk) {
-  const int64_t units = tiles_of(m, sequences, hq / hk, kWideRows) * hk;
+// Splits of the keys of a tile of 128 rows: until every CU has two blocks.
+int wide_splits(int64_t units) {
   if (units >= 384) return 1;
   const int64_t s = 1024 / units;
   return (int)(s < 64 ? s : 64);
 }
 
-template <int DP, bool kExact>
+// ---- few rows: tiles of 32 or 64 -----------------------------------------------------------
+
+// Bound by the cache's bytes.  Each wave of a block streams keys and values of its
+// own, 32 at a time, through its own part of LDS: no barrier stands in the stream,
+// and while a wave computes on one tile, one to three are on their way.  The four
+// waves take every fourth tile and join their sums through LDS at the end.
+//
+// A fixed number of blocks, one or two a CU, shares out the whole batch's work,
+// counted in steps of 128 keys: sequences in order, in each the kv heads, in each
+// the tiles of rows, in each the steps.  A block takes an equal run of steps,
+// wherever it begins and ends, so that contexts of any lengths load the chip
+// evenly.  A tile that is cut between blocks leaves a partial result in each (a
+// block has at most one tile that it continues and one that others continue), and
+// a second launch joins them in order.
+constexpr int kNarrowStep = 128;
+template <int DT>
+constexpr int ring_of() { return DT > 128 ? 1 : 2; }   // tiles of keys, and of values, in a wave's part of LDS
+template <int DT>
+constexpr size_t narrow_bytes() { return 4 * ring_of<DT>() * 2 * 32 * Layout<DT>::row; }
+template <int DT>
+constexpr int narrow_blocks() { return DT > 64 ? 256 : 512; }
+
+// A block's tile that others continue: what the second launch joins.
+struct Cut {
+  int sequence;   // -1: none
+  int first;      // the tile's first row
+  int head;
+  int last;       // the last block that has a part of it
+};
+
+// A sequence's share of the work.
+struct Share {
+  Tile t;
+  Span span;
+  int tiles, steps;
+};
+__device__ __forceinline__ Share share_of(const AttendArgs& a, int s, int group, int size) {
+  Share w{};
+  const int64_t start = a.batch.q_start[s], end = a.batch.q_start[s + 1];
+  if (start < 0 || end <= start || start >= a.m) return w;
+  w.t.sequence = s;
+  w.t.start = (int)start;
+  w.t.end = (int)end;
+  w.t.rows = (int)(((end < a.m ? end : a.m) - start) * group);
+  w.t.length = a.batch.kv_len[s] > 0 ? a.batch.kv_len[s] : 0;
+  w.span = span_of(a, w.t, 0, w.t.rows, group);
+  w.tiles = (w.t.rows + size - 1) / size;
+  const int begin = w.span.lo & ~(kNarrowStep - 1);
+  w.steps = (w.span.hi - begin + kNarrowStep - 1) / kNarrowStep;
+  if (w.steps < 1) w.steps = 1;   // rows that see nothing are written too
+  return w;
+}
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  const uint32_t low = __builtin_amdgcn_readfirstlane((uint32_t)v), high = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return (int64_t)((uint64_t)high << 32 | low);
+}
+__device__ __forceinline__ int64_t wave_sum64(int64_t v) {
+#pragma unroll
+  for (int off = 1; off < 64; off *= 2) v += __shfl_xor(v, off, 64);
+  return uniform(v);
+}
+
+template <int DT, int NT>
+__global__ __launch_bounds__(kThreads, DT > 64 ? 1 : 2)
+void attend_narrow_kernel(AttendArgs a, float* parts, Cut* cuts) {
+  constexpr int kRows = 32 * NT, R = ring_of<DT>();
+  constexpr uint32_t kTile = 32 * Layout<DT>::row;
+  constexpr int N = kTile / 1024;   // loads of a tile
+  extern __shared__ __align__(16) uint8_t lds[];
+  __shared__ int list[kListed];
+  __shared__ float marks[4][kRows][2];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int hk = a.cache.heads, group = a.hq / hk, b = a.batch.sequences;
+  auto work_of = [&](int s) {
+    if (s >= b) return (int64_t)0;
+    const Share w = share_of(a, s, group, kRows);
+    return (int64_t)w.tiles * w.steps * hk;
+  };
+
+  // The block's run of steps [begin, end), and the sequence that holds its first.
+  int64_t total = 0;
+  for (int s0 = 0; s0 < b; s0 += 64) total += wave_sum64(work_of(s0 + lane));
+  const int64_t share = uniform((total + gridDim.x - 1) / gridDim.x);
+  const int64_t from = share * blockIdx.x, to = from + share < total ? from + share : total;
+  Cut cut{-1, 0, 0, 0};
+  int s = 0;
+  int64_t before = 0;   // steps of the sequences before s
+  if (from < to) {
+    for (int s0 = 0; s0 < b; s0 += 64) {
+      int64_t sum = work_of(s0 + lane);
+#pragma unroll
+      for (int off = 1; off < 64; off *= 2) {
+        const int64_t up = __shfl_up(sum, off, 64);
+        if (lane >= off) sum += up;
+      }
+      const int64_t all = uniform(__shfl(sum, 63, 64));
+      if (before + all > from) {
+        const int n = __popcll(__ballot(before + sum <= from));   // sequences of these that end before
+        const int64_t skipped = uniform(__shfl(sum, n > 0 ? n - 1 : 0, 64));
+        before += n > 0 ? skipped : 0;
+        s = s0 + n;
+        break;
+      }
+      before += all;
+    }
+  }
+  s = __builtin_amdgcn_readfirstlane(s);
+
+  uint8_t* mine = lds + wave * (R * 2) * kTile;   // [slot][keys, values]
+  const uint32_t base = lds_offset(mine);
+  Loader<DT, 32> loader;
+  loader.init(lane, 0);
+  Pages pages{list, 0};
+
+  for (int64_t at = from; at < to;) {
+    if (s >= b) break;
+    const Share sh = share_of(a, s, group, kRows);
+    const int64_t here = (int64_t)sh.tiles * sh.steps * hk, in = at - before;
+    if (in >= here) {
+      before += here;
+      ++s;
+      continue;
+    }
+    const int unit = (int)uniform(in / sh.steps), c0 = (int)(in - (int64_t)unit * sh.steps);
+    const int n = (int)(sh.steps - c0 < to - at ? sh.steps - c0 : to - at);
+    const int head = __builtin_amdgcn_readfirstlane(unit / sh.tiles);
+    Tile t = sh.t;
+    t.first = (unit - head * sh.tiles) * kRows;
+    const int live = t.rows - t.first < kRows ? t.rows - t.first : kRows;
+    const int begin = sh.span.lo & ~(kNarrowStep - 1);
+    const int first_position = position_of(t, t.first, group);
+    const int last_position = position_of(t, t.first + live - 1, group);
+    const int last_low = below_window(a, last_position);
+    const bool complete = c0 == 0 && n == sh.steps;
+    if (c0 == 0 && !complete) {
+      const int64_t last = at + sh.steps - 1;   // the tile's last step
+      cut = Cut{s, t.first, head, (int)uniform(last / share)};
+    }
+
+    Wave<DT, NT> w;
+    w.init(a, t, head, group, 0, live, lane);
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // the compiler waits for nothing of it inside the loop
+    const int run = listed_keys(a, kNarrowStep) / kNarrowStep;
+    for (int w0 = c0; w0 < c0 + n; w0 += run) {
+      const int w1 = c0 + n - w0 < run ? c0 + n : w0 + run;
+      wait_loads<0>();   // earlier stores too: what follows counts loads
+      meet();            // the list and the ring are free
+      list_pages(a, t, begin + w0 * kNarrowStep, begin + w1 * kNarrowStep, pages, threadIdx.x, kThreads);
+      wait_loads<0>();
+      meet();
+      // This wave's tiles: 32 keys from begin + 128 (w0 + i) + 32 wave on.
+      const int key_w = begin + w0 * kNarrowStep + 32 * wave;
+      int count = (sh.span.hi - key_w + kNarrowStep - 1) / kNarrowStep;
+      count = count < 0 ? 0 : count < w1 - w0 ? count : w1 - w0;
+      auto issue = [&](int i, int which) {
+        loader.issue(a, pages, head, key_w + i * kNarrowStep, 0, which, base + ((i & (R - 1)) * 2 + which) * kTile, lane);
+      };
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (i < count) {
+          issue(i, 0);
+          issue(i, 1);
+        }
+      }
+      for (int i = 0; i < count; ++i) {
+        const int key0 = key_w + i * kNarrowStep, left = count - i;
+        uint8_t* kt = mine + (i & (R - 1)) * 2 * kTile;
+        uint8_t* vt = kt + kTile;
+        const uint32_t there = (uint32_t)there_of(a, pages, key0, sh.span.hi, 32, lane);
+        const bool none = there == 0 || key0 > last_position;
+        const bool whole = ~there == 0 && key0 + 31 <= first_position && key0 > last_low;
+        // Under way behind this tile's keys: its values and the R - 1 tiles after it.
+        if (R == 2 && left >= 2) wait_loads<3 * N>();
+        else wait_loads<N>();
+        bf16x8 p[NT][2];
+        if (!none) {
+          f32x16 sc[NT][1];
+          w.scores(kt, sc, lane);
+          if (!whole) w.mask(sc, there, key0, lane);
+          w.template weigh<1>(sc, p);
+        }
+        reads_done();
+        if (left > R) issue(i + R, 0);
+        if (R == 2) {
+          if (left >= 3) wait_loads<3 * N>();
+          else if (left == 2) wait_loads<2 * N>();
+          else wait_loads<0>();
+        } else {
+          if (left >= 2) wait_loads<N>();
+          else wait_loads<0>();
+        }
+        if (!none) {
+          int bad = 0;
+          if (!whole) {
+            bad = __any(clean_values<DT, 32>(vt, there, lane));
+            reads_done();
+          }
+          w.template values<1>(vt, p);
+          if (bad) w.add_unseen(a, pages, there, head, key0, 32, lane);
+        }
+        reads_done();
+        if (left > R) issue(i + R, 1);
+      }
+    }
+
+    // The four waves' sums: each scaled to the largest maximum, then added in order,
+    // 32 values of all rows at a time.
+    meet();   // the ring is free
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const float sum = w.sum[i] + other_half(w.sum[i]);
+      if (lane < 32) {
+        marks[wave][32 * i + lane][0] = w.top[i];
+        marks[wave][32 * i + lane][1] = sum;
+      }
+    }
+    meet();
+    float f[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) top = fmaxf(top, marks[v][32 * i + (lane & 31)][0]);
+      f[i] = w.top[i] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(w.top[i] - top);
+    }
+    // Slots of what is continued, block by block, then of what is begun.
+    float* slot = parts + (blockIdx.x + (c0 == 0 ? (int64_t)gridDim.x : 0)) * slot_floats<DT>(kRows);
+    constexpr int kPitch = 36;   // floats of 32 values and room against bank conflicts
+    float* buf = reinterpret_cast<float*>(lds);
+#pragma unroll
+    for (int d0 = 0; d0 < DT / 32; ++d0) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        float* to = buf + (wave * kRows + 32 * i + (lane & 31)) * kPitch + 4 * (lane >> 5);
+        const f32x16& o = w.o[i][d0];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<f32x4*>(to + 8 * j) = f32x4{o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]} * f[i];
+      }
+      meet();
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const int row = 32 * i + threadIdx.x / 8, e = 4 * (threadIdx.x % 8);
+        if (row < live) {
+          f32x4 v = {};
+          float top = -INFINITY, sum = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            v += *reinterpret_cast<const f32x4*>(buf + (k * kRows + row) * kPitch + e);
+            top = fmaxf(top, marks[k][row][0]);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float m = marks[k][row][0];
+            sum += m == -INFINITY ? 0.f : marks[k][row][1] * __builtin_amdgcn_exp2f(m - top);
+          }
+          if (complete) {
+            const int r = t.first + row;
+            const int64_t token = t.start + r / group;
+            const int qhead = head * group + r % group;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            if (32 * d0 + e < a.cache.d) store4(a, token, qhead, 32 * d0 + e, v * inv);
+            if (a.lse && d0 == 0 && e == 0) a.lse[token * a.hq + qhead] = lse_of(top, sum);
+          } else {
+            *reinterpret_cast<f32x4*>(slot + row * DT + 32 * d0 + e) = v;
+            if (d0 == 0 && e == 0) {
+              slot[kRows * DT + 2 * row] = top;
+              slot[kRows * DT + 2 * row + 1] = sum;
+            }
+          }
+        }
+      }
+      meet();
+    }
+    at += n;
+  }
+  if (threadIdx.x == 0) cuts[blockIdx.x] = cut;
+}
+
+// Block x joins the tile that block x of the kernel above began and others went on with.
+template <int DT, int NT>
+__global__ __launch_bounds__(kThreads) void attend_narrow_join_kernel(AttendArgs a, const float* parts, const Cut* cuts) {
+  constexpr int kRows = 32 * NT;
+  const Cut cut = cuts[blockIdx.x];
+  if (cut.sequence < 0) return;
+  const int group = a.hq / a.cache.heads;
+  Tile t = share_of(a, cut.sequence, group, kRows).t;
+  t.first = cut.first;
+  const int row = blockIdx.y * 8 + threadIdx.x / 32;
+  if (row >= t.rows - t.first) return;
+  const int64_t x = blockIdx.x, blocks = gridDim.x;
+  join_row<DT>(a, t, cut.head, group, [&](int z) { return parts + (z ? x + z : blocks + x) * slot_floats<DT>(kRows); },
+               cut.last - (int)x + 1, kRows, row, threadIdx.x % 32);
+}
+
+// ---- which of them -----------------------------------------------------------------------
+
+enum Form { kNarrow32, kNarrow64, kWide };
+// By the rows that a sequence has on average.  (Two tiles of rows of more than 128
+// values do not fit a wave's registers.)
+Form form_of(int64_t m, int64_t sequences, int group, int dim) {
+  const int64_t rows = m * group;
+  if (rows <= 32 * sequences || (dim > 128 && rows <= 64 * sequences)) return kNarrow32;
+  return rows <= 128 * sequences && dim <= 128 ? kNarrow64 : kWide;
+}
+
+template <typename F>
+auto by_dim(int d, F&& f) {
+  if (d <= 64) return f(std::integral_constant<int, 64>{});
+  if (d <= 96) return f(std::integral_constant<int, 96>{});
+  if (d <= 128) return f(std::integral_constant<int, 128>{});
+  if (d <= 192) return f(std::integral_constant<int, 192>{});
+  return f(std::integral_constant<int, 256>{});
+}
+
+template <int DT>
 hipError_t launch_wide(const AttendArgs& a, float* parts, hipStream_t s) {
-  const int hk = a.cache.heads, splits = splits_of(a.m, a.batch.sequences, a.hq, hk);
-  const int64_t units = tiles_of(a.m, a.batch.sequences, a.hq / hk, kWideRows) * hk;
-  constexpr size_t shm = 4 * kStep * DP * 2;
+  const int64_t units = tiles_of(a.m, a.batch.sequences, a.hq / a.cache.heads, kWideRows) * a.cache.heads;
+  const int splits = wide_splits(units);
+  constexpr size_t shm = 4 * kStep * Layout<DT>::row;
   static LdsAllowance seen;
-  const hipError_t ok = allow_dynamic_lds(reinterpret_cast<const void*>(attend_wide_kernel<DP, kExact>), shm, seen);
+  const hipError_t ok = allow_dynamic_lds(reinterpret_cast<const void*>(attend_wide_kernel<DT>), shm, seen);
   if (ok != hipSuccess) return ok;
-  hipLaunchKernelGGL((attend_wide_kernel<DP, kExact>), dim3((unsigned)(units * splits)), dim3(kWideThreads), shm, s, a,
-                     splits, parts);
-  hipError_t e = hipGetLastError();
+  hipLaunchKernelGGL((attend_wide_kernel<DT>), dim3((unsigned)(units * splits)), dim3(kThreads), shm, s, a, splits,
+                     parts);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
-  hipLaunchKernelGGL(attend_join_kernel<DP>, dim3((unsigned)units, kWideRows / 8), dim3(256), 0, s, a, splits, parts);
+  hipLaunchKernelGGL(attend_wide_join_kernel<DT>, dim3((unsigned)units, kWideRows / 8), dim3(kThreads), 0, s, a, splits,
+                     parts);
+  return hipGetLastError();
+}
+
+template <int DT, int NT>
+hipError_t launch_narrow(const AttendArgs& a, float* parts, hipStream_t s) {
+  constexpr int blocks = narrow_blocks<DT>();
+  constexpr size_t shm = narrow_bytes<DT>();
+  Cut* cuts = reinterpret_cast<Cut*>(parts + 2 * blocks * slot_floats<DT>(32 * NT));
+  static LdsAllowance seen;
+  const hipError_t ok = allow_dynamic_lds(reinterpret_cast<const void*>(attend_narrow_kernel<DT, NT>), shm, seen);
+  if (ok != hipSuccess) return ok;
+  hipLaunchKernelGGL((attend_narrow_kernel<DT, NT>), dim3(blocks), dim3(kThreads), shm, s, a, parts, cuts);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((attend_narrow_join_kernel<DT, NT>), dim3(blocks, 4 * NT), dim3(kThreads), 0, s, a, parts, cuts);
   return hipGetLastError();
 }
 
 }  // namespace
 
 int64_t attend_workspace_bytes(int64_t m, int64_t sequences, int32_t hq, int32_t hk, int32_t d) {
-  const int splits = splits_of(m, sequences, hq, hk);
-  if (splits == 1) return 0;
-  const int dp = padded(d);
-  return tiles_of(m, sequences, hq / hk, kWideRows) * hk * splits * kWideRows * (dp + 2) * 4;
+  return by_dim(d, [&](auto dim) -> int64_t {
+    constexpr int DT = decltype(dim)::value;
+    const Form form = form_of(m, sequences, hq / hk, DT);
+    if (form != kWide) {
+      const int64_t blocks = narrow_blocks<DT>();
+      return blocks * (2 * 4 * slot_floats<DT>(form == kNarrow32 ? 32 : 64) + (int64_t)sizeof(Cut));
+    }
+    const int64_t units = tiles_of(m, sequences, hq / hk, kWideRows) * hk;
+    const int splits = wide_splits(units);
+    return splits == 1 ? 0 : units * splits * slot_floats<DT>(kWideRows) * 4;
+  });
 }
 
 hipError_t launch_attend(const AttendArgs& a, void* ws, hipStream_t s) {
   float* parts = static_cast<float*>(ws);
-  switch (a.cache.d) {
-    case 64: return launch_wide<64, true>(a, parts, s);
-    case 128: return launch_wide<128, true>(a, parts, s);
-    case 256: return launch_wide<256, true>(a, parts, s);
-  }
-  if (a.cache.d < 64) return launch_wide<64, false>(a, parts, s);
-  if (a.cache.d < 128) return launch_wide<128, false>(a, parts, s);
-  return launch_wide<256, false>(a, parts, s);
+  return by_dim(a.cache.d, [&](auto dim) {
+    constexpr int DT = decltype(dim)::value;
+    const Form form = form_of(a.m, a.batch.sequences, a.hq / a.cache.heads, DT);
+    if (form == kNarrow32) return launch_narrow<DT, 1>(a, parts, s);
+    if constexpr (DT <= 128)
+      if (form == kNarrow64) return launch_narrow<DT, 2>(a, parts, s);
+    return launch_wide<DT>(a, parts, s);
+  });
 }
 
 }  // namespace q3
