@@ -447,21 +447,36 @@ __device__ __forceinline__ void store4(const AttendArgs& a, int64_t token, int q
       u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
 }
 
-// Row `row` (of `rows`) of a tile from its `count` partial results slot(0).., in
-// order, by 32 lanes of which this is l.
+// Row `row` (of `rows`) of a tile from its `count` partial results slot(0)..: a
+// wave, whose halves take every other one and add up in that order.
 template <int DT, typename Slot>
 __device__ __forceinline__ void join_row(const AttendArgs& a, const Tile& t, int head, int group, Slot&& slot, int count,
-                                         int rows, int row, int l) {
+                                         int rows, int row, int lane) {
+  const int half = lane >> 5, l = lane & 31;
+  const float* marks = nullptr;
   float top = -INFINITY, sum = 0.f;
-  for (int z = 0; z < count; ++z) top = fmaxf(top, slot(z)[rows * DT + 2 * row]);
-  f32x4 o[(DT + 127) / 128] = {};
-  for (int z = 0; z < count; ++z) {
+  for (int z = lane; z < count; z += 64) {
+    marks = slot(z) + rows * DT + 2 * row;
+    top = fmaxf(top, marks[0]);
+  }
+#pragma unroll
+  for (int off = 1; off < 64; off *= 2) top = fmaxf(top, __shfl_xor(top, off, 64));
+  for (int z = lane; z < count; z += 64) {
+    marks = slot(z) + rows * DT + 2 * row;
+    if (marks[0] > -INFINITY) sum += marks[1] * __builtin_amdgcn_exp2f(marks[0] - top);
+    else sum += marks[1];   // 0, or NaN
+  }
+#pragma unroll
+  for (int off = 1; off < 64; off *= 2) sum += __shfl_xor(sum, off, 64);
+  constexpr int V = (DT + 127) / 128;
+  f32x4 o[V] = {};
+#pragma unroll 8
+  for (int z = half; z < count; z += 2) {
     const float* p = slot(z);
     const float m = p[rows * DT + 2 * row];
     const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
-    sum += f * p[rows * DT + 2 * row + 1];
 #pragma unroll
-    for (int i = 0; i < (DT + 127) / 128; ++i)
+    for (int i = 0; i < V; ++i)
       if (128 * i + 4 * l < DT) o[i] += f * *reinterpret_cast<const f32x4*>(p + row * DT + 128 * i + 4 * l);
   }
   const int r = t.first + row;
@@ -469,18 +484,22 @@ __device__ __forceinline__ void join_row(const AttendArgs& a, const Tile& t, int
   const int qhead = head * group + r % group;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-  for (int i = 0; i < (DT + 127) / 128; ++i)
-    if (128 * i + 4 * l < a.cache.d) store4(a, token, qhead, 128 * i + 4 * l, o[i] * inv);
-  if (a.lse && l == 0) a.lse[token * a.hq + qhead] = lse_of(top, sum);
+  for (int i = 0; i < V; ++i) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[i][e] += other_half(o[i][e]);
+    if (half == 0 && 128 * i + 4 * l < a.cache.d) store4(a, token, qhead, 128 * i + 4 * l, o[i] * inv);
+  }
+  if (a.lse && lane == 0) a.lse[token * a.hq + qhead] = lse_of(top, sum);
 }
 
 // ---- many rows: tiles of 128 -----------------------------------------------------------
 
 constexpr int kWideRows = 128, kStep = 64, kThreads = 256;
 
-// Parts that a tile's steps go to: at most `splits`.
+// Parts that a tile's steps go to: at most `splits`, of four steps at least.
 __device__ __forceinline__ int parts_of(int steps, int splits) {
-  return steps < splits ? (steps > 0 ? steps : 1) : splits;
+  const int most = (steps + 3) / 4;
+  return most < splits ? (most > 0 ? most : 1) : splits;
 }
 __device__ __forceinline__ int steps_of(const Span& span) {
   return (span.hi - (span.lo & ~(kStep - 1)) + kStep - 1) / kStep;
@@ -498,13 +517,13 @@ void attend_wide_kernel(AttendArgs a, int splits, float* parts) {
   const int hk = a.cache.heads, group = a.hq / hk;
 
   // Contiguous runs of (head, tile) to each XCD: tiles that read the same keys share an L2.
-  const int64_t tiles = tiles_of(a.m, a.batch.sequences, group, kWideRows);
-  const int64_t total = tiles * hk, id = blockIdx.x % total;
-  const int z = (int)(blockIdx.x / total);
-  const int64_t per = total >> 3, rem = total & 7, xcd = id & 7;
-  const int64_t unit = xcd * per + (xcd < rem ? xcd : rem) + (id >> 3);
-  const int head = __builtin_amdgcn_readfirstlane((int)(unit / tiles));
-  const int64_t tile = tiles - 1 - unit % tiles;     // the long ones of a chunk first
+  const uint32_t tiles = (uint32_t)tiles_of(a.m, a.batch.sequences, group, kWideRows);
+  const uint32_t total = tiles * hk;   // below 2^24
+  const int z = __builtin_amdgcn_readfirstlane(blockIdx.x / total);
+  const uint32_t id = blockIdx.x - z * total, per = total >> 3, rem = total & 7, xcd = id & 7;
+  const uint32_t unit = xcd * per + (xcd < rem ? xcd : rem) + (id >> 3);
+  const int head = __builtin_amdgcn_readfirstlane(unit / tiles);
+  const int64_t tile = tiles - 1 - (unit - head * tiles);     // the long ones of a chunk first
   const Tile t = find_tile(a, tile, group, kWideRows, lane);
   if (t.sequence == a.batch.sequences) return;
   const int live = t.rows - t.first < kWideRows ? t.rows - t.first : kWideRows;
@@ -516,7 +535,6 @@ void attend_wide_kernel(AttendArgs a, int splits, float* parts) {
 
   Wave<DT, 1> w;
   w.init(a, t, head, group, 32 * wave, live, lane);
-  __builtin_amdgcn_s_waitcnt(0x0F70);   // the compiler waits for nothing of it inside the loop
   const int first_position = position_of(t, t.first, group);   // of the tile's rows
   const int last_low = below_window(a, position_of(t, t.first + live - 1, group));
   Loader<DT, 16> loader;
@@ -535,6 +553,7 @@ void attend_wide_kernel(AttendArgs a, int splits, float* parts) {
     const int w1 = s1 - w0 < run ? s1 : w0 + run;
     meet();   // the list and the buffers are free
     list_pages(a, t, begin + w0 * kStep, begin + w1 * kStep, pages, threadIdx.x, kThreads);
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // the compiler knows that queries are here (and waits in the loop for nothing)
     meet();
     issue(w0);
     for (int s = w0; s < w1; ++s) {
@@ -596,21 +615,20 @@ void attend_wide_kernel(AttendArgs a, int splits, float* parts) {
   }
 }
 
-// The parts of a tile's rows: eight rows a block, 32 lanes a row.
+// The parts of a tile's rows, a wave a row.
 template <int DT>
 __global__ __launch_bounds__(kThreads) void attend_wide_join_kernel(AttendArgs a, int splits, const float* parts) {
   const int hk = a.cache.heads, group = a.hq / hk;
-  const int64_t tile = blockIdx.x / hk;
-  const int head = blockIdx.x % hk;
+  const int tile = __builtin_amdgcn_readfirstlane(blockIdx.x / (uint32_t)hk), head = blockIdx.x - tile * hk;
   const Tile t = find_tile(a, tile, group, kWideRows, threadIdx.x & 63);
   if (t.sequence == a.batch.sequences) return;
   const int live = t.rows - t.first < kWideRows ? t.rows - t.first : kWideRows;
   const int count = parts_of(steps_of(span_of(a, t, t.first, t.first + live, group)), splits);
-  const int row = blockIdx.y * 8 + threadIdx.x / 32;
-  if (count == 1 || row >= live) return;
-  const float* first = parts + (tile * hk + head) * splits * slot_floats<DT>(kWideRows);
-  join_row<DT>(a, t, head, group, [&](int z) { return first + z * slot_floats<DT>(kWideRows); }, count, kWideRows, row,
-               threadIdx.x % 32);
+  if (count == 1) return;
+  const float* first = parts + ((int64_t)tile * hk + head) * splits * slot_floats<DT>(kWideRows);
+  for (int row = blockIdx.y * 4 + threadIdx.x / 64; row < live; row += 4 * gridDim.y)
+    join_row<DT>(a, t, head, group, [&](int z) { return first + z * slot_floats<DT>(kWideRows); }, count, kWideRows, row,
+                 threadIdx.x & 63);
 }
 
 // Splits of the keys of a tile of 128 rows: until every CU has two blocks.
@@ -700,32 +718,34 @@ void attend_narrow_kernel(AttendArgs a, float* parts, Cut* cuts) {
     return (int64_t)w.tiles * w.steps * hk;
   };
 
-  // The block's run of steps [begin, end), and the sequence that holds its first.
-  int64_t total = 0;
-  for (int s0 = 0; s0 < b; s0 += 64) total += wave_sum64(work_of(s0 + lane));
-  const int64_t share = uniform((total + gridDim.x - 1) / gridDim.x);
+  // The block's run of steps [from, to), and the sequence that holds its first.
+  constexpr int blocks = narrow_blocks<DT>();
+  auto running = [&](int64_t v) {   // sums of lanes 0..lane
+#pragma unroll
+    for (int off = 1; off < 64; off *= 2) {
+      const int64_t up = __shfl_up(v, off, 64);
+      if (lane >= off) v += up;
+    }
+    return v;
+  };
+  int64_t sums = running(work_of(lane)), total = uniform(__shfl(sums, 63, 64));   // of the first 64 sequences
+  for (int s0 = 64; s0 < b; s0 += 64) total += wave_sum64(work_of(s0 + lane));
+  const int64_t share = (total + blocks - 1) / blocks;
   const int64_t from = share * blockIdx.x, to = from + share < total ? from + share : total;
   Cut cut{-1, 0, 0, 0};
   int s = 0;
   int64_t before = 0;   // steps of the sequences before s
-  if (from < to) {
-    for (int s0 = 0; s0 < b; s0 += 64) {
-      int64_t sum = work_of(s0 + lane);
-#pragma unroll
-      for (int off = 1; off < 64; off *= 2) {
-        const int64_t up = __shfl_up(sum, off, 64);
-        if (lane >= off) sum += up;
-      }
-      const int64_t all = uniform(__shfl(sum, 63, 64));
-      if (before + all > from) {
-        const int n = __popcll(__ballot(before + sum <= from));   // sequences of these that end before
-        const int64_t skipped = uniform(__shfl(sum, n > 0 ? n - 1 : 0, 64));
-        before += n > 0 ? skipped : 0;
-        s = s0 + n;
-        break;
-      }
-      before += all;
+  for (int s0 = 0; from < to && s0 < b; s0 += 64) {
+    if (s0) sums = running(work_of(s0 + lane));
+    const int64_t all = uniform(__shfl(sums, 63, 64));
+    if (before + all > from) {
+      const int n = __popcll(__ballot(before + sums <= from));   // sequences of these that end before
+      const int64_t skipped = uniform(__shfl(sums, n > 0 ? n - 1 : 0, 64));
+      before += n > 0 ? skipped : 0;
+      s = s0 + n;
+      break;
     }
+    before += all;
   }
   s = __builtin_amdgcn_readfirstlane(s);
 
@@ -744,7 +764,9 @@ void attend_narrow_kernel(AttendArgs a, float* parts, Cut* cuts) {
       ++s;
       continue;
     }
-    const int unit = (int)uniform(in / sh.steps), c0 = (int)(in - (int64_t)unit * sh.steps);
+    const int unit = in >> 32 ? (int)uniform(in / sh.steps)
+                              : (int)__builtin_amdgcn_readfirstlane((uint32_t)in / (uint32_t)sh.steps);
+    const int c0 = (int)(in - (int64_t)unit * sh.steps);
     const int n = (int)(sh.steps - c0 < to - at ? sh.steps - c0 : to - at);
     const int head = __builtin_amdgcn_readfirstlane(unit / sh.tiles);
     Tile t = sh.t;
@@ -762,14 +784,14 @@ void attend_narrow_kernel(AttendArgs a, float* parts, Cut* cuts) {
 
     Wave<DT, NT> w;
     w.init(a, t, head, group, 0, live, lane);
-    __builtin_amdgcn_s_waitcnt(0x0F70);   // the compiler waits for nothing of it inside the loop
     const int run = listed_keys(a, kNarrowStep) / kNarrowStep;
     for (int w0 = c0; w0 < c0 + n; w0 += run) {
       const int w1 = c0 + n - w0 < run ? c0 + n : w0 + run;
-      wait_loads<0>();   // earlier stores too: what follows counts loads
-      meet();            // the list and the ring are free
+      meet();   // the list and the ring are free
       list_pages(a, t, begin + w0 * kNarrowStep, begin + w1 * kNarrowStep, pages, threadIdx.x, kThreads);
-      wait_loads<0>();
+      // The stream counts its loads: nothing else is under way, and the compiler
+      // knows that queries are here (it would wait for them inside the loop).
+      __builtin_amdgcn_s_waitcnt(0x0F70);
       meet();
       // This wave's tiles: 32 keys from begin + 128 (w0 + i) + 32 wave on.
       const int key_w = begin + w0 * kNarrowStep + 32 * wave;
@@ -909,11 +931,11 @@ __global__ __launch_bounds__(kThreads) void attend_narrow_join_kernel(AttendArgs
   const int group = a.hq / a.cache.heads;
   Tile t = share_of(a, cut.sequence, group, kRows).t;
   t.first = cut.first;
-  const int row = blockIdx.y * 8 + threadIdx.x / 32;
-  if (row >= t.rows - t.first) return;
+  const int live = t.rows - t.first < kRows ? t.rows - t.first : kRows;
   const int64_t x = blockIdx.x, blocks = gridDim.x;
-  join_row<DT>(a, t, cut.head, group, [&](int z) { return parts + (z ? x + z : blocks + x) * slot_floats<DT>(kRows); },
-               cut.last - (int)x + 1, kRows, row, threadIdx.x % 32);
+  for (int row = blockIdx.y * 4 + threadIdx.x / 64; row < live; row += 4 * gridDim.y)
+    join_row<DT>(a, t, cut.head, group, [&](int z) { return parts + (z ? x + z : blocks + x) * slot_floats<DT>(kRows); },
+                 cut.last - (int)x + 1, kRows, row, threadIdx.x & 63);
 }
 
 // ---- which of them -----------------------------------------------------------------------
@@ -948,7 +970,7 @@ hipError_t launch_wide(const AttendArgs& a, float* parts, hipStream_t s) {
                      parts);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
-  hipLaunchKernelGGL(attend_wide_join_kernel<DT>, dim3((unsigned)units, kWideRows / 8), dim3(kThreads), 0, s, a, splits,
+  hipLaunchKernelGGL(attend_wide_join_kernel<DT>, dim3((unsigned)units, kWideRows / 4), dim3(kThreads), 0, s, a, splits,
                      parts);
   return hipGetLastError();
 }
@@ -964,7 +986,7 @@ hipError_t launch_narrow(const AttendArgs& a, float* parts, hipStream_t s) {
   hipLaunchKernelGGL((attend_narrow_kernel<DT, NT>), dim3(blocks), dim3(kThreads), shm, s, a, parts, cuts);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((attend_narrow_join_kernel<DT, NT>), dim3(blocks, 4 * NT), dim3(kThreads), 0, s, a, parts, cuts);
+  hipLaunchKernelGGL((attend_narrow_join_kernel<DT, NT>), dim3(blocks, 8 * NT), dim3(kThreads), 0, s, a, parts, cuts);
   return hipGetLastError();
 }
 

@@ -10,10 +10,11 @@
 // Both are bound by memory: 4 bytes in and 2 out per value (backward 4 and 2 or
 // 4 in, 2 out).  A token is a block of 256 threads; a head belongs to a group of L
 // lanes with 8 values each (L the power of two with 8 L >= d), so the mean is a
-// few lane exchanges and loads and stores are 32 and 16 bytes a lane.  The
-// token's angles are formed once by the block: position * freq in 64 bits,
-// reduced there to [-pi, pi], where a 32-bit sine is good to 2^-22 whatever the
-// position.
+// few lane exchanges.  A lane's values are two runs of four: where halves are
+// rotated, four values and their four partners, so that the rotation stays in the
+// lane (a half that is no multiple of four goes through LDS instead).  The
+// token's angles are formed once by the block while the first heads' loads are
+// under way.
 #include <type_traits>
 
 #include "q3_device.h"
@@ -29,46 +30,83 @@ constexpr int kThreads = 256;
 // Values of the token's angles; [0] cosines, [1] sines.
 typedef float Turn[2][128];
 
+// Cosine and sine of position * freq.  The angle is taken to turns in 64 bits with
+// the product's and 1 / (2 pi)'s own remainders, to its place in a quarter turn, and
+// from there by the series of both up to the eleventh power (left over below
+// 2^-29 at pi / 4).
 __device__ __forceinline__ void angle_of(double position, float freq, float& c, float& s) {
-  constexpr double kTurns = 0.15915494309189535;              // 1 / (2 pi)
-  constexpr double kHigh = 6.283185307179586, kLow = 2.4492935982947064e-16;   // 2 pi
-  double a = position * (double)freq;
-  const double k = rint(a * kTurns);
-  a = fma(-k, kLow, fma(-k, kHigh, a));
-  sincosf((float)a, &s, &c);
+  constexpr double kTurns = 0.15915494309189535, kRest = -9.839338337591215e-18;   // 1 / (2 pi)
+  const double a = position * (double)freq, t = a * kTurns;
+  const double turn = (t - rint(t)) + fma(a, kRest, fma(a, kTurns, -t));
+  const double q = rint(4.0 * turn);
+  const float x = (float)((turn - 0.25 * q) * 6.283185307179586), y = x * x;
+  const float sn = x + x * y * (-1.f / 6 + y * (1.f / 120 + y * (-1.f / 5040 + y * (1.f / 362880 - y * (1.f / 39916800)))));
+  const float cs = 1.f + y * (-0.5f + y * (1.f / 24 + y * (-1.f / 720 + y * (1.f / 40320 - y * (1.f / 3628800)))));
+  const int n = (int)q;
+  c = n & 1 ? sn : cs;
+  s = n & 1 ? cs : sn;
+  c = (n + 1) & 2 ? -c : c;
+  s = n & 2 ? -s : s;
 }
 
 struct Vec8 {
   float v[8];
 };
-__device__ __forceinline__ Vec8 load8(const float* p) {
-  const f32x4 a = reinterpret_cast<const f32x4*>(p)[0], b = reinterpret_cast<const f32x4*>(p)[1];
+// The lane's values of a head, at e[0].. and e[1]...
+struct Places {
+  int e[2];
+  bool low;    // halves: e[1] are the partners of e[0]; angles from e[0] on
+  bool live;   // inside the head
+};
+template <int L>
+__device__ __forceinline__ Places places(int d, int rot, bool interleaved) {
+  const int l = threadIdx.x % L;
+  Places p;
+  p.low = !interleaved && rot % 8 == 0 && l < rot / 8;
+  p.live = l < d / 8;
+  if (p.low) {
+    p.e[0] = 4 * l;
+    p.e[1] = rot / 2 + 4 * l;
+  } else if (interleaved) {
+    p.e[0] = 4 * l;
+    p.e[1] = d / 2 + 4 * l;
+  } else {
+    p.e[0] = 8 * l;
+    p.e[1] = 8 * l + 4;
+  }
+  return p;
+}
+__device__ __forceinline__ Vec8 load8(const float* p, const Places& at) {
+  const f32x4 a = *reinterpret_cast<const f32x4*>(p + at.e[0]), b = *reinterpret_cast<const f32x4*>(p + at.e[1]);
   return {{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
 }
-__device__ __forceinline__ Vec8 load8(const uint16_t* p) {
-  const u32x4 u = *reinterpret_cast<const u32x4*>(p);
+__device__ __forceinline__ Vec8 load8(const uint16_t* p, const Places& at) {
   Vec8 o;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    o.v[2 * i] = __builtin_bit_cast(float, u[i] << 16);
-    o.v[2 * i + 1] = __builtin_bit_cast(float, u[i] & 0xFFFF0000u);
+  for (int h = 0; h < 2; ++h) {
+    const u32x2 u = *reinterpret_cast<const u32x2*>(p + at.e[h]);
+    o.v[4 * h] = __builtin_bit_cast(float, u.x << 16);
+    o.v[4 * h + 1] = __builtin_bit_cast(float, u.x & 0xFFFF0000u);
+    o.v[4 * h + 2] = __builtin_bit_cast(float, u.y << 16);
+    o.v[4 * h + 3] = __builtin_bit_cast(float, u.y & 0xFFFF0000u);
   }
   return o;
 }
-__device__ __forceinline__ void store8(uint16_t* p, const Vec8& x) {
-  u32x4 u;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const bf16x2 b = {static_cast<__bf16>(x.v[2 * i]), static_cast<__bf16>(x.v[2 * i + 1])};
-    u[i] = __builtin_bit_cast(uint32_t, b);
-  }
-  *reinterpret_cast<u32x4*>(p) = u;
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const bf16x2 v = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
+  return __builtin_bit_cast(uint32_t, v);
 }
-// A weight's eight values at e (4-byte aligned); ones without one.
-__device__ __forceinline__ Vec8 weight8(const float* w, int e, bool live) {
+__device__ __forceinline__ void store8(uint16_t* p, const Places& at, const Vec8& x) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    *reinterpret_cast<u32x2*>(p + at.e[h]) =
+        u32x2{pack_bf16(x.v[4 * h], x.v[4 * h + 1]), pack_bf16(x.v[4 * h + 2], x.v[4 * h + 3])};
+}
+// A weight's values (4-byte aligned); ones without one.
+__device__ __forceinline__ Vec8 weight8(const float* w, const Places& at) {
   Vec8 o;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) o.v[i] = w && live ? w[e + i] : 1.f;
+  for (int i = 0; i < 8; ++i) o.v[i] = w && at.live ? w[at.e[i / 4] + i % 4] : 1.f;
   return o;
 }
 
@@ -79,29 +117,40 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// The rotation of a lane's eight values, those from e = 8 (lane % L) on; sign -1
-// turns back.  `swap` is the wave's own 512 floats of LDS.  Every lane of the
-// wave comes here.
+// The rotation of a lane's values; sign -1 turns back.  `swap` is the wave's own
+// 512 floats of LDS.  Every lane of the wave comes here.
 template <int L>
-__device__ __forceinline__ void rotate(Vec8& x, int rot, bool interleaved, const Turn& turn, float sign, float* swap,
-                                       int lane) {
-  const int e = 8 * (lane % L);
+__device__ __forceinline__ void rotate(Vec8& x, const Places& at, int rot, bool interleaved, const Turn& turn, float sign,
+                                       float* swap, int lane) {
+  if (rot == 0) return;
   if (interleaved) {
-    if (e >= rot) return;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int j = at.e[h] + 2 * i;
+        if (j < rot) {   // rot is even
+          const float c = turn[0][j / 2], s = sign * turn[1][j / 2];
+          const float a = x.v[4 * h + 2 * i], b = x.v[4 * h + 2 * i + 1];
+          x.v[4 * h + 2 * i] = a * c - b * s;
+          x.v[4 * h + 2 * i + 1] = b * c + a * s;
+        }
+      }
+    return;
+  }
+  if (rot % 8 == 0) {
+    if (!at.low) return;
+    const f32x4 c = *reinterpret_cast<const f32x4*>(&turn[0][at.e[0]]), s = *reinterpret_cast<const f32x4*>(&turn[1][at.e[0]]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (e + 2 * i < rot) {   // rot is even
-        const float c = turn[0][e / 2 + i], s = sign * turn[1][e / 2 + i];
-        const float a = x.v[2 * i], b = x.v[2 * i + 1];
-        x.v[2 * i] = a * c - b * s;
-        x.v[2 * i + 1] = b * c + a * s;
-      }
+      const float a = x.v[i], b = x.v[4 + i], t = sign * s[i];
+      x.v[i] = a * c[i] - b * t;
+      x.v[4 + i] = b * c[i] + a * t;
     }
     return;
   }
-  // Halves: value j goes with j + rot/2, which stands in another lane.
+  // Value j goes with j + rot/2, which stands in another lane (e[1] = e[0] + 4 here).
   const int half = rot / 2;
-  if (rot == 0) return;
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -112,19 +161,20 @@ __device__ __forceinline__ void rotate(Vec8& x, int rot, bool interleaved, const
   const float* head = swap + (lane / L) * (8 * L);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int j = e + i;
+    const int j = at.e[0] + i;
     if (j < rot) {
       const bool low = j < half;
-      const int at = low ? j : j - half;
-      const float other = head[low ? j + half : at];
-      const float c = turn[0][at], s = low ? -sign * turn[1][at] : sign * turn[1][at];
+      const int k = low ? j : j - half;
+      const float other = head[low ? j + half : k];
+      const float c = turn[0][k], s = low ? -sign * turn[1][k] : sign * turn[1][k];
       x.v[i] = x.v[i] * c + other * s;
     }
   }
 }
 
 // One token per block (blockIdx.x); blockIdx.y takes every gridDim.y-th run of
-// 256 / L heads.
+// 256 / L heads, three of them at a time.
+constexpr int kAhead = 3;
 template <int L>
 __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(RopeArgs a) {
   __shared__ __align__(16) Turn turn;
@@ -132,9 +182,21 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(RopeArgs a) {
   constexpr int kHeads = kThreads / L;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t row = a.first + blockIdx.x;
-  const int e = 8 * (threadIdx.x % L);
-  const bool live = e < a.d;
-  const int heads = a.hq + 2 * a.hk;
+  const Places at = places<L>(a.d, a.rot, a.interleaved);
+  const int heads = a.hq + 2 * a.hk, stride = gridDim.y * kHeads;
+  const float* src = a.qkv + row * a.ld;
+  Vec8 x[kAhead];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int h = h0 + k * stride + threadIdx.x / L;
+      x[k] = Vec8{};
+      if (at.live && h < heads) x[k] = load8(src + h * a.d, at);
+    }
+  };
+  const int first = blockIdx.y * kHeads;
+  load(first);
+  const Vec8 wq = weight8(a.wq, at), wk = weight8(a.wk, at);
 
   int64_t position = 0, page = -1;
   if (a.batch.sequences) {
@@ -148,35 +210,35 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(RopeArgs a) {
   for (int t = threadIdx.x; t < a.rot / 2; t += kThreads) angle_of((double)position, a.freq[t], turn[0][t], turn[1][t]);
   __syncthreads();
 
-  for (int h0 = blockIdx.y * kHeads; h0 < heads; h0 += gridDim.y * kHeads) {
-    const int h = h0 + threadIdx.x / L;
-    const bool here = live && h < heads;
-    Vec8 x = {};
-    if (here) x = load8(a.qkv + row * a.ld + (int64_t)h * a.d + e);
-    const bool query = h < a.hq, value = h >= a.hq + a.hk;
-    const float* w = value ? nullptr : query ? a.wq : a.wk;
-    float q = 0.f;
+  for (int h0 = first; h0 < heads; h0 += kAhead * stride) {
+    if (h0 != first) load(h0);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q += x.v[i] * x.v[i];
-    const float s = rsqrtf(group_sum<L>(q) / (float)a.d + a.eps);
-    Vec8 o = x;
-    if (w) {
-      const Vec8 g = weight8(w, e, here);
+    for (int k = 0; k < kAhead; ++k) {
+      if (h0 + k * stride >= heads) break;   // the whole block
+      const int h = h0 + k * stride + threadIdx.x / L;
+      const bool query = h < a.hq, value = h >= a.hq + a.hk;
+      float q = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o.v[i] = x.v[i] * s * g.v[i];
-    }
-    rotate<L>(o, a.rot, a.interleaved, turn, 1.f, swap[wave], lane);
-    if (!here) continue;
-    if (query) {
-      store8(a.q + row * a.ldq + (int64_t)h * a.d + e, o);
-    } else {
-      const int kh = value ? h - a.hq - a.hk : h - a.hq;
-      if (value) o = x;
-      if (!a.batch.sequences) {
-        store8((value ? a.v + row * a.ldv : a.k + row * a.ldk) + (int64_t)kh * a.d + e, o);
-      } else if (page >= 0) {
-        uint16_t* to = (value ? a.cache.v : a.cache.k) + page * a.cache.page_stride;
-        store8(to + (((int64_t)kh << a.cache.shift) + inside) * a.d + e, o);
+      for (int i = 0; i < 8; ++i) q += x[k].v[i] * x[k].v[i];
+      const float s = rsqrtf(group_sum<L>(q) / (float)a.d + a.eps);
+      Vec8 o = x[k];
+      if (query ? a.wq : a.wk) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o.v[i] = x[k].v[i] * s * (query ? wq.v[i] : wk.v[i]);
+      }
+      rotate<L>(o, at, a.rot, a.interleaved, turn, 1.f, swap[wave], lane);
+      if (!at.live || h >= heads) continue;
+      if (query) {
+        store8(a.q + row * a.ldq + h * a.d, at, o);
+      } else {
+        const int kh = value ? h - a.hq - a.hk : h - a.hq;
+        if (value) o = x[k];
+        if (!a.batch.sequences) {
+          store8((value ? a.v + row * a.ldv : a.k + row * a.ldk) + kh * a.d, at, o);
+        } else if (page >= 0) {
+          uint16_t* to = (value ? a.cache.v : a.cache.k) + page * a.cache.page_stride;
+          store8(to + (((int64_t)kh << a.cache.shift) + inside) * a.d, at, o);
+        }
       }
     }
   }
@@ -185,17 +247,32 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(RopeArgs a) {
 // Blocks walk the tokens; a thread adds up the weight gradients of its eight
 // values over its heads, the block's groups are added in order at the end.
 template <int L, typename E>
-__global__ __launch_bounds__(kThreads) void qk_norm_rope_back_kernel(RopeBackArgs a) {
+__global__ __launch_bounds__(kThreads, 4) void qk_norm_rope_back_kernel(RopeBackArgs a) {
   __shared__ __align__(16) Turn turn[2];
   __shared__ __align__(16) float swap[kThreads / 64][512];
   constexpr int kHeads = kThreads / L;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int e = 8 * (threadIdx.x % L);
-  const bool live = e < a.d;
+  const Places at = places<L>(a.d, a.rot, a.interleaved);
   const int heads = a.hq + 2 * a.hk;
   Vec8 sums[2] = {};
-  const Vec8 wq = weight8(a.wq, e, live), wk = weight8(a.wk, e, live);
+  const Vec8 wq = weight8(a.wq, at), wk = weight8(a.wk, at);
+  struct Head {
+    Vec8 g, x;
+  };
+  // A head's gradient and, where it is normed, its values.
+  auto load = [&](int64_t row, int h) {
+    Head o = {};
+    if (!at.live || h >= heads) return o;
+    const bool query = h < a.hq, value = h >= a.hq + a.hk;
+    const void* d = query ? a.dq : value ? a.dv : a.dk;
+    const int64_t ld = query ? a.ld_dq : value ? a.ld_dv : a.ld_dk;
+    const int k = query ? h : value ? h - a.hq - a.hk : h - a.hq;
+    if (d) o.g = load8(static_cast<const E*>(d) + row * ld + k * a.d, at);
+    if (!value && (query ? a.wq : a.wk)) o.x = load8(a.qkv + row * a.ld + h * a.d, at);
+    return o;
+  };
   int parity = 0;
+  Head next = load(blockIdx.x, threadIdx.x / L);
   for (int64_t row = blockIdx.x; row < a.m; row += a.groups, parity ^= 1) {
     // The other buffer's readers are a barrier behind.
     for (int t = threadIdx.x; t < a.rot / 2; t += kThreads)
@@ -203,23 +280,14 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_back_kernel(RopeBackArg
     __syncthreads();
     for (int h0 = 0; h0 < heads; h0 += kHeads) {
       const int h = h0 + threadIdx.x / L;
-      const bool here = live && h < heads;
       const bool query = h < a.hq, value = h >= a.hq + a.hk;
-      Vec8 g = {};
-      if (here) {
-        if (query) {
-          if (a.dq) g = load8(static_cast<const E*>(a.dq) + row * a.ld_dq + (int64_t)h * a.d + e);
-        } else if (!value) {
-          if (a.dk) g = load8(static_cast<const E*>(a.dk) + row * a.ld_dk + (int64_t)(h - a.hq) * a.d + e);
-        } else if (a.dv) {
-          g = load8(static_cast<const E*>(a.dv) + row * a.ld_dv + (int64_t)(h - a.hq - a.hk) * a.d + e);
-        }
-      }
+      Head cur = next;
+      // The next heads', or the next token's first, while these are worked on.
+      const bool more = h0 + kHeads < heads;
+      if (more || row + a.groups < a.m) next = load(more ? row : row + a.groups, (more ? h0 + kHeads : 0) + threadIdx.x / L);
       const bool norm = !value && (query ? a.wq : a.wk);
-      Vec8 x = {};
-      if (here && norm) x = load8(a.qkv + row * a.ld + (int64_t)h * a.d + e);
-      Vec8 dn = g;
-      rotate<L>(dn, a.rot, a.interleaved, turn[parity], -1.f, swap[wave], lane);
+      Vec8 x = cur.x, g = cur.g, dn = g;
+      rotate<L>(dn, at, a.rot, a.interleaved, turn[parity], -1.f, swap[wave], lane);
       float q = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) q += x.v[i] * x.v[i];
@@ -233,7 +301,7 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_back_kernel(RopeBackArg
         c += b.v[i] * x.v[i];
       }
       c = group_sum<L>(c) / (float)a.d;
-      if (!here) continue;
+      if (!at.live || h >= heads) continue;
       if (norm) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -245,21 +313,27 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_back_kernel(RopeBackArg
       } else if (!value) {
         g = dn;
       }
-      store8(a.dqkv + row * a.ld_out + (int64_t)h * a.d + e, g);
+      store8(a.dqkv + row * a.ld_out + h * a.d, at, g);
     }
   }
   if (!a.part) return;
-  __shared__ float all[2][kThreads][9];   // 9: no two lanes of a step on one bank
+  __shared__ float all[kThreads][9];   // 9: no two lanes of a step on one bank
+  for (int k = 0; k < 2; ++k) {
+    __syncthreads();
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) all[k][threadIdx.x][i] = sums[k].v[i];
-  __syncthreads();
-  for (int t = threadIdx.x; t < 2 * a.d; t += kThreads) {
-    const int k = t >= a.d, j = k ? t - a.d : t;
-    float v = 0.f;
-    for (int g = 0; g < kHeads; ++g) v += all[k][g * L + j / 8][j % 8];
-    a.part[((int64_t)blockIdx.x * 2 + k) * a.d + j] = v;
+    for (int i = 0; i < 8; ++i) all[threadIdx.x][i] = sums[k].v[i];
+    __syncthreads();
+    // The group's lane and value i hold the same column in every group of the block.
+    for (int t = threadIdx.x; t < 8 * L; t += kThreads) {
+      const int l = t / 8, i = t % 8;
+      if (l >= a.d / 8) continue;
+      float v = 0.f;
+      for (int g = 0; g < kHeads; ++g) v += all[g * L + l][i];
+      const bool low = !a.interleaved && a.rot % 8 == 0 && l < a.rot / 8;
+      const int e0 = low || a.interleaved ? 4 * l : 8 * l;
+      const int e1 = low ? a.rot / 2 + 4 * l : a.interleaved ? a.d / 2 + 4 * l : 8 * l + 4;
+      a.part[((int64_t)blockIdx.x * 2 + k) * a.d + (i < 4 ? e0 + i : e1 + i - 4)] = v;
+    }
   }
 }
 
