@@ -8,17 +8,18 @@
 //
 // Bound by memory: the forward reads each logit once.  A block holds 8192 of a
 // row's logits in registers at a time and keeps the running M, S and T of every
-// thread (rescaled where M grows).  Differences to M are formed before they are
-// scaled, so large logits lose nothing.  Rows are split over blocks where there
-// are few; a second launch joins the parts in order.
+// thread (rescaled where M grows; T in powers of two).  Differences to M are formed
+// before they are scaled, so large logits lose nothing.  Rows are split over blocks
+// where there are few; a second launch joins the parts in order.
 //
-// Top alternatives: each wave keeps the best `top` entries it has seen, sorted,
-// one per lane.  An entry is one 64-bit key, the logit's order in the high word
-// and the inverted index in the low one, so that a plain comparison ranks and no
-// two are equal.  Of 1024 new entries only those above the list's last matter.
-// Where there are many (the list is still empty), the list's size-th largest of
-// the 64 lanes' maxima is a bound that at least that many entries reach; what
-// passes is packed into lanes, sorted with the list and cut.
+// Top alternatives: each wave keeps the best `top` entries it has seen, sorted, in
+// LDS.  An entry is one 64-bit key, the logit's order in the high word and the
+// inverted index in the low one, so that a plain comparison ranks and no two are
+// equal.  Most of 1024 new logits are below the list's last and cost the comparison
+// with their lanes' maxima alone, which are there for the sums.  Where the list is
+// not full yet, the top-th largest of the 64 lanes' maxima is a bound that at least
+// that many entries reach (found bit by bit, 18 of 32 bits: a lower bound is one
+// too).  What passes is packed behind one another and ranked by counting.
 #include "q3_device.h"
 #include "../../include/q3_block.h"
 #include "q3_internal.h"
@@ -29,38 +30,29 @@ namespace {
 constexpr int kThreads = 512, kWaves = kThreads / 64;
 constexpr int kEach = 16;                     // logits of a thread
 constexpr int kChunk = kThreads * kEach;      // of a block
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 typedef unsigned long long Key;
 
-__device__ __forceinline__ Key key_of(float l, uint32_t index) {
+// A logit's order as a number above 0 (for what is not NaN).
+__device__ __forceinline__ uint32_t order_of(float l) {
   const uint32_t b = __builtin_bit_cast(uint32_t, l + 0.f);   // -0 as 0
-  const uint32_t up = b & 0x80000000u ? ~b : b | 0x80000000u;
-  return (Key)up << 32 | (uint32_t)~index;
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
-__device__ __forceinline__ float logit_of(Key k) {
-  const uint32_t up = (uint32_t)(k >> 32);
-  return __builtin_bit_cast(float, up & 0x80000000u ? up & 0x7FFFFFFFu : ~up);
+__device__ __forceinline__ float logit_of(uint32_t order) {
+  return __builtin_bit_cast(float, order & 0x80000000u ? order & 0x7FFFFFFFu : ~order);
 }
+__device__ __forceinline__ Key key_of(float l, uint32_t index) { return (Key)order_of(l) << 32 | (uint32_t)~index; }
 __device__ __forceinline__ Key max_key(Key a, Key b) { return a > b ? a : b; }
 __device__ __forceinline__ Key min_key(Key a, Key b) { return a < b ? a : b; }
-
-// The wave's 64 keys in descending lane order.
-__device__ __forceinline__ Key sort_wave(Key k, int lane) {
-#pragma unroll
-  for (int size = 2; size <= 64; size *= 2) {
-#pragma unroll
-    for (int step = size / 2; step > 0; step /= 2) {
-      const Key o = __shfl_xor(k, step, 64);
-      const bool down = (lane & size) == 0 || size == 64;     // this run descends
-      const bool first = (lane & step) == 0;
-      k = down == first ? max_key(k, o) : min_key(k, o);
-    }
-  }
-  return k;
+__device__ __forceinline__ void wave_sync() {   // the wave's own LDS, written before, read behind
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
-// Two descending lists of 32, `k` in lanes 0..31 of each: the best 32 of both,
-// descending, in lanes 0..31.
+
+// Two descending lists of 32, `k` in lanes 0..31 (and again in 32..63) of each: the
+// best 32 of both, descending.
 __device__ __forceinline__ Key merge_best(Key mine, Key other, int lane) {
   const Key back = __shfl(other, 31 - (lane & 31), 64);
   Key k = max_key(mine, back);   // the larger halves of a bitonic sequence
@@ -73,30 +65,30 @@ __device__ __forceinline__ Key merge_best(Key mine, Key other, int lane) {
 }
 
 struct Sums {
-  float m, s, t;   // largest logit (raw), sum of weights, sum of weights * c (l - m)
+  float m, s, t;   // largest logit (raw), sum of weights, sum of weights * log2 of them
 };
 __device__ __forceinline__ Sums empty_sums() { return {-INFINITY, 0.f, 0.f}; }
-// Sums under a larger maximum.
-__device__ __forceinline__ void rise(Sums& a, float m, float c) {
+// Sums under a larger maximum; c2 = log2(e) / temperature.
+__device__ __forceinline__ void rise(Sums& a, float m, float c2) {
   if (!(m > a.m)) return;
   if (a.m > -INFINITY) {
-    const float d = (a.m - m) * c, f = exp2f(d * kLog2e);
+    const float d = (a.m - m) * c2, f = __builtin_amdgcn_exp2f(d);
     a.t = f > 0.f ? f * (a.t + d * a.s) : 0.f;
     a.s *= f;
   }
   a.m = m;
 }
-__device__ __forceinline__ Sums join(Sums a, Sums b, float c) {
+__device__ __forceinline__ Sums join(Sums a, Sums b, float c2) {
   const float m = fmaxf(a.m, b.m);
-  rise(a, m, c);
-  rise(b, m, c);
+  rise(a, m, c2);
+  rise(b, m, c2);
   return {m, a.s + b.s, a.t + b.t};
 }
-__device__ __forceinline__ Sums join_wave(Sums a, float c) {
+__device__ __forceinline__ Sums join_wave(Sums a, float c2) {
 #pragma unroll
   for (int off = 1; off < 64; off *= 2) {
     const Sums o = {__shfl_xor(a.m, off, 64), __shfl_xor(a.s, off, 64), __shfl_xor(a.t, off, 64)};
-    a = join(a, o, c);
+    a = join(a, o, c2);
   }
   return a;
 }
@@ -121,7 +113,7 @@ __device__ __forceinline__ f32x4 load4(rsrc_t row, const float* p, int j, int n,
 __device__ __forceinline__ void finish(const LogprobArgs& a, int64_t row, Sums r, float target) {
   const bool some = r.m > -INFINITY;
   const float ln = some ? logf(r.s) : 0.f;
-  const float h = some ? ln - r.t / r.s : 0.f;
+  const float h = some ? ln - r.t / r.s * kLn2 : 0.f;
   const int t = a.targets[row];
   float lp = 0.f;
   if (t >= 0 && t < a.n) {
@@ -135,165 +127,210 @@ __device__ __forceinline__ void finish(const LogprobArgs& a, int64_t row, Sums r
 // Lane j < top writes place j.
 __device__ __forceinline__ void finish_top(const LogprobArgs& a, int64_t row, Sums r, Key k, int lane) {
   if (lane >= a.top) return;
-  const float l = logit_of(k), ln = logf(r.s);
+  const float l = logit_of((uint32_t)(k >> 32)), ln = logf(r.s);
   const float d = l == r.m ? 0.f : (l - r.m) * a.inv_t;
   a.top_ids[row * a.top + lane] = k ? (int32_t)~(uint32_t)k : -1;
   a.top_logprobs[row * a.top + lane] = k ? d - ln : -INFINITY;
 }
+
+// The waves' lists, `count` of them in LDS, into the first: a tree of merges.  Every
+// thread of the block comes here.
+__device__ __forceinline__ void merge_lists(Key (*list)[32], int count, int wave, int lane) {
+  for (int half = count / 2; half > 0; half /= 2) {
+    __syncthreads();
+    if (wave < half) {
+      const Key k = merge_best(list[wave][lane & 31], list[wave + half][lane & 31], lane);
+      wave_sync();
+      if (lane < 32) list[wave][lane] = k;
+    }
+  }
+  __syncthreads();
+}
+
+// A chunk's logits into the wave's list: l[i] stands at first + i % 4 + (i / 4) * 4 *
+// kThreads, m is the lane's largest.  `last` is the value in the list's last place
+// (-inf: it is not full), `size` its entries, `shared` the order of the best of the
+// block's last places.
+struct Best {
+  Key* list;     // the wave's 32
+  Key* packed;   // and its 64 for new ones
+  uint32_t* shared;
+  int top, size;
+  float last;
+
+  __device__ __forceinline__ void add(const float (&l)[kEach], float m, int first, int lane) {
+    // Of what stands in other waves' lists, an equal one may rank behind this one.
+    const float others = logit_of(*shared);   // NaN (order 0): none is full
+    const float floor_ = others > last ? others : last;
+    if (__ballot(m > last && m >= floor_) == 0) return;
+    float bound = floor_;
+    if (size < top) {
+      const uint32_t o = m > -INFINITY ? order_of(m) : 0;
+      uint32_t t = 0;
+#pragma unroll
+      for (int bit = 31; bit > 13; --bit)
+        if (__popcll(__ballot(o >= (t | 1u << bit))) >= top) t |= 1u << bit;
+      if (t) bound = fmaxf(bound, logit_of(t));   // a number, or below all of them
+    }
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const bool in = l[i] >= bound && l[i] > last;
+      const uint64_t who = __ballot(in);
+      if (who == 0) continue;
+      const int place = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
+      if (in && place < 64) packed[place] = key_of(l[i], first + (i / 4) * 4 * kThreads + i % 4);
+      n += __popcll(who);
+    }
+    wave_sync();
+    Key old = lane < size ? list[lane & 31] : 0, fresh = 0;
+    if (n <= 64) {
+      // Each entry's place is the number of entries above it.
+      fresh = lane < n ? packed[lane] : 0;
+      int a = lane, b = 0;
+      for (int j = 0; j < n; ++j) {
+        const Key k = packed[j];
+        a += k > old;
+        b += k > fresh;
+      }
+      for (int j = 0; j < size; ++j) b += list[j] > fresh;
+      wave_sync();
+      if (lane < size && a < top) list[a] = old;
+      if (lane < n && b < top) list[b] = fresh;
+      size = size + n < top ? size + n : top;
+    } else {
+      // Many equal ones, or many in few lanes: one at a time, best first.  `top`
+      // steps are enough.
+      Key below = ~0ull;   // the last one taken
+      for (int step = 0; step < top; ++step) {
+        Key k = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          const Key c = l[i] >= bound && l[i] > last ? key_of(l[i], first + (i / 4) * 4 * kThreads + i % 4) : 0;
+          if (c < below) k = max_key(k, c);
+        }
+#pragma unroll
+        for (int off = 1; off < 64; off *= 2) k = max_key(k, __shfl_xor(k, off, 64));
+        if (k == 0 || k <= __shfl(old, top - 1, 64)) break;
+        const int place = __popcll(__ballot(old > k));
+        const Key up = __shfl_up(old, 1, 64);
+        old = lane < place ? old : lane == place ? k : up;
+        if (lane >= top) old = 0;
+        below = k;
+      }
+      wave_sync();
+      if (lane < 32) list[lane] = old;
+      size = __popcll(__ballot(old != 0));
+    }
+    wave_sync();
+    if (size == top) {
+      const uint32_t o = (uint32_t)(list[top - 1] >> 32);
+      last = logit_of(o);
+      if (lane == 0) atomicMax(shared, o);
+    }
+  }
+};
 
 // Block (part, row): the logits [part * per, (part + 1) * per) of the row, per a
 // multiple of kChunk.
 template <bool kTop>
 __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a, int per, Part* parts, Key* lists) {
   __shared__ Sums red[kWaves];
-  __shared__ Key best[kWaves][32];
-  __shared__ Key packed[kWaves][64];
+  __shared__ Key list[kTop ? kWaves : 1][32];
+  __shared__ Key packed[kTop ? kWaves : 1][64];
+  __shared__ uint32_t shared;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t row = blockIdx.y;
   const int from = blockIdx.x * per, to = min(a.n, from + per);
   const float* logits = a.logits + row * a.ld;
   const rsrc_t src = make_rsrc(logits, (uint32_t)a.n * 4u);
   Sums sums = empty_sums();
-  Key list = 0, last = 0;   // the wave's best, descending by lane; the one in place top - 1
+  Best best{list[kTop ? wave : 0], packed[kTop ? wave : 0], &shared, a.top, 0, -INFINITY};
+  if constexpr (kTop) {
+    if (lane < 32) list[wave][lane] = 0;
+    if (threadIdx.x == 0) shared = 0;
+    __syncthreads();
+  }
   const float c2 = a.inv_t * kLog2e;
   for (int at = from; at < to; at += kChunk) {
     float l[kEach];
     const int first = at + 4 * (int)threadIdx.x;   // four consecutive ones every 4 * kThreads
+    const bool whole = at + kChunk <= a.n;
 #pragma unroll
     for (int q = 0; q < kEach / 4; ++q) {
-      const f32x4 v = load4(src, logits, first + q * 4 * kThreads, a.n, at + kChunk <= a.n);
+      const f32x4 v = load4(src, logits, first + q * 4 * kThreads, a.n, whole);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) l[4 * q + i] = v[i];
+      for (int i = 0; i < 4; ++i) l[4 * q + i] = fmaxf(v[i], -INFINITY);   // NaN is masked
     }
-    float m = -INFINITY;
+    if (!whole) {
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int j = first + (i / 4) * 4 * kThreads + i % 4;
-      if (!(l[i] == l[i]) || j >= to) l[i] = -INFINITY;   // NaN is masked
-      m = fmaxf(m, l[i]);
+      for (int i = 0; i < kEach; ++i)
+        if (first + (i / 4) * 4 * kThreads + i % 4 >= a.n) l[i] = -INFINITY;
     }
-    rise(sums, m, a.inv_t);
-    if (sums.m > -INFINITY) {
-      const float top = sums.m;
+    float m = l[0];
+#pragma unroll
+    for (int i = 1; i < kEach; ++i) m = fmaxf(m, l[i]);
+    rise(sums, m, c2);
+    if (m == INFINITY) {   // only these count in this row
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) sums.s += l[i] == INFINITY ? 1.f : 0.f;
+    } else if (sums.m > -INFINITY && sums.m < INFINITY) {
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
-        const float d = l[i] == top ? 0.f : l[i] - top;   // +inf
-        const float e = exp2f(d * c2);
+        const float d = fmaxf((l[i] - sums.m) * c2, -1000.f), e = __builtin_amdgcn_exp2f(d);
         sums.s += e;
-        sums.t += e > 0.f ? e * (d * a.inv_t) : 0.f;
+        sums.t = fmaf(e, d, sums.t);
       }
     }
-    if constexpr (kTop) {
-      // Entries above the list's last one, by value (an equal one has a higher index).
-      const uint32_t floor_up = (uint32_t)(last >> 32);
-      Key mine = 0;   // the lane's best
-      int above = 0;
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const int j = first + (i / 4) * 4 * kThreads + i % 4;
-        const Key k = l[i] > -INFINITY ? key_of(l[i], j) : 0;
-        mine = max_key(mine, k);
-        above += (uint32_t)(k >> 32) > floor_up;
-      }
-      if (__ballot(above > 0) == 0) continue;
-      int count = above;
-#pragma unroll
-      for (int off = 1; off < 64; off *= 2) count += __shfl_xor(count, off, 64);
-      Key bound = last;
-      if (count > 32) bound = max_key(bound, __shfl(sort_wave(mine, lane), a.top - 1, 64));
-      // Pack what reaches the bound.
-      int n = 0;
-      bool fits = true;
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const int j = first + (i / 4) * 4 * kThreads + i % 4;
-        const Key k = l[i] > -INFINITY ? key_of(l[i], j) : 0;
-        const bool in = k >= bound && k > last;
-        const uint64_t who = __ballot(in);
-        const int place = n + __popcll(who & ((1ull << lane) - 1));
-        if (in && place < 64) packed[wave][place] = k;
-        n += __popcll(who);
-      }
-      fits = n <= 32;
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-      if (fits) {
-        // The list in lanes 0..31, the new ones behind it.
-        Key k = __shfl(list, lane & 31, 64);
-        if (lane >= 32) k = lane - 32 < n ? packed[wave][lane - 32] : 0;
-        list = sort_wave(k, lane);
-      } else {
-        // Many that reach it: one at a time, best first.  The bound stays below
-        // every entry that belongs to the list, so `top` steps are enough.
-        Key below = ~0ull;   // the last one taken
-        for (int step = 0; step < a.top; ++step) {
-          Key k = 0;
-#pragma unroll
-          for (int i = 0; i < kEach; ++i) {
-            const int j = first + (i / 4) * 4 * kThreads + i % 4;
-            const Key c = l[i] > -INFINITY ? key_of(l[i], j) : 0;
-            if (c < below) k = max_key(k, c);
-          }
-#pragma unroll
-          for (int off = 1; off < 64; off *= 2) k = max_key(k, __shfl_xor(k, off, 64));
-          if (k <= __shfl(list, a.top - 1, 64)) break;
-          const int place = __popcll(__ballot(list > k));
-          const Key up = __shfl_up(list, 1, 64);
-          list = lane < place ? list : lane == place ? k : up;
-          below = k;
-        }
-      }
-      if (lane >= a.top) list = 0;
-      last = __shfl(list, a.top - 1, 64);
-      __builtin_amdgcn_wave_barrier();   // the next chunk packs behind these reads
-    }
+    if constexpr (kTop) best.add(l, m, first, lane);
   }
 
-  sums = join_wave(sums, a.inv_t);
+  sums = join_wave(sums, c2);
   if (lane == 0) red[wave] = sums;
-  if (kTop && lane < 32) best[wave][lane] = list;
-  __syncthreads();
+  if constexpr (kTop) merge_lists(list, kWaves, wave, lane);
+  else __syncthreads();
   if (wave != 0) return;
-  sums = join_wave(lane < kWaves ? red[lane] : empty_sums(), a.inv_t);
-  if constexpr (kTop) {
-    list = best[0][lane & 31];
-    for (int w = 1; w < kWaves; ++w) list = merge_best(list, best[w][lane & 31], lane);
-  }
+  sums = join_wave(lane < kWaves ? red[lane] : empty_sums(), c2);
   const int t = a.targets[row];
   if (!parts) {
-    if (lane == 0) finish(a, row, sums, t >= 0 && t < a.n ? a.logits[row * a.ld + t] : 0.f);
-    if (kTop) finish_top(a, row, sums, list, lane);
+    if (lane == 0) finish(a, row, sums, t >= 0 && t < a.n ? logits[t] : 0.f);
+    if (kTop) finish_top(a, row, sums, list[0][lane & 31], lane);
     return;
   }
   const int64_t slot = row * gridDim.x + blockIdx.x;
   if (lane == 0) parts[slot] = {sums.m, sums.s, sums.t, 0.f};
-  if (kTop && lane < a.top) lists[slot * a.top + lane] = list;
+  if (kTop && lane < a.top) lists[slot * a.top + lane] = list[0][lane];
 }
 
-// A wave per row joins its parts in order.
+// A block per row joins its parts in order.
 template <bool kTop>
-__global__ __launch_bounds__(256) void logprobs_join_kernel(LogprobArgs a, int count, const Part* parts,
-                                                            const Key* lists) {
-  const int lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (row >= a.m) return;   // whole waves
-  Sums sums = empty_sums();
-  for (int i = lane; i < count; i += 64) {
-    const Part p = parts[row * count + i];
-    sums = join(sums, {p.m, p.s, p.t}, a.inv_t);
-  }
-  sums = join_wave(sums, a.inv_t);
+__global__ __launch_bounds__(kThreads) void logprobs_join_kernel(LogprobArgs a, int count, const Part* parts,
+                                                                 const Key* lists) {
+  __shared__ Key list[kTop ? kWaves : 1][32];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t row = blockIdx.x;
+  const float c2 = a.inv_t * kLog2e;
   const int t = a.targets[row];
-  if (lane == 0) finish(a, row, sums, t >= 0 && t < a.n ? a.logits[row * a.ld + t] : 0.f);
-  if constexpr (kTop) {
-    Key list = 0;
-    for (int i = 0; i < count; ++i) {
-      const int j = lane & 31;
-      list = merge_best(list, j < a.top ? lists[(row * count + i) * a.top + j] : 0, lane);
+  const float target = t >= 0 && t < a.n ? a.logits[row * a.ld + t] : 0.f;
+  Sums sums = empty_sums();
+  if (wave == 0) {
+    for (int i = lane; i < count; i += 64) {
+      const Part p = parts[row * count + i];
+      sums = join(sums, {p.m, p.s, p.t}, c2);
     }
-    finish_top(a, row, sums, list, lane);
   }
+  if constexpr (kTop) {
+    Key k = 0;
+    const int j = lane & 31;
+    for (int i = wave; i < count; i += kWaves)
+      k = merge_best(k, j < a.top ? lists[(row * count + i) * a.top + j] : 0, lane);
+    if (lane < 32) list[wave][lane] = k;
+    merge_lists(list, kWaves, wave, lane);
+  }
+  if (wave != 0) return;
+  sums = join_wave(sums, c2);
+  if (lane == 0) finish(a, row, sums, target);
+  if constexpr (kTop) finish_top(a, row, sums, list[0][lane & 31], lane);
 }
 
 // Four consecutive gradients a thread.
@@ -314,7 +351,7 @@ __global__ __launch_bounds__(256) void logprobs_back_kernel(LogprobBackArgs a, i
   for (int i = 0; i < 4; ++i) {
     const float l = v[i];
     const float lp = (l == st.x ? 0.f : (l - st.x) * a.inv_t) - st.y;
-    const float p = l > -INFINITY ? exp2f(lp * kLog2e) : 0.f;
+    const float p = l > -INFINITY ? __builtin_amdgcn_exp2f(lp * kLog2e) : 0.f;
     const float d = (j + i == t ? g : 0.f) - p * (g + h * (lp + st.z));
     o[i] = p > 0.f ? a.inv_t * d : finite && j + i == t && l > -INFINITY ? a.inv_t * g : 0.f;
   }
@@ -378,9 +415,9 @@ hipError_t launch_logprobs(const LogprobArgs& args, void* ws, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   if (!p) return hipSuccess;
-  const dim3 join((unsigned)((args.m + 3) / 4));
-  if (args.top) hipLaunchKernelGGL(logprobs_join_kernel<true>, join, dim3(256), 0, s, args, parts, p, lists);
-  else hipLaunchKernelGGL(logprobs_join_kernel<false>, join, dim3(256), 0, s, args, parts, p, lists);
+  const dim3 join((unsigned)args.m);
+  if (args.top) hipLaunchKernelGGL(logprobs_join_kernel<true>, join, dim3(kThreads), 0, s, args, parts, p, lists);
+  else hipLaunchKernelGGL(logprobs_join_kernel<false>, join, dim3(64), 0, s, args, parts, p, lists);
   return hipGetLastError();
 }
 
