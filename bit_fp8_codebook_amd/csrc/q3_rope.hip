@@ -52,28 +52,24 @@ __device__ __forceinline__ void angle_of(double position, float freq, float& c, 
 struct Vec8 {
   float v[8];
 };
-// The lane's values of a head, at e[0].. and e[1]...
+// How values pair up: with those half a rotation away, in runs of four (also where
+// nothing is rotated); adjacent ones; halves that are no multiple of four.
+enum Pairing { kHalves, kAdjacent, kOddHalves };
+int pairing_of(int rot, int interleaved) { return interleaved ? kAdjacent : rot % 8 == 0 ? kHalves : kOddHalves; }
+
+// Lane l's values of a head: e[0].. and e[1]...
 struct Places {
   int e[2];
-  bool low;    // halves: e[1] are the partners of e[0]; angles from e[0] on
+  bool low;    // kHalves: e[1] are the partners of e[0]; angles from e[0] on
   bool live;   // inside the head
 };
-template <int L>
-__device__ __forceinline__ Places places(int d, int rot, bool interleaved) {
-  const int l = threadIdx.x % L;
+template <int P>
+__device__ __forceinline__ Places places(int l, int d, int rot) {
   Places p;
-  p.low = !interleaved && rot % 8 == 0 && l < rot / 8;
+  p.low = P == kHalves && l < rot / 8;
   p.live = l < d / 8;
-  if (p.low) {
-    p.e[0] = 4 * l;
-    p.e[1] = rot / 2 + 4 * l;
-  } else if (interleaved) {
-    p.e[0] = 4 * l;
-    p.e[1] = d / 2 + 4 * l;
-  } else {
-    p.e[0] = 8 * l;
-    p.e[1] = 8 * l + 4;
-  }
+  p.e[0] = P == kAdjacent || p.low ? 4 * l : 8 * l;
+  p.e[1] = P == kAdjacent ? d / 2 + 4 * l : p.low ? rot / 2 + 4 * l : 8 * l + 4;
   return p;
 }
 __device__ __forceinline__ Vec8 load8(const float* p, const Places& at) {
@@ -119,11 +115,10 @@ __device__ __forceinline__ float group_sum(float v) {
 
 // The rotation of a lane's values; sign -1 turns back.  `swap` is the wave's own
 // 512 floats of LDS.  Every lane of the wave comes here.
-template <int L>
-__device__ __forceinline__ void rotate(Vec8& x, const Places& at, int rot, bool interleaved, const Turn& turn, float sign,
-                                       float* swap, int lane) {
-  if (rot == 0) return;
-  if (interleaved) {
+template <int L, int P>
+__device__ __forceinline__ void rotate(Vec8& x, const Places& at, int rot, const Turn& turn, float sign, float* swap,
+                                       int lane) {
+  if constexpr (P == kAdjacent) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -138,7 +133,7 @@ __device__ __forceinline__ void rotate(Vec8& x, const Places& at, int rot, bool 
       }
     return;
   }
-  if (rot % 8 == 0) {
+  if constexpr (P == kHalves) {
     if (!at.low) return;
     const f32x4 c = *reinterpret_cast<const f32x4*>(&turn[0][at.e[0]]), s = *reinterpret_cast<const f32x4*>(&turn[1][at.e[0]]);
 #pragma unroll
@@ -149,25 +144,27 @@ __device__ __forceinline__ void rotate(Vec8& x, const Places& at, int rot, bool 
     }
     return;
   }
-  // Value j goes with j + rot/2, which stands in another lane (e[1] = e[0] + 4 here).
-  const int half = rot / 2;
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
+  if constexpr (P == kOddHalves) {
+    // Value j goes with j + rot/2, which stands in another lane (e[1] = e[0] + 4 here).
+    const int half = rot / 2;
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) swap[lane * 8 + i] = x.v[i];
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-  const float* head = swap + (lane / L) * (8 * L);
+    for (int i = 0; i < 8; ++i) swap[lane * 8 + i] = x.v[i];
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    const float* head = swap + (lane / L) * (8 * L);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int j = at.e[0] + i;
-    if (j < rot) {
-      const bool low = j < half;
-      const int k = low ? j : j - half;
-      const float other = head[low ? j + half : k];
-      const float c = turn[0][k], s = low ? -sign * turn[1][k] : sign * turn[1][k];
-      x.v[i] = x.v[i] * c + other * s;
+    for (int i = 0; i < 8; ++i) {
+      const int j = at.e[0] + i;
+      if (j < rot) {
+        const bool low = j < half;
+        const int k = low ? j : j - half;
+        const float other = head[low ? j + half : k];
+        const float c = turn[0][k], s = low ? -sign * turn[1][k] : sign * turn[1][k];
+        x.v[i] = x.v[i] * c + other * s;
+      }
     }
   }
 }
@@ -175,14 +172,14 @@ __device__ __forceinline__ void rotate(Vec8& x, const Places& at, int rot, bool 
 // One token per block (blockIdx.x); blockIdx.y takes every gridDim.y-th run of
 // 256 / L heads, three of them at a time.
 constexpr int kAhead = 3;
-template <int L>
+template <int L, int P>
 __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(RopeArgs a) {
   __shared__ __align__(16) Turn turn;
-  __shared__ __align__(16) float swap[kThreads / 64][512];
+  __shared__ __align__(16) float swap[P == kOddHalves ? kThreads / 64 : 1][512];
   constexpr int kHeads = kThreads / L;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t row = a.first + blockIdx.x;
-  const Places at = places<L>(a.d, a.rot, a.interleaved);
+  const Places at = places<P>(threadIdx.x % L, a.d, a.rot);
   const int heads = a.hq + 2 * a.hk, stride = gridDim.y * kHeads;
   const float* src = a.qkv + row * a.ld;
   Vec8 x[kAhead];
@@ -226,7 +223,7 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(RopeArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) o.v[i] = x[k].v[i] * s * (query ? wq.v[i] : wk.v[i]);
       }
-      rotate<L>(o, at, a.rot, a.interleaved, turn, 1.f, swap[wave], lane);
+      rotate<L, P>(o, at, a.rot, turn, 1.f, swap[P == kOddHalves ? wave : 0], lane);
       if (!at.live || h >= heads) continue;
       if (query) {
         store8(a.q + row * a.ldq + h * a.d, at, o);
@@ -246,13 +243,13 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(RopeArgs a) {
 
 // Blocks walk the tokens; a thread adds up the weight gradients of its eight
 // values over its heads, the block's groups are added in order at the end.
-template <int L, typename E>
+template <int L, int P, typename E>
 __global__ __launch_bounds__(kThreads, 4) void qk_norm_rope_back_kernel(RopeBackArgs a) {
   __shared__ __align__(16) Turn turn[2];
-  __shared__ __align__(16) float swap[kThreads / 64][512];
+  __shared__ __align__(16) float swap[P == kOddHalves ? kThreads / 64 : 1][512];
   constexpr int kHeads = kThreads / L;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const Places at = places<L>(a.d, a.rot, a.interleaved);
+  const Places at = places<P>(threadIdx.x % L, a.d, a.rot);
   const int heads = a.hq + 2 * a.hk;
   Vec8 sums[2] = {};
   const Vec8 wq = weight8(a.wq, at), wk = weight8(a.wk, at);
@@ -287,7 +284,7 @@ __global__ __launch_bounds__(kThreads, 4) void qk_norm_rope_back_kernel(RopeBack
       if (more || row + a.groups < a.m) next = load(more ? row : row + a.groups, (more ? h0 + kHeads : 0) + threadIdx.x / L);
       const bool norm = !value && (query ? a.wq : a.wk);
       Vec8 x = cur.x, g = cur.g, dn = g;
-      rotate<L>(dn, at, a.rot, a.interleaved, turn[parity], -1.f, swap[wave], lane);
+      rotate<L, P>(dn, at, a.rot, turn[parity], -1.f, swap[P == kOddHalves ? wave : 0], lane);
       float q = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) q += x.v[i] * x.v[i];
@@ -329,10 +326,7 @@ __global__ __launch_bounds__(kThreads, 4) void qk_norm_rope_back_kernel(RopeBack
       if (l >= a.d / 8) continue;
       float v = 0.f;
       for (int g = 0; g < kHeads; ++g) v += all[g * L + l][i];
-      const bool low = !a.interleaved && a.rot % 8 == 0 && l < a.rot / 8;
-      const int e0 = low || a.interleaved ? 4 * l : 8 * l;
-      const int e1 = low ? a.rot / 2 + 4 * l : a.interleaved ? a.d / 2 + 4 * l : 8 * l + 4;
-      a.part[((int64_t)blockIdx.x * 2 + k) * a.d + (i < 4 ? e0 + i : e1 + i - 4)] = v;
+      a.part[((int64_t)blockIdx.x * 2 + k) * a.d + places<P>(l, a.d, a.rot).e[i / 4] + i % 4] = v;
     }
   }
 }
@@ -358,19 +352,24 @@ __global__ __launch_bounds__(1024) void rope_reduce_kernel(const float* part, in
 }
 
 template <typename F>
-hipError_t by_lanes(int d, F&& f) {
-  if (d <= 16) return f(std::integral_constant<int, 2>{});
-  if (d <= 32) return f(std::integral_constant<int, 4>{});
-  if (d <= 64) return f(std::integral_constant<int, 8>{});
-  if (d <= 128) return f(std::integral_constant<int, 16>{});
-  return f(std::integral_constant<int, 32>{});
+hipError_t by_lanes(int d, int pairing, F&& f) {
+  auto with = [&](auto lanes) {
+    if (pairing == kHalves) return f(lanes, std::integral_constant<int, kHalves>{});
+    if (pairing == kAdjacent) return f(lanes, std::integral_constant<int, kAdjacent>{});
+    return f(lanes, std::integral_constant<int, kOddHalves>{});
+  };
+  if (d <= 16) return with(std::integral_constant<int, 2>{});
+  if (d <= 32) return with(std::integral_constant<int, 4>{});
+  if (d <= 64) return with(std::integral_constant<int, 8>{});
+  if (d <= 128) return with(std::integral_constant<int, 16>{});
+  return with(std::integral_constant<int, 32>{});
 }
 
 }  // namespace
 
 hipError_t launch_qk_norm_rope(const RopeArgs& args, hipStream_t s) {
-  return by_lanes(args.d, [&](auto lanes) {
-    constexpr int L = decltype(lanes)::value;
+  return by_lanes(args.d, pairing_of(args.rot, args.interleaved), [&](auto lanes, auto pairing) {
+    constexpr int L = decltype(lanes)::value, P = decltype(pairing)::value;
     const int runs = (args.hq + 2 * args.hk + kThreads / L - 1) / (kThreads / L);
     // Few tokens: a block per run of heads, so that one token's heads load at once.
     const unsigned split = args.m >= 1024 ? 1u : (unsigned)runs;
@@ -378,7 +377,7 @@ hipError_t launch_qk_norm_rope(const RopeArgs& args, hipStream_t s) {
     constexpr int64_t most = int64_t(1) << 22;   // a launch takes less than 2^32 threads
     for (a.first = 0; a.first < a.m; a.first += most) {
       const int64_t rows = a.m - a.first < most ? a.m - a.first : most;
-      hipLaunchKernelGGL(qk_norm_rope_kernel<L>, dim3((unsigned)rows, split), dim3(kThreads), 0, s, a);
+      hipLaunchKernelGGL((qk_norm_rope_kernel<L, P>), dim3((unsigned)rows, split), dim3(kThreads), 0, s, a);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
@@ -390,12 +389,13 @@ hipError_t launch_qk_norm_rope(const RopeArgs& args, hipStream_t s) {
 int64_t rope_back_groups(int64_t m) { return m < 1024 ? m : 1024; }
 
 hipError_t launch_qk_norm_rope_back(const RopeBackArgs& a, int32_t d_type, hipStream_t s) {
-  const hipError_t err = by_lanes(a.d, [&](auto lanes) {
-    constexpr int L = decltype(lanes)::value;
+  const hipError_t err = by_lanes(a.d, pairing_of(a.rot, a.interleaved), [&](auto lanes, auto pairing) {
+    constexpr int L = decltype(lanes)::value, P = decltype(pairing)::value;
     if (d_type == Q3_BF16)
-      hipLaunchKernelGGL((qk_norm_rope_back_kernel<L, uint16_t>), dim3((unsigned)a.groups), dim3(kThreads), 0, s, a);
+      hipLaunchKernelGGL((qk_norm_rope_back_kernel<L, P, uint16_t>), dim3((unsigned)a.groups), dim3(kThreads), 0, s,
+                         a);
     else
-      hipLaunchKernelGGL((qk_norm_rope_back_kernel<L, float>), dim3((unsigned)a.groups), dim3(kThreads), 0, s, a);
+      hipLaunchKernelGGL((qk_norm_rope_back_kernel<L, P, float>), dim3((unsigned)a.groups), dim3(kThreads), 0, s, a);
     return hipGetLastError();
   });
   if (err != hipSuccess || !a.part) return err;
