@@ -143,12 +143,20 @@ struct Pages {
   int* id;
   int first;   // the page number that id[0] stands for
 };
-__device__ __forceinline__ void list_pages(const AttendArgs& a, const Tile& t, int key0, int key1, Pages& pages,
+// Lists those of [key0, key1); whether all that this thread saw of positions below
+// `hi` are there.
+__device__ __forceinline__ bool list_pages(const AttendArgs& a, const Tile& t, int key0, int key1, int hi, Pages& pages,
                                            int thread, int threads) {
   pages.first = key0 >> a.cache.shift;
   const int count = key1 > key0 ? ((key1 - 1) >> a.cache.shift) - pages.first + 1 : 0;
-  for (int i = thread; i < count && i < kListed; i += threads)
-    pages.id[i] = (int)find_page(a.batch, a.cache, t.sequence, (int64_t)(pages.first + i) << a.cache.shift);
+  bool all = true;
+  for (int i = thread; i < count && i < kListed; i += threads) {
+    const int64_t key = (int64_t)(pages.first + i) << a.cache.shift;
+    const int id = (int)find_page(a.batch, a.cache, t.sequence, key);
+    pages.id[i] = id;
+    all &= id >= 0 || key >= hi;
+  }
+  return all;
 }
 // Keys that a list takes, a multiple of `step`.
 __device__ __forceinline__ int listed_keys(const AttendArgs& a, int step) {
@@ -176,30 +184,41 @@ struct Loader {
 #pragma unroll
       for (int w = 0; w < 2; ++w) off[w][i] = (key_of(i, lane) * DT + 8 * chunk_of(i, lane, at, w)) * 2;
   }
-  // Positions key0.. of `head` (key0 a multiple of KEYS); which: 0 keys, 1 values.
-  __device__ __forceinline__ void issue(const AttendArgs& a, const Pages& pages, int head, int key0, int at, int which,
-                                        uint32_t dst, int lane) const {
+  // The page of position key0, to be fetched some time before from() takes it.
+  static __device__ __forceinline__ int page_of(const AttendArgs& a, const Pages& pages, int key0) {
+    return pages.id[(key0 >> a.cache.shift) - pages.first];
+  }
+  // Where position key0 of `head` stands in the cache (key0 a multiple of KEYS).
+  static __device__ __forceinline__ const uint16_t* from(const AttendArgs& a, int page, int head, int key0, int which) {
+    const int shift = a.cache.shift;
+    int id = __builtin_amdgcn_readfirstlane(page);
+    id = id < 0 ? 0 : id;   // read, but never used
+    return (which ? a.cache.v : a.cache.k) + (int64_t)id * a.cache.page_stride +
+           (((int64_t)head << shift) + (key0 & ((1 << shift) - 1))) * DT;
+  }
+  // Load i of positions key0.. of `head`, which: 0 keys, 1 values, in one page from
+  // `run` = from() on, rows of DT values;
+  __device__ __forceinline__ void load_run(const uint16_t* run, int which, int i, uint32_t dst) const {
+    load_lds(run, off[which][i], dst + 1024u * i);
+  }
+  // and wherever they are.
+  static __device__ __forceinline__ void load_any(const AttendArgs& a, const Pages& pages, int head, int key0, int at,
+                                                  int which, int i, uint32_t dst, int lane) {
     const int shift = a.cache.shift, mask = (1 << shift) - 1, d = a.cache.d;
-    const uint16_t* base = which ? a.cache.v : a.cache.k;
-    if (d == DT && (1 << shift) >= KEYS) {   // one page, whole rows
-      int id = __builtin_amdgcn_readfirstlane(pages.id[(key0 >> shift) - pages.first]);
-      id = id < 0 ? 0 : id;                  // read, but never used
-      const uint16_t* from = base + (int64_t)id * a.cache.page_stride + (((int64_t)head << shift) + (key0 & mask)) * DT;
-#pragma unroll
-      for (int i = 0; i < count; ++i) load_lds(from, off[which][i], dst + 1024u * i);
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < count; ++i) {
-      const int key = key0 + (int)key_of(i, lane);
-      int id = pages.id[(key >> shift) - pages.first];
-      id = id < 0 ? 0 : id;
-      const uint32_t c = chunk_of(i, lane, at, which);
-      const uint16_t* p = base + (int64_t)id * a.cache.page_stride + (((int64_t)head << shift) + (key & mask)) * d + 8 * c;
-      load_lds(8 * c < (uint32_t)d ? (const void*)p : (const void*)&kZeros, dst + 1024u * i);
-    }
+    const int key = key0 + (int)key_of(i, lane);
+    int id = pages.id[(key >> shift) - pages.first];
+    id = id < 0 ? 0 : id;
+    const uint32_t c = chunk_of(i, lane, at, which);
+    const uint16_t* p = (which ? a.cache.v : a.cache.k) + (int64_t)id * a.cache.page_stride +
+                        (((int64_t)head << shift) + (key & mask)) * d + 8 * c;
+    load_lds(8 * c < (uint32_t)d ? (const void*)p : (const void*)&kZeros, dst + 1024u * i);
   }
 };
+// Whether `keys` consecutive positions lie in one page, in rows of DT values.
+template <int DT>
+__host__ __device__ __forceinline__ bool in_runs(const CacheView& c, int keys) {
+  return c.d == DT && (1 << c.shift) >= keys;
+}
 
 // ---- the products of one wave -------------------------------------------------------
 
@@ -307,24 +326,37 @@ struct Wave {
     }
   }
 
-  // Scores of 32 NB keys from the tile at `k` (rows of its LDS tile from `at` on).
+  // Scores of 32 NB keys from the tile at `k`.  Six fragments are read ahead, one
+  // beside each product: left to the compiler, every read is waited for at once.
+  // beside(i) stands behind product i of kReads.
   template <int NB>
-  __device__ __forceinline__ void scores(const uint8_t* k, f32x16 (&sc)[NT][NB], int lane) const {
+  static constexpr int score_products() { return NB * DT / 16; }
+  template <int NB, typename Beside>
+  __device__ __forceinline__ void scores(const uint8_t* k, f32x16 (&sc)[NT][NB], int lane, Beside&& beside) const {
     const int half = lane >> 5;
+    constexpr int kReads = score_products<NB>(), kAhead = 6;
+    auto read = [&](int i) {   // 16 values of 32 keys
+      const uint32_t key = 32 * (i % NB) + (lane & 31);
+      return *reinterpret_cast<const bf16x8*>(k + key * Layout<DT>::row +
+                                              16u * ((2 * (i / NB) + half) ^ Layout<DT>::place_k(key)));
+    };
+    bf16x8 f[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead && i < kReads; ++i) f[i] = read(i);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int b = 0; b < NB; ++b) sc[n][b] = f32x16{};
 #pragma unroll
-    for (int j = 0; j < DT / 16; ++j)
+    for (int i = 0; i < kReads; ++i) {
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const uint32_t key = 32 * b + (lane & 31);
-        const bf16x8 f = *reinterpret_cast<const bf16x8*>(k + key * Layout<DT>::row +
-                                                          16u * ((2 * j + half) ^ Layout<DT>::place_k(key)));
-#pragma unroll
-        for (int n = 0; n < NT; ++n) sc[n][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[n][j], sc[n][b], 0, 0, 0);
-      }
+      for (int n = 0; n < NT; ++n)
+        sc[n][i % NB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i % kAhead], q[n][i / NB], sc[n][i % NB], 0, 0, 0);
+      if (i + kAhead < kReads) f[i % kAhead] = read(i + kAhead);
+      beside(i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
   // -inf for what the row does not see: a bit per key, widened to a word each, so
   // that no comparison is kept per register.
@@ -350,59 +382,90 @@ struct Wave {
   }
   // Scores to weights, as bf16 operands of 16 keys each (what the second product
   // takes: a weight is then off by half a step, 2^-8 of itself, as the result is
-  // once more.  The sum is that of the unrounded ones).  A second term for what the
+  // once more.  The sum is that of the unrounded ones.  A second term for what the
   // rounding leaves would cost the narrow kernel nothing, but turns an infinite
-  // value into NaN.
+  // value into NaN), and O^T += V^T P^T for 32 NB values from the tile at `v`.  The
+  // products of one operand run beside the exponentials of the next.
   template <int NB>
-  __device__ __forceinline__ void weigh(const f32x16 (&sc)[NT][NB], bf16x8 (&p)[NT][2 * NB]) {
+  __device__ __forceinline__ void raise(const f32x16 (&sc)[NT][NB]) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float high = sc[n][0][0];
+      float part[4];   // four chains side by side
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
+      for (int i = 0; i < 4; ++i) {
+        part[i] = sc[n][0][4 * i];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) high = fmaxf(high, sc[n][b][i]);
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) part[i] = fmaxf(part[i], sc[n][b][4 * i + j]);
+      }
+      float high = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
       high = fmaxf(top[n], fmaxf(high, other_half(high)) * c);
-      const float base = high == -INFINITY ? 0.f : high;
       if (__any(high > top[n])) {
-        const float f = __builtin_amdgcn_exp2f(top[n] - base);
+        const float f = __builtin_amdgcn_exp2f(top[n] - (high == -INFINITY ? 0.f : high));
         sum[n] *= f;
 #pragma unroll
         for (int i = 0; i < DT / 32; ++i) o[n][i] *= f;
         top[n] = high;
       }
-#pragma unroll
-      for (int b = 0; b < 2 * NB; ++b) {
-        u32x4 u;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x = __builtin_amdgcn_exp2f(fmaf(sc[n][b / 2][8 * (b % 2) + 2 * i], c, -base));
-          const float y = __builtin_amdgcn_exp2f(fmaf(sc[n][b / 2][8 * (b % 2) + 2 * i + 1], c, -base));
-          sum[n] += x + y;
-          u[i] = pack_bf16(x, y);
-        }
-        p[n][b] = __builtin_bit_cast(bf16x8, u);
-      }
     }
   }
-  // O^T += V^T P^T for 32 NB values from the tile at `v`.
   template <int NB>
-  __device__ __forceinline__ void values(const uint8_t* v, const bf16x8 (&p)[NT][2 * NB]) {
+  static constexpr int value_products() { return 2 * NB * (DT / 32); }
+  template <int NB, typename Beside>
+  __device__ __forceinline__ void values(const uint8_t* v, const f32x16 (&sc)[NT][NB], Beside&& beside) {
+    constexpr int P = DT / 32, kFrags = value_products<NB>(), kAhead = 4;
+    float base[NT];
 #pragma unroll
-    for (int b = 0; b < 2 * NB; ++b)
+    for (int n = 0; n < NT; ++n) base[n] = top[n] == -INFINITY ? 0.f : top[n];
+    // Weights 2 i and 2 i + 1 of operand b.
+    auto pair = [&](int n, int b, int i) {
+      const float x = __builtin_amdgcn_exp2f(fmaf(sc[n][b / 2][8 * (b % 2) + 2 * i], c, -base[n]));
+      const float y = __builtin_amdgcn_exp2f(fmaf(sc[n][b / 2][8 * (b % 2) + 2 * i + 1], c, -base[n]));
+      sum[n] += x + y;
+      return pack_bf16(x, y);
+    };
+    auto read = [&](int t) {   // 16 keys of 32 values
+      union {
+        s16x4 part[2];
+        bf16x8 all;
+      } f;
 #pragma unroll
-      for (int i = 0; i < DT / 32; ++i) {
-        union {
-          s16x4 part[2];
-          bf16x8 all;
-        } f;
+      for (int e = 0; e < 2; ++e)
+        f.part[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(
+            v + value[t % P] + (16 * (t / P) + 8 * e) * Layout<DT>::row));
+      return f.all;
+    };
+    bf16x8 f[kAhead];
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          f.part[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (__attribute__((address_space(3))) s16x4*)(v + value[i] + (16 * b + 8 * e) * Layout<DT>::row));
+    for (int t = 0; t < kAhead && t < kFrags; ++t) f[t] = read(t);
+    __builtin_amdgcn_sched_barrier(0);
+    u32x4 now[NT], next[NT];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) o[n][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.all, p[n][b], o[n][i], 0, 0, 0);
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) now[n][i] = pair(n, 0, i);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int t = 0; t < kFrags; ++t) {
+      const int b = t / P, i = t % P;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        o[n][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[t % kAhead], __builtin_bit_cast(bf16x8, now[n]), o[n][i], 0, 0, 0);
+      if (t + kAhead < kFrags) f[t % kAhead] = read(t + kAhead);
+      if (b + 1 < 2 * NB) {
+#pragma unroll
+        for (int j = 4 * i / P; j < 4 * (i + 1) / P; ++j)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) next[n][j] = pair(n, b + 1, j);
+        if (i == P - 1) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) now[n] = next[n];
+        }
       }
+      beside(t);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
   // Values that clean_values took out, for the rows that see them (a weight times
   // an infinity or NaN is that again).
@@ -494,7 +557,11 @@ __device__ __forceinline__ void join_row(const AttendArgs& a, const Tile& t, int
 
 // ---- many rows: tiles of 128 -----------------------------------------------------------
 
-constexpr int kWideRows = 128, kStep = 64, kThreads = 256;
+constexpr int kStep = 64, kWideRows = 128, kThreads = 256;   // keys of a step, rows of a tile
+// Blocks of a CU: two where a wave's sums and queries leave room for a second one on
+// its SIMD.  Steps that the LDS of a block holds.
+__host__ __device__ constexpr int wide_blocks(int dim) { return dim > 128 ? 1 : 2; }
+__host__ __device__ constexpr int wide_ring(int dim) { return dim > 192 ? 2 : dim > 128 ? 3 : dim > 64 ? 2 : 4; }
 
 // Parts that a tile's steps go to: at most `splits`, of four steps at least.
 __device__ __forceinline__ int parts_of(int steps, int splits) {
@@ -505,10 +572,13 @@ __device__ __forceinline__ int steps_of(const Span& span) {
   return (span.hi - (span.lo & ~(kStep - 1)) + kStep - 1) / kStep;
 }
 
-// Four waves with 32 rows each share 64 keys at a time through two LDS buffers.
-template <int DT>
-__global__ __launch_bounds__(kThreads, DT > 128 ? 1 : 2)
+// Four waves with 32 rows each share 64 keys at a time through a ring of LDS
+// buffers.  The loads of a step are asked for beside the products of scores, up to
+// three steps ahead.  kRuns: 16 keys are in one page, whole rows.
+template <int DT, bool kRuns>
+__global__ __launch_bounds__(kThreads, wide_blocks(DT))
 void attend_wide_kernel(AttendArgs a, int splits, float* parts) {
+  constexpr int R = wide_ring(DT);
   constexpr uint32_t kTile = kStep * Layout<DT>::row, kBuf = 2 * kTile;
   extern __shared__ __align__(16) uint8_t lds[];
   __shared__ int list[kListed];
@@ -537,47 +607,89 @@ void attend_wide_kernel(AttendArgs a, int splits, float* parts) {
   w.init(a, t, head, group, 32 * wave, live, lane);
   const int first_position = position_of(t, t.first, group);   // of the tile's rows
   const int last_low = below_window(a, position_of(t, t.first + live - 1, group));
+  const bool mine = 32 * wave < live;
+  // A wave brings 16 keys of a step, and their values.
+  const int keys16 = 16 * wave;
   Loader<DT, 16> loader;
-  loader.init(lane, 16 * wave);
+  loader.init(lane, keys16);
+  constexpr int N = 2 * Loader<DT, 16>::count;   // a wave's loads of a step
   Pages pages{list, 0};
-  const uint32_t base = lds_offset(lds) + wave * 16 * Layout<DT>::row;
-  auto issue = [&](int s) {
-    const int key0 = begin + s * kStep + 16 * wave;
+  const uint32_t base = lds_offset(lds) + keys16 * Layout<DT>::row;
+  // Where this wave's part of step s stands, and load i of N of it.
+  struct Where {
+    int key0;
+    const uint16_t* run[2];
+  };
+  auto where = [&](int s, int page) {
+    Where o;
+    o.key0 = begin + s * kStep + keys16;
 #pragma unroll
-    for (int which = 0; which < 2; ++which)
-      loader.issue(a, pages, head, key0, 16 * wave, which, base + (s & 1) * kBuf + which * kTile, lane);
+    for (int i = 0; i < 2; ++i) o.run[i] = kRuns ? loader.from(a, page, head, o.key0, i) : nullptr;
+    return o;
+  };
+  auto load = [&](const Where& o, int slot, int i) {
+    const int which = i / loader.count, j = i % loader.count;
+    const uint32_t dst = base + slot * kBuf + which * kTile;
+    if (kRuns) loader.load_run(o.run[which], which, j, dst);
+    else loader.load_any(a, pages, head, o.key0, keys16, which, j, dst, lane);
   };
 
-  const int run = listed_keys(a, kStep) / kStep;
-  for (int w0 = s0; w0 < s1; w0 += run) {
-    const int w1 = s1 - w0 < run ? s1 : w0 + run;
-    meet();   // the list and the buffers are free
-    list_pages(a, t, begin + w0 * kStep, begin + w1 * kStep, pages, threadIdx.x, kThreads);
+  const int run_steps = listed_keys(a, kStep) / kStep;
+  for (int w0 = s0; w0 < s1; w0 += run_steps) {
+    const int w1 = s1 - w0 < run_steps ? s1 : w0 + run_steps;
+    meet();   // the list and the ring are free
+    bool all = list_pages(a, t, begin + w0 * kStep, begin + w1 * kStep, span.hi, pages, threadIdx.x, kThreads);
     __builtin_amdgcn_s_waitcnt(0x0F70);   // the compiler knows that queries are here (and waits in the loop for nothing)
-    meet();
-    issue(w0);
+    all = __syncthreads_and(all);
+    // Behind the last step it is asked for again, and never used, so that every step
+    // has the same loads under way.
+    auto page_of = [&](int s) { return loader.page_of(a, pages, begin + (s < w1 ? s : w1 - 1) * kStep + keys16); };
+#pragma unroll
+    for (int i = 0; i < R - 1; ++i) {
+      const Where o = where(w0 + i < w1 ? w0 + i : w1 - 1, page_of(w0 + i));
+#pragma unroll
+      for (int j = 0; j < N; ++j) load(o, i, j);
+    }
+    int page = page_of(w0 + R - 1);
+    int slot = 0, free = R - 1;   // this step's, and the one that the step before has left
+    // Steps that every row of the tile sees whole, all of them there.
+    const int last = span.hi - 1 < first_position ? span.hi - 1 : first_position;
     for (int s = w0; s < w1; ++s) {
-      wait_loads<0>();
-      meet();   // everyone's loads of this step are in, and everyone has left the step before
-      if (s + 1 < w1) issue(s + 1);
-      uint8_t* buf = lds + (s & 1) * kBuf;
-      const int key0 = begin + s * kStep;
-      const uint64_t there = there_of(a, pages, key0, span.hi, kStep, lane);
-      const bool whole = ~there == 0 && key0 + kStep - 1 <= first_position && key0 > last_low;
+      wait_loads<(R - 2) * N>();   // this step's: all but those of the R - 2 behind it
+      meet();                      // everyone's, and everyone has left the step before
+      uint8_t* buf = lds + slot * kBuf;
+      const int key0 = begin + s * kStep, next = s + R - 1 < w1 ? s + R - 1 : w1 - 1;
+      const bool whole = all && key0 + kStep - 1 <= last && key0 > last_low;
+      const Where o = where(next, page);
+      uint64_t there = ~0ull;
       int bad = 0;
       if (!whole) {
-        bad = clean_values<DT, 16>(buf + kTile + wave * 16 * Layout<DT>::row, (uint32_t)(there >> (16 * wave)), lane);
+        there = there_of(a, pages, key0, span.hi, kStep, lane);
+        bad = clean_values<DT, 16>(buf + kTile + keys16 * Layout<DT>::row, (uint32_t)(there >> keys16), lane);
         bad = __syncthreads_or(bad);
       }
-      if (32 * wave >= live) continue;
       f32x16 sc[1][2];
-      w.scores(buf, sc, lane);
-      if (!whole) w.mask(sc, there, key0, lane);
-      bf16x8 p[1][4];
-      w.template weigh<2>(sc, p);
-      w.template values<2>(buf + kTile, p);
-      if (bad) w.add_unseen(a, pages, there, head, key0, kStep, lane);
+      if (mine) {
+        constexpr int kProducts = w.template score_products<2>();
+        w.scores(buf, sc, lane, [&](int i) {
+#pragma unroll
+          for (int j = i * N / kProducts; j < (i + 1) * N / kProducts; ++j) load(o, free, j);
+        });
+      } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) load(o, free, j);
+      }
+      page = page_of(s + R);
+      if (mine) {
+        if (!whole) w.mask(sc, there, key0, lane);
+        w.raise(sc);
+        w.values(buf + kTile, sc, [](int) {});
+        if (bad) w.add_unseen(a, pages, there, head, key0, kStep, lane);
+      }
+      free = slot;
+      slot = slot + 1 == R ? 0 : slot + 1;
     }
+    wait_loads<0>();
   }
 
   const int row = 32 * wave + (lane & 31), half = lane >> 5;
@@ -631,10 +743,11 @@ __global__ __launch_bounds__(kThreads) void attend_wide_join_kernel(AttendArgs a
                  threadIdx.x & 63);
 }
 
-// Splits of the keys of a tile of 128 rows: until every CU has two blocks.
-int wide_splits(int64_t units) {
-  if (units >= 384) return 1;
-  const int64_t s = 1024 / units;
+// Splits of the keys of a tile: until every CU has the blocks that it takes, twice over.
+int wide_splits(int64_t units, int dim) {
+  const int64_t want = 256 * wide_blocks(dim);
+  if (4 * units >= 3 * want) return 1;
+  const int64_t s = 2 * want / units;
   return (int)(s < 64 ? s : 64);
 }
 
@@ -753,6 +866,7 @@ void attend_narrow_kernel(AttendArgs a, float* parts, Cut* cuts) {
   const uint32_t base = lds_offset(mine);
   Loader<DT, 32> loader;
   loader.init(lane, 0);
+  const bool runs = in_runs<DT>(a.cache, 32);
   Pages pages{list, 0};
 
   for (int64_t at = from; at < to;) {
@@ -788,7 +902,7 @@ void attend_narrow_kernel(AttendArgs a, float* parts, Cut* cuts) {
     for (int w0 = c0; w0 < c0 + n; w0 += run) {
       const int w1 = c0 + n - w0 < run ? c0 + n : w0 + run;
       meet();   // the list and the ring are free
-      list_pages(a, t, begin + w0 * kNarrowStep, begin + w1 * kNarrowStep, pages, threadIdx.x, kThreads);
+      list_pages(a, t, begin + w0 * kNarrowStep, begin + w1 * kNarrowStep, sh.span.hi, pages, threadIdx.x, kThreads);
       // The stream counts its loads: nothing else is under way, and the compiler
       // knows that queries are here (it would wait for them inside the loop).
       __builtin_amdgcn_s_waitcnt(0x0F70);
@@ -798,7 +912,16 @@ void attend_narrow_kernel(AttendArgs a, float* parts, Cut* cuts) {
       int count = (sh.span.hi - key_w + kNarrowStep - 1) / kNarrowStep;
       count = count < 0 ? 0 : count < w1 - w0 ? count : w1 - w0;
       auto issue = [&](int i, int which) {
-        loader.issue(a, pages, head, key_w + i * kNarrowStep, 0, which, base + ((i & (R - 1)) * 2 + which) * kTile, lane);
+        const int key0 = key_w + i * kNarrowStep;
+        const uint32_t dst = base + ((i & (R - 1)) * 2 + which) * kTile;
+        if (runs) {
+          const uint16_t* from = loader.from(a, loader.page_of(a, pages, key0), head, key0, which);
+#pragma unroll
+          for (int j = 0; j < N; ++j) loader.load_run(from, which, j, dst);
+        } else {
+#pragma unroll
+          for (int j = 0; j < N; ++j) loader.load_any(a, pages, head, key0, 0, which, j, dst, lane);
+        }
       };
 #pragma unroll
       for (int i = 0; i < R; ++i) {
@@ -817,12 +940,11 @@ void attend_narrow_kernel(AttendArgs a, float* parts, Cut* cuts) {
         // Under way behind this tile's keys: its values and the R - 1 tiles after it.
         if (R == 2 && left >= 2) wait_loads<3 * N>();
         else wait_loads<N>();
-        bf16x8 p[NT][2];
+        f32x16 sc[NT][1];
         if (!none) {
-          f32x16 sc[NT][1];
-          w.scores(kt, sc, lane);
+          w.scores(kt, sc, lane, [](int) {});
           if (!whole) w.mask(sc, there, key0, lane);
-          w.template weigh<1>(sc, p);
+          w.raise(sc);
         }
         reads_done();
         if (left > R) issue(i + R, 0);
@@ -840,7 +962,7 @@ void attend_narrow_kernel(AttendArgs a, float* parts, Cut* cuts) {
             bad = __any(clean_values<DT, 32>(vt, there, lane));
             reads_done();
           }
-          w.template values<1>(vt, p);
+          w.values(vt, sc, [](int) {});
           if (bad) w.add_unseen(a, pages, there, head, key0, 32, lane);
         }
         reads_done();
@@ -961,13 +1083,14 @@ auto by_dim(int d, F&& f) {
 template <int DT>
 hipError_t launch_wide(const AttendArgs& a, float* parts, hipStream_t s) {
   const int64_t units = tiles_of(a.m, a.batch.sequences, a.hq / a.cache.heads, kWideRows) * a.cache.heads;
-  const int splits = wide_splits(units);
-  constexpr size_t shm = 4 * kStep * Layout<DT>::row;
-  static LdsAllowance seen;
-  const hipError_t ok = allow_dynamic_lds(reinterpret_cast<const void*>(attend_wide_kernel<DT>), shm, seen);
+  const int splits = wide_splits(units, DT);
+  constexpr size_t shm = wide_ring(DT) * 2 * kStep * Layout<DT>::row;
+  static LdsAllowance seen, seen_runs;
+  const bool runs = in_runs<DT>(a.cache, 16);
+  auto* kernel = runs ? attend_wide_kernel<DT, true> : attend_wide_kernel<DT, false>;
+  const hipError_t ok = allow_dynamic_lds(reinterpret_cast<const void*>(kernel), shm, runs ? seen_runs : seen);
   if (ok != hipSuccess) return ok;
-  hipLaunchKernelGGL((attend_wide_kernel<DT>), dim3((unsigned)(units * splits)), dim3(kThreads), shm, s, a, splits,
-                     parts);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(units * splits)), dim3(kThreads), shm, s, a, splits, parts);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
   hipLaunchKernelGGL(attend_wide_join_kernel<DT>, dim3((unsigned)units, kWideRows / 4), dim3(kThreads), 0, s, a, splits,
@@ -1001,7 +1124,7 @@ int64_t attend_workspace_bytes(int64_t m, int64_t sequences, int32_t hq, int32_t
       return blocks * (2 * 4 * slot_floats<DT>(form == kNarrow32 ? 32 : 64) + (int64_t)sizeof(Cut));
     }
     const int64_t units = tiles_of(m, sequences, hq / hk, kWideRows) * hk;
-    const int splits = wide_splits(units);
+    const int splits = wide_splits(units, DT);
     return splits == 1 ? 0 : units * splits * slot_floats<DT>(kWideRows) * 4;
   });
 }
