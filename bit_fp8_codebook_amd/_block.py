@@ -436,7 +436,7 @@ class PagedCache:
         if pages < 1 or heads < 1 or size < 1 or dim < 1:
             raise ValueError(f"a cache of shape {tuple(k.shape)} holds nothing")
         for t, name in ((k, "k"), (v, "v")):
-            if not t[0].is_contiguous() or (pages > 1 and t.stride(0) < heads * size * dim):
+            if not (t.is_contiguous() or t[0].is_contiguous()) or (pages > 1 and t.stride(0) < heads * size * dim):
                 raise ValueError(f"{name}'s pages must be contiguous and must not overlap")
         stride = k.stride(0) if pages > 1 else heads * size * dim
         if pages > 1 and v.stride(0) != stride:
