@@ -55,6 +55,7 @@ __device__ __forceinline__ Tile find_tile(const AttendArgs& a, int64_t tile, int
   const int s = __builtin_amdgcn_readfirstlane(lo - 1);
   const int64_t m = a.m;
   const int64_t start = b.q_start[s], end = b.q_start[s + 1];
+  const int length = b.kv_len[s];   // asked for beside the two above
   if (start < 0 || end <= start || start >= m) return t;
   const int64_t rows = ((end < m ? end : m) - start) * group;
   const int64_t first = (tile - number(s)) * size;
@@ -64,7 +65,7 @@ __device__ __forceinline__ Tile find_tile(const AttendArgs& a, int64_t tile, int
   t.end = (int)end;
   t.rows = (int)rows;   // m * heads_q < 2^31
   t.first = (int)first;
-  t.length = b.kv_len[s] > 0 ? b.kv_len[s] : 0;
+  t.length = length > 0 ? length : 0;
   return t;
 }
 
@@ -777,10 +778,10 @@ constexpr int narrow_blocks() { return DT > 64 ? 256 : 512; }
 
 // A block's tile that others continue: what the second launch joins.
 struct Cut {
-  int sequence;   // -1: none
-  int first;      // the tile's first row
+  int start, rows;   // the sequence's first row of q and its rows (0: no tile)
+  int first;         // the tile's first row
   int head;
-  int last;       // the last block that has a part of it
+  int last;          // the last block that has a part of it
 };
 
 // A sequence's share of the work.
@@ -792,12 +793,13 @@ struct Share {
 __device__ __forceinline__ Share share_of(const AttendArgs& a, int s, int group, int size) {
   Share w{};
   const int64_t start = a.batch.q_start[s], end = a.batch.q_start[s + 1];
+  const int length = a.batch.kv_len[s];   // asked for beside the two above
   if (start < 0 || end <= start || start >= a.m) return w;
   w.t.sequence = s;
   w.t.start = (int)start;
   w.t.end = (int)end;
   w.t.rows = (int)(((end < a.m ? end : a.m) - start) * group);
-  w.t.length = a.batch.kv_len[s] > 0 ? a.batch.kv_len[s] : 0;
+  w.t.length = length > 0 ? length : 0;
   w.span = span_of(a, w.t, 0, w.t.rows, group);
   w.tiles = (w.t.rows + size - 1) / size;
   const int begin = w.span.lo & ~(kNarrowStep - 1);
@@ -847,7 +849,7 @@ void attend_narrow_kernel(AttendArgs a, float* parts, Cut* cuts) {
   for (int s0 = 64; s0 < b; s0 += 64) total += wave_sum64(work_of(s0 + lane));
   const int64_t share = (total + blocks - 1) / blocks;
   const int64_t from = share * blockIdx.x, to = from + share < total ? from + share : total;
-  Cut cut{-1, 0, 0, 0};
+  Cut cut{};
   int s = 0;
   int64_t before = 0;   // steps of the sequences before s
   for (int s0 = 0; from < to && s0 < b; s0 += 64) {
@@ -895,7 +897,7 @@ void attend_narrow_kernel(AttendArgs a, float* parts, Cut* cuts) {
     const bool complete = c0 == 0 && n == sh.steps;
     if (c0 == 0 && !complete) {
       const int64_t last = at + sh.steps - 1;   // the tile's last step
-      cut = Cut{s, t.first, head, (int)uniform(last / share)};
+      cut = Cut{t.start, t.rows, t.first, head, (int)uniform(last / share)};
     }
 
     Wave<DT, NT> w;
@@ -973,7 +975,7 @@ void attend_narrow_kernel(AttendArgs a, float* parts, Cut* cuts) {
     }
 
     // The four waves' sums: each scaled to the largest maximum, then added in order,
-    // 32 values of all rows at a time.
+    // as many values of all rows at a time as the ring's LDS holds.
     meet();   // the ring is free
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
@@ -995,46 +997,58 @@ void attend_narrow_kernel(AttendArgs a, float* parts, Cut* cuts) {
     // Slots of what is continued, block by block, then of what is begun.
     float* slot = parts + (blockIdx.x + (c0 == 0 ? (int64_t)gridDim.x : 0)) * slot_floats<DT>(kRows);
     constexpr int kPitch = 36;   // floats of 32 values and room against bank conflicts
-    float* buf = reinterpret_cast<float*>(lds);
+    constexpr int kAll = DT / 32, kSlice = 4 * kRows * kPitch;
+    constexpr int kFit = (int)(narrow_bytes<DT>() / (4 * kSlice));
+    // (Two tiles of rows have no registers left for more than one slice.)
+    constexpr int kSlices = NT > 1 ? 1 : kFit >= kAll ? kAll : kFit >= 2 && kAll % 2 == 0 ? 2 : 1;
+    static_assert(kFit >= kSlices, "");
 #pragma unroll
-    for (int d0 = 0; d0 < DT / 32; ++d0) {
+    for (int d1 = 0; d1 < kAll; d1 += kSlices) {
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        float* to = buf + (wave * kRows + 32 * i + (lane & 31)) * kPitch + 4 * (lane >> 5);
-        const f32x16& o = w.o[i][d0];
+      for (int g = 0; g < kSlices; ++g)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<f32x4*>(to + 8 * j) = f32x4{o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]} * f[i];
-      }
+        for (int i = 0; i < NT; ++i) {
+          float* to = reinterpret_cast<float*>(lds) + g * kSlice + (wave * kRows + 32 * i + (lane & 31)) * kPitch +
+                      4 * (lane >> 5);
+          const f32x16& o = w.o[i][d1 + g];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<f32x4*>(to + 8 * j) = f32x4{o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]} * f[i];
+        }
       meet();
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const int row = 32 * i + threadIdx.x / 8, e = 4 * (threadIdx.x % 8);
-        if (row < live) {
-          f32x4 v = {};
-          float top = -INFINITY, sum = 0.f;
+      for (int g = 0; g < kSlices; ++g) {
+        const int d0 = d1 + g;
+        const float* buf = reinterpret_cast<const float*>(lds) + g * kSlice;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            v += *reinterpret_cast<const f32x4*>(buf + (k * kRows + row) * kPitch + e);
-            top = fmaxf(top, marks[k][row][0]);
-          }
+        for (int i = 0; i < NT; ++i) {
+          const int row = 32 * i + threadIdx.x / 8, e = 4 * (threadIdx.x % 8);
+          if (row < live) {
+            f32x4 v = {};
+            float top = -INFINITY, sum = 0.f;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float m = marks[k][row][0];
-            sum += m == -INFINITY ? 0.f : marks[k][row][1] * __builtin_amdgcn_exp2f(m - top);
-          }
-          if (complete) {
-            const int r = t.first + row;
-            const int64_t token = t.start + r / group;
-            const int qhead = head * group + r % group;
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            if (32 * d0 + e < a.cache.d) store4(a, token, qhead, 32 * d0 + e, v * inv);
-            if (a.lse && d0 == 0 && e == 0) a.lse[token * a.hq + qhead] = lse_of(top, sum);
-          } else {
-            *reinterpret_cast<f32x4*>(slot + row * DT + 32 * d0 + e) = v;
-            if (d0 == 0 && e == 0) {
-              slot[kRows * DT + 2 * row] = top;
-              slot[kRows * DT + 2 * row + 1] = sum;
+            for (int k = 0; k < 4; ++k) {
+              v += *reinterpret_cast<const f32x4*>(buf + (k * kRows + row) * kPitch + e);
+              top = fmaxf(top, marks[k][row][0]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float m = marks[k][row][0];
+              sum += m == -INFINITY ? 0.f : marks[k][row][1] * __builtin_amdgcn_exp2f(m - top);
+            }
+            if (complete) {
+              const int r = t.first + row;
+              const int64_t token = t.start + r / group;
+              const int qhead = head * group + r % group;
+              const float inv = sum == 0.f ? 0.f : 1.f / sum;
+              if (32 * d0 + e < a.cache.d) store4(a, token, qhead, 32 * d0 + e, v * inv);
+              if (a.lse && d0 == 0 && e == 0) a.lse[token * a.hq + qhead] = lse_of(top, sum);
+            } else {
+              *reinterpret_cast<f32x4*>(slot + row * DT + 32 * d0 + e) = v;
+              if (d0 == 0 && e == 0) {
+                slot[kRows * DT + 2 * row] = top;
+                slot[kRows * DT + 2 * row + 1] = sum;
+              }
             }
           }
         }
@@ -1051,9 +1065,11 @@ template <int DT, int NT>
 __global__ __launch_bounds__(kThreads) void attend_narrow_join_kernel(AttendArgs a, const float* parts, const Cut* cuts) {
   constexpr int kRows = 32 * NT;
   const Cut cut = cuts[blockIdx.x];
-  if (cut.sequence < 0) return;
+  if (cut.rows == 0) return;
   const int group = a.hq / a.cache.heads;
-  Tile t = share_of(a, cut.sequence, group, kRows).t;
+  Tile t{};
+  t.start = cut.start;
+  t.rows = cut.rows;
   t.first = cut.first;
   const int live = t.rows - t.first < kRows ? t.rows - t.first : kRows;
   const int64_t x = blockIdx.x, blocks = gridDim.x;
