@@ -511,48 +511,43 @@ __device__ __forceinline__ void store4(const AttendArgs& a, int64_t token, int q
       u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
 }
 
-// Row `row` (of `rows`) of a tile from its `count` partial results slot(0)..: a
-// wave, whose halves take every other one and add up in that order.
+// Row `row` (of `rows`) of a tile from its `count` partial results slot(0)..: a wave,
+// whose groups of as many lanes as a row has fours of values take every so manieth one
+// (each slot read once, its maximum beside its sums) and add up in that order.
 template <int DT, typename Slot>
 __device__ __forceinline__ void join_row(const AttendArgs& a, const Tile& t, int head, int group, Slot&& slot, int count,
                                          int rows, int row, int lane) {
-  const int half = lane >> 5, l = lane & 31;
-  const float* marks = nullptr;
+  constexpr int L = DT <= 64 ? 16 : DT <= 128 ? 32 : 64, G = 64 / L;
+  const int l = lane % L;
   float top = -INFINITY, sum = 0.f;
-  for (int z = lane; z < count; z += 64) {
-    marks = slot(z) + rows * DT + 2 * row;
-    top = fmaxf(top, marks[0]);
-  }
-#pragma unroll
-  for (int off = 1; off < 64; off *= 2) top = fmaxf(top, __shfl_xor(top, off, 64));
-  for (int z = lane; z < count; z += 64) {
-    marks = slot(z) + rows * DT + 2 * row;
-    if (marks[0] > -INFINITY) sum += marks[1] * __builtin_amdgcn_exp2f(marks[0] - top);
-    else sum += marks[1];   // 0, or NaN
-  }
-#pragma unroll
-  for (int off = 1; off < 64; off *= 2) sum += __shfl_xor(sum, off, 64);
-  constexpr int V = (DT + 127) / 128;
-  f32x4 o[V] = {};
+  f32x4 o = {};
+  auto add = [&](float m, float s, f32x4 v) {
+    const float high = fmaxf(top, m), base = high == -INFINITY ? 0.f : high;
+    const float f = __builtin_amdgcn_exp2f(top - base), g = __builtin_amdgcn_exp2f(m - base);
+    sum = f * sum + g * s;
+    o = f * o + g * v;
+    top = high;
+  };
 #pragma unroll 8
-  for (int z = half; z < count; z += 2) {
+  for (int z = lane / L; z < count; z += G) {
     const float* p = slot(z);
-    const float m = p[rows * DT + 2 * row];
-    const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
+    const float m = p[rows * DT + 2 * row], s = p[rows * DT + 2 * row + 1];
+    f32x4 v = {};
+    if (4 * l < DT) v = *reinterpret_cast<const f32x4*>(p + row * DT + 4 * l);
+    add(m, s, v);
+  }
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (128 * i + 4 * l < DT) o[i] += f * *reinterpret_cast<const f32x4*>(p + row * DT + 128 * i + 4 * l);
+  for (int off = L; off < 64; off *= 2) {
+    f32x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = __shfl_xor(o[e], off, 64);
+    add(__shfl_xor(top, off, 64), __shfl_xor(sum, off, 64), v);
   }
   const int r = t.first + row;
   const int64_t token = t.start + r / group;
   const int qhead = head * group + r % group;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[i][e] += other_half(o[i][e]);
-    if (half == 0 && 128 * i + 4 * l < a.cache.d) store4(a, token, qhead, 128 * i + 4 * l, o[i] * inv);
-  }
+  if (lane < L && 4 * l < a.cache.d) store4(a, token, qhead, 4 * l, o * inv);
   if (a.lse && lane == 0) a.lse[token * a.hq + qhead] = lse_of(top, sum);
 }
 
