@@ -511,14 +511,21 @@ __device__ __forceinline__ void store4(const AttendArgs& a, int64_t token, int q
       u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
 }
 
-// Row `row` (of `rows`) of a tile from its `count` partial results slot(0)..: a wave,
-// whose groups of as many lanes as a row has fours of values take every so manieth one
-// (each slot read once, its maximum beside its sums) and add up in that order.
-template <int DT, typename Slot>
+// A wave's groups of as many lanes as a row has fours of values.
+template <int DT>
+__host__ __device__ constexpr int join_lanes() { return DT <= 64 ? 16 : DT <= 128 ? 32 : 64; }
+
+// Row `row` (of `rows`, below `live`) of a tile from its `count` partial results
+// slot(0).., each read once, its maximum beside its sums: a wave, whose groups take
+// every so manieth part and add up in that order, or with kRowEach have a row each,
+// `row` and those after it.
+template <int DT, bool kRowEach, typename Slot>
 __device__ __forceinline__ void join_row(const AttendArgs& a, const Tile& t, int head, int group, Slot&& slot, int count,
-                                         int rows, int row, int lane) {
-  constexpr int L = DT <= 64 ? 16 : DT <= 128 ? 32 : 64, G = 64 / L;
+                                         int rows, int row, int live, int lane) {
+  constexpr int L = join_lanes<DT>(), G = 64 / L;
   const int l = lane % L;
+  if (kRowEach) row += lane / L;
+  if (row >= live) return;
   float top = -INFINITY, sum = 0.f;
   f32x4 o = {};
   auto add = [&](float m, float s, f32x4 v) {
@@ -529,7 +536,7 @@ __device__ __forceinline__ void join_row(const AttendArgs& a, const Tile& t, int
     top = high;
   };
 #pragma unroll 8
-  for (int z = lane / L; z < count; z += G) {
+  for (int z = kRowEach ? 0 : lane / L; z < count; z += kRowEach ? 1 : G) {
     const float* p = slot(z);
     const float m = p[rows * DT + 2 * row], s = p[rows * DT + 2 * row + 1];
     f32x4 v = {};
@@ -537,7 +544,7 @@ __device__ __forceinline__ void join_row(const AttendArgs& a, const Tile& t, int
     add(m, s, v);
   }
 #pragma unroll
-  for (int off = L; off < 64; off *= 2) {
+  for (int off = kRowEach ? 64 : L; off < 64; off *= 2) {
     f32x4 v;
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = __shfl_xor(o[e], off, 64);
@@ -547,8 +554,8 @@ __device__ __forceinline__ void join_row(const AttendArgs& a, const Tile& t, int
   const int64_t token = t.start + r / group;
   const int qhead = head * group + r % group;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  if (lane < L && 4 * l < a.cache.d) store4(a, token, qhead, 4 * l, o * inv);
-  if (a.lse && lane == 0) a.lse[token * a.hq + qhead] = lse_of(top, sum);
+  if ((kRowEach || lane < L) && 4 * l < a.cache.d) store4(a, token, qhead, 4 * l, o * inv);
+  if (a.lse && (kRowEach ? l : lane) == 0) a.lse[token * a.hq + qhead] = lse_of(top, sum);
 }
 
 // ---- many rows: tiles of 128 -----------------------------------------------------------
@@ -725,8 +732,10 @@ void attend_wide_kernel(AttendArgs a, int splits, float* parts) {
   }
 }
 
-// The parts of a tile's rows, a wave a row.
-template <int DT>
+// The parts of a tile's rows.  With few splits a wave has several rows (a chunk of 500
+// and 8 tokens, heads of 64, up to 6 parts: 5.3 us, with a wave for each row 12.3).
+constexpr int kFewSplits = 8;
+template <int DT, bool kFew>
 __global__ __launch_bounds__(kThreads) void attend_wide_join_kernel(AttendArgs a, int splits, const float* parts) {
   const int hk = a.cache.heads, group = a.hq / hk;
   const int tile = __builtin_amdgcn_readfirstlane(blockIdx.x / (uint32_t)hk), head = blockIdx.x - tile * hk;
@@ -736,9 +745,10 @@ __global__ __launch_bounds__(kThreads) void attend_wide_join_kernel(AttendArgs a
   const int count = parts_of(steps_of(span_of(a, t, t.first, t.first + live, group)), splits);
   if (count == 1) return;
   const float* first = parts + ((int64_t)tile * hk + head) * splits * slot_floats<DT>(kWideRows);
-  for (int row = blockIdx.y * 4 + threadIdx.x / 64; row < live; row += 4 * gridDim.y)
-    join_row<DT>(a, t, head, group, [&](int z) { return first + z * slot_floats<DT>(kWideRows); }, count, kWideRows, row,
-                 threadIdx.x & 63);
+  constexpr int each = kFew ? 64 / join_lanes<DT>() : 1;   // rows of a wave
+  for (int row = (blockIdx.y * 4 + threadIdx.x / 64) * each; row < live; row += 4 * each * gridDim.y)
+    join_row<DT, kFew>(a, t, head, group, [&](int z) { return first + z * slot_floats<DT>(kWideRows); }, count, kWideRows,
+                       row, live, threadIdx.x & 63);
 }
 
 // Splits of the keys of a tile: until every CU has the blocks that it takes, twice over.
@@ -1069,8 +1079,9 @@ __global__ __launch_bounds__(kThreads) void attend_narrow_join_kernel(AttendArgs
   const int live = t.rows - t.first < kRows ? t.rows - t.first : kRows;
   const int64_t x = blockIdx.x, blocks = gridDim.x;
   for (int row = blockIdx.y * 4 + threadIdx.x / 64; row < live; row += 4 * gridDim.y)
-    join_row<DT>(a, t, cut.head, group, [&](int z) { return parts + (z ? x + z : blocks + x) * slot_floats<DT>(kRows); },
-                 cut.last - (int)x + 1, kRows, row, threadIdx.x & 63);
+    join_row<DT, false>(a, t, cut.head, group,
+                        [&](int z) { return parts + (z ? x + z : blocks + x) * slot_floats<DT>(kRows); },
+                        cut.last - (int)x + 1, kRows, row, live, threadIdx.x & 63);
 }
 
 // ---- which of them -----------------------------------------------------------------------
@@ -1106,8 +1117,12 @@ hipError_t launch_wide(const AttendArgs& a, float* parts, hipStream_t s) {
   hipLaunchKernelGGL(kernel, dim3((unsigned)(units * splits)), dim3(kThreads), shm, s, a, splits, parts);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
-  hipLaunchKernelGGL(attend_wide_join_kernel<DT>, dim3((unsigned)units, kWideRows / 4), dim3(kThreads), 0, s, a, splits,
-                     parts);
+  if (splits <= kFewSplits)
+    hipLaunchKernelGGL((attend_wide_join_kernel<DT, true>), dim3((unsigned)units, kWideRows * join_lanes<DT>() / 256),
+                       dim3(kThreads), 0, s, a, splits, parts);
+  else
+    hipLaunchKernelGGL((attend_wide_join_kernel<DT, false>), dim3((unsigned)units, kWideRows / 4), dim3(kThreads), 0, s, a,
+                       splits, parts);
   return hipGetLastError();
 }
 
