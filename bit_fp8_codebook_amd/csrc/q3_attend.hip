@@ -511,52 +511,61 @@ __device__ __forceinline__ void store4(const AttendArgs& a, int64_t token, int q
       u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
 }
 
-// A wave's groups of as many lanes as a row has fours of values.
+// A row's partial results, put together: a group of as many lanes as it has fours of
+// values.
 template <int DT>
-__host__ __device__ constexpr int join_lanes() { return DT <= 64 ? 16 : DT <= 128 ? 32 : 64; }
-
-// Row `row` (of `rows`, below `live`) of a tile from its `count` partial results
-// slot(0).., each read once, its maximum beside its sums: a wave, whose groups take
-// every so manieth part and add up in that order, or with kRowEach have a row each,
-// `row` and those after it.
-template <int DT, bool kRowEach, typename Slot>
-__device__ __forceinline__ void join_row(const AttendArgs& a, const Tile& t, int head, int group, Slot&& slot, int count,
-                                         int rows, int row, int live, int lane) {
-  constexpr int L = join_lanes<DT>(), G = 64 / L;
-  const int l = lane % L;
-  if (kRowEach) row += lane / L;
-  if (row >= live) return;
+struct Joined {
+  static constexpr int L = DT <= 64 ? 16 : DT <= 128 ? 32 : 64;
   float top = -INFINITY, sum = 0.f;
   f32x4 o = {};
-  auto add = [&](float m, float s, f32x4 v) {
+
+  __device__ __forceinline__ void add(float m, float s, f32x4 v) {
     const float high = fmaxf(top, m), base = high == -INFINITY ? 0.f : high;
     const float f = __builtin_amdgcn_exp2f(top - base), g = __builtin_amdgcn_exp2f(m - base);
     sum = f * sum + g * s;
     o = f * o + g * v;
     top = high;
-  };
-#pragma unroll 8
-  for (int z = kRowEach ? 0 : lane / L; z < count; z += kRowEach ? 1 : G) {
-    const float* p = slot(z);
-    const float m = p[rows * DT + 2 * row], s = p[rows * DT + 2 * row + 1];
-    f32x4 v = {};
-    if (4 * l < DT) v = *reinterpret_cast<const f32x4*>(p + row * DT + 4 * l);
-    add(m, s, v);
   }
+  // Parts first, first + stride, .. of `count` of row `row` of tiles of `rows`, each read
+  // once, kAtOnce of them under way at a time (behind the last it is asked for again).
+  template <int kAtOnce, typename Slot>
+  __device__ __forceinline__ void gather(Slot&& slot, int first, int stride, int count, int rows, int row, int lane) {
+    const int e = 4 * (lane % L) < DT ? 4 * (lane % L) : 0;
+    for (int z0 = first; z0 < count; z0 += kAtOnce * stride) {
+      float m[kAtOnce], s[kAtOnce];
+      f32x4 v[kAtOnce];
 #pragma unroll
-  for (int off = kRowEach ? 64 : L; off < 64; off *= 2) {
-    f32x4 v;
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int z = z0 + i * stride;
+        const float* p = slot(z < count ? z : count - 1);
+        m[i] = p[rows * DT + 2 * row];
+        s[i] = p[rows * DT + 2 * row + 1];
+        v[i] = *reinterpret_cast<const f32x4*>(p + row * DT + e);
+      }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = __shfl_xor(o[e], off, 64);
-    add(__shfl_xor(top, off, 64), __shfl_xor(sum, off, 64), v);
+      for (int i = 0; i < kAtOnce; ++i)
+        if (z0 + i * stride < count) add(m[i], s[i], v[i]);
+    }
   }
-  const int r = t.first + row;
-  const int64_t token = t.start + r / group;
-  const int qhead = head * group + r % group;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  if ((kRowEach || lane < L) && 4 * l < a.cache.d) store4(a, token, qhead, 4 * l, o * inv);
-  if (a.lse && (kRowEach ? l : lane) == 0) a.lse[token * a.hq + qhead] = lse_of(top, sum);
-}
+  // What the wave's groups hold of one row, in every group.
+  __device__ __forceinline__ void add_groups() {
+#pragma unroll
+    for (int off = L; off < 64; off *= 2) {
+      f32x4 v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = __shfl_xor(o[e], off, 64);
+      add(__shfl_xor(top, off, 64), __shfl_xor(sum, off, 64), v);
+    }
+  }
+  __device__ __forceinline__ void write(const AttendArgs& a, const Tile& t, int head, int group, int row, int lane) const {
+    const int r = t.first + row, l = lane % L;
+    const int64_t token = t.start + r / group;
+    const int qhead = head * group + r % group;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    if (4 * l < a.cache.d) store4(a, token, qhead, 4 * l, o * inv);
+    if (a.lse && l == 0) a.lse[token * a.hq + qhead] = lse_of(top, sum);
+  }
+};
 
 // ---- many rows: tiles of 128 -----------------------------------------------------------
 
@@ -745,10 +754,21 @@ __global__ __launch_bounds__(kThreads) void attend_wide_join_kernel(AttendArgs a
   const int count = parts_of(steps_of(span_of(a, t, t.first, t.first + live, group)), splits);
   if (count == 1) return;
   const float* first = parts + ((int64_t)tile * hk + head) * splits * slot_floats<DT>(kWideRows);
-  constexpr int each = kFew ? 64 / join_lanes<DT>() : 1;   // rows of a wave
-  for (int row = (blockIdx.y * 4 + threadIdx.x / 64) * each; row < live; row += 4 * each * gridDim.y)
-    join_row<DT, kFew>(a, t, head, group, [&](int z) { return first + z * slot_floats<DT>(kWideRows); }, count, kWideRows,
-                       row, live, threadIdx.x & 63);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  auto slot = [&](int z) { return first + z * slot_floats<DT>(kWideRows); };
+  constexpr int L = Joined<DT>::L, G = 64 / L;
+  for (int row0 = (blockIdx.y * 4 + wave) * (kFew ? G : 1); row0 < live; row0 += 4 * gridDim.y * (kFew ? G : 1)) {
+    const int row = kFew ? row0 + lane / L : row0;
+    if (row >= live) break;
+    Joined<DT> x;
+    if (kFew) {
+      x.template gather<4>(slot, 0, 1, count, kWideRows, row, lane);
+    } else {
+      x.template gather<8>(slot, lane / L, G, count, kWideRows, row, lane);
+      x.add_groups();
+    }
+    if (kFew || lane < L) x.write(a, t, head, group, row, lane);
+  }
 }
 
 // Splits of the keys of a tile: until every CU has the blocks that it takes, twice over.
@@ -1065,23 +1085,55 @@ void attend_narrow_kernel(AttendArgs a, float* parts, Cut* cuts) {
   if (threadIdx.x == 0) cuts[blockIdx.x] = cut;
 }
 
-// Block x joins the tile that block x of the kernel above began and others went on with.
+// Blocks (x, y) join the tile that block x of the kernel above began and others went on
+// with: a wave a row, or, of more parts than a wave reads in two turns, a block a row,
+// whose waves take every fourth turn and whose first adds the four up in order (3
+// sequences of 19 tokens over up to 92000, one kv head of 192 values, 85 parts: 12.3
+// us, with a wave a row 38.6; 21 parts of 64 values: 13.5 with a block a row, 5.8 with a
+// wave).
 template <int DT, int NT>
 __global__ __launch_bounds__(kThreads) void attend_narrow_join_kernel(AttendArgs a, const float* parts, const Cut* cuts) {
-  constexpr int kRows = 32 * NT;
+  constexpr int kRows = 32 * NT, L = Joined<DT>::L, G = 64 / L;
+  __shared__ f32x4 sums[3][L];
+  __shared__ float marks[3][2];
   const Cut cut = cuts[blockIdx.x];
-  if (cut.rows == 0) return;
   const int group = a.hq / a.cache.heads;
   Tile t{};
   t.start = cut.start;
   t.rows = cut.rows;
   t.first = cut.first;
-  const int live = t.rows - t.first < kRows ? t.rows - t.first : kRows;
+  const int live = t.rows - t.first < kRows ? t.rows - t.first : kRows;   // 0: no tile
   const int64_t x = blockIdx.x, blocks = gridDim.x;
-  for (int row = blockIdx.y * 4 + threadIdx.x / 64; row < live; row += 4 * gridDim.y)
-    join_row<DT, false>(a, t, cut.head, group,
-                        [&](int z) { return parts + (z ? x + z : blocks + x) * slot_floats<DT>(kRows); },
-                        cut.last - (int)x + 1, kRows, row, live, threadIdx.x & 63);
+  const int count = cut.last - (int)x + 1, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  auto slot = [&](int z) { return parts + (z ? x + z : blocks + x) * slot_floats<DT>(kRows); };
+  if (count <= 16 * G) {
+    const int row = blockIdx.y * 4 + wave;   // there is a wave for each
+    if (row >= live) return;
+    Joined<DT> j;
+    j.template gather<8>(slot, lane / L, G, count, kRows, row, lane);
+    j.add_groups();
+    if (lane < L) j.write(a, t, cut.head, group, row, lane);
+    return;
+  }
+  for (int row = blockIdx.y; row < live; row += gridDim.y) {
+    Joined<DT> j;
+    j.template gather<8>(slot, wave * G + lane / L, 4 * G, count, kRows, row, lane);
+    j.add_groups();
+    if (wave && lane < L) {
+      sums[wave - 1][lane] = j.o;
+      if (lane == 0) {
+        marks[wave - 1][0] = j.top;
+        marks[wave - 1][1] = j.sum;
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x < L) {
+#pragma unroll
+      for (int w = 0; w < 3; ++w) j.add(marks[w][0], marks[w][1], sums[w][lane]);
+      j.write(a, t, cut.head, group, row, lane);
+    }
+    __syncthreads();
+  }
 }
 
 // ---- which of them -----------------------------------------------------------------------
@@ -1118,7 +1170,7 @@ hipError_t launch_wide(const AttendArgs& a, float* parts, hipStream_t s) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
   if (splits <= kFewSplits)
-    hipLaunchKernelGGL((attend_wide_join_kernel<DT, true>), dim3((unsigned)units, kWideRows * join_lanes<DT>() / 256),
+    hipLaunchKernelGGL((attend_wide_join_kernel<DT, true>), dim3((unsigned)units, kWideRows * Joined<DT>::L / 256),
                        dim3(kThreads), 0, s, a, splits, parts);
   else
     hipLaunchKernelGGL((attend_wide_join_kernel<DT, false>), dim3((unsigned)units, kWideRows / 4), dim3(kThreads), 0, s, a,
@@ -1137,7 +1189,8 @@ hipError_t launch_narrow(const AttendArgs& a, float* parts, hipStream_t s) {
   hipLaunchKernelGGL((attend_narrow_kernel<DT, NT>), dim3(blocks), dim3(kThreads), shm, s, a, parts, cuts);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((attend_narrow_join_kernel<DT, NT>), dim3(blocks, 8 * NT), dim3(kThreads), 0, s, a, parts, cuts);
+  static_assert(8192 / blocks * 4 >= 32 * NT, "a wave for each row");
+  hipLaunchKernelGGL((attend_narrow_join_kernel<DT, NT>), dim3(blocks, 8192 / blocks), dim3(kThreads), 0, s, a, parts, cuts);
   return hipGetLastError();
 }
 
