@@ -267,3 +267,17 @@ def test_long_contexts(q3):
                 ll = torch.logsumexp(sc, -1)
                 off = (lse[rows][:, h * 4:h * 4 + 4].double() - ll).abs()
                 assert (off <= 1e-3 + 70001 * F32).all()
+
+
+@pytest.mark.parametrize("d", [64, 80, 128, 192, 256])
+@pytest.mark.parametrize("new,length,hq,hk", [
+    ([1], [20000], 3, 1), ([20, 1], [20000, 9000], 3, 1), ([400], [800], 48, 24), ([200, 3], [3000, 40], 2, 1)])
+def test_many_and_few_parts(q3, new, length, hq, hk, d):
+    # tiles in more parts than blocks read at a time, and in a few
+    rng = np.random.default_rng(17)
+    p = Paged(rng, new, length, hk, d, 64)
+    q = _q(rng, p.m, hq, d)
+    out, lse = _run(q3, p, q, d ** -0.5, 0)
+    _check(p, q, out, lse, d ** -0.5, 0)
+    out2, lse2 = _run(q3, p, q, d ** -0.5, 700)
+    _check(p, q, out2, lse2, d ** -0.5, 700)
