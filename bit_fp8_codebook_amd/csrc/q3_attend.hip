@@ -842,7 +842,7 @@ __device__ __forceinline__ int64_t wave_sum64(int64_t v) {
   return uniform(v);
 }
 
-template <int DT, int NT>
+template <int DT, int NT, bool kRuns>
 __global__ __launch_bounds__(kThreads, DT > 64 ? 1 : 2)
 void attend_narrow_kernel(AttendArgs a, float* parts, Cut* cuts) {
   constexpr int kRows = 32 * NT, R = ring_of<DT>();
@@ -895,7 +895,6 @@ void attend_narrow_kernel(AttendArgs a, float* parts, Cut* cuts) {
   const uint32_t base = lds_offset(mine);
   Loader<DT, 32> loader;
   loader.init(lane, 0);
-  const bool runs = in_runs<DT>(a.cache, 32);
   Pages pages{list, 0};
 
   for (int64_t at = from; at < to;) {
@@ -943,7 +942,7 @@ void attend_narrow_kernel(AttendArgs a, float* parts, Cut* cuts) {
       auto issue = [&](int i, int which) {
         const int key0 = key_w + i * kNarrowStep;
         const uint32_t dst = base + ((i & (R - 1)) * 2 + which) * kTile;
-        if (runs) {
+        if (kRuns) {
           const uint16_t* from = loader.from(a, loader.page_of(a, pages, key0), head, key0, which);
 #pragma unroll
           for (int j = 0; j < N; ++j) loader.load_run(from, which, j, dst);
@@ -1139,12 +1138,16 @@ __global__ __launch_bounds__(kThreads) void attend_narrow_join_kernel(AttendArgs
 // ---- which of them -----------------------------------------------------------------------
 
 enum Form { kNarrow32, kNarrow64, kWide };
-// By the rows that a sequence has on average.  (Two tiles of rows of more than 128
-// values do not fit a wave's registers.)
+// By the rows that a sequence has on average.  8 sequences of 20000, 8 kv heads of 128
+// values: at 32 rows 132 us (narrow, 32) and 135 (wide), at 64 rows 202 (narrow, 32), 146
+// (narrow, 64) and 164, at 72 rows 230 (narrow, 64) and 166; of 256 values at 32 rows
+// 247 and 299, at 48 (narrow, 32: two tiles) 556 and 388 (two tiles at a time do not fit
+// a wave's registers there).  Unlike lengths are a reason for the narrow ones besides:
+// 64 single tokens over up to 16384, heads of 192, 533 us and 829.
 Form form_of(int64_t m, int64_t sequences, int group, int dim) {
   const int64_t rows = m * group;
-  if (rows <= 32 * sequences || (dim > 128 && rows <= 64 * sequences)) return kNarrow32;
-  return rows <= 128 * sequences && dim <= 128 ? kNarrow64 : kWide;
+  if (rows <= 32 * sequences) return kNarrow32;
+  return rows <= 64 * sequences && dim <= 128 ? kNarrow64 : kWide;
 }
 
 template <typename F>
@@ -1183,10 +1186,12 @@ hipError_t launch_narrow(const AttendArgs& a, float* parts, hipStream_t s) {
   constexpr int blocks = narrow_blocks<DT>();
   constexpr size_t shm = narrow_bytes<DT>();
   Cut* cuts = reinterpret_cast<Cut*>(parts + 2 * blocks * slot_floats<DT>(32 * NT));
-  static LdsAllowance seen;
-  const hipError_t ok = allow_dynamic_lds(reinterpret_cast<const void*>(attend_narrow_kernel<DT, NT>), shm, seen);
+  static LdsAllowance seen, seen_runs;
+  const bool runs = in_runs<DT>(a.cache, 32);
+  auto* kernel = runs ? attend_narrow_kernel<DT, NT, true> : attend_narrow_kernel<DT, NT, false>;
+  const hipError_t ok = allow_dynamic_lds(reinterpret_cast<const void*>(kernel), shm, runs ? seen_runs : seen);
   if (ok != hipSuccess) return ok;
-  hipLaunchKernelGGL((attend_narrow_kernel<DT, NT>), dim3(blocks), dim3(kThreads), shm, s, a, parts, cuts);
+  hipLaunchKernelGGL(kernel, dim3(blocks), dim3(kThreads), shm, s, a, parts, cuts);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   static_assert(8192 / blocks * 4 >= 32 * NT, "a wave for each row");
