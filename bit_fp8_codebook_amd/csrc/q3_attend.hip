@@ -783,10 +783,10 @@ int wide_splits(int64_t units, int dim) {
 
 // Bound by the cache's bytes.  Each wave of a block streams keys and values of its
 // own, 32 at a time, through its own part of LDS: no barrier stands in the stream,
-// and while a wave computes on one tile, one to three are on their way.  The four
+// and while a wave computes on one tile, others are on their way.  The four
 // waves take every fourth tile and join their sums through LDS at the end.
 //
-// A fixed number of blocks, one or two a CU, shares out the whole batch's work,
+// A fixed number of blocks, one to three a CU, shares out the whole batch's work,
 // counted in steps of 128 keys: sequences in order, in each the kv heads, in each
 // the tiles of rows, in each the steps.  A block takes an equal run of steps,
 // wherever it begins and ends, so that contexts of any lengths load the chip
@@ -794,12 +794,20 @@ int wide_splits(int64_t units, int dim) {
 // block has at most one tile that it continues and one that others continue), and
 // a second launch joins them in order.
 constexpr int kNarrowStep = 128;
-template <int DT>
-constexpr int ring_of() { return DT > 128 ? 1 : 2; }   // tiles of keys, and of values, in a wave's part of LDS
-template <int DT>
-constexpr size_t narrow_bytes() { return 4 * ring_of<DT>() * 2 * 32 * Layout<DT>::row; }
-template <int DT>
-constexpr int narrow_blocks() { return DT > 64 ? 256 : 512; }
+// Blocks of a CU, as many as registers allow, so that some stream while another begins
+// or ends a tile, and how many tiles of keys, and of values, a wave's part of LDS holds.
+// Heads of 128, two blocks with one tile each against one block with two: 64 single
+// tokens over up to 500 positions 36 and 55 us, over up to 16384 359 and 372.  Heads of
+// 64, three with one tile against two with two: 22 and 26, 200 and 199 (four: 37 and
+// 281, spilled).
+template <int DT, int NT>
+constexpr int per_cu() { return NT == 1 ? (DT <= 64 ? 3 : DT <= 128 ? 2 : 1) : DT <= 64 ? 2 : 1; }
+template <int DT, int NT>
+constexpr int ring_of() { return NT == 1 || DT > 128 ? 1 : 2; }
+template <int DT, int NT>
+constexpr size_t narrow_bytes() { return 4 * ring_of<DT, NT>() * 2 * 32 * Layout<DT>::row; }
+template <int DT, int NT>
+constexpr int narrow_blocks() { return 256 * per_cu<DT, NT>(); }
 
 // A block's tile that others continue: what the second launch joins.
 struct Cut {
@@ -843,9 +851,9 @@ __device__ __forceinline__ int64_t wave_sum64(int64_t v) {
 }
 
 template <int DT, int NT, bool kRuns>
-__global__ __launch_bounds__(kThreads, DT > 64 ? 1 : 2)
+__global__ __launch_bounds__(kThreads, (per_cu<DT, NT>()))
 void attend_narrow_kernel(AttendArgs a, float* parts, Cut* cuts) {
-  constexpr int kRows = 32 * NT, R = ring_of<DT>();
+  constexpr int kRows = 32 * NT, R = ring_of<DT, NT>();
   constexpr uint32_t kTile = 32 * Layout<DT>::row;
   constexpr int N = kTile / 1024;   // loads of a tile
   extern __shared__ __align__(16) uint8_t lds[];
@@ -861,7 +869,7 @@ void attend_narrow_kernel(AttendArgs a, float* parts, Cut* cuts) {
   };
 
   // The block's run of steps [from, to), and the sequence that holds its first.
-  constexpr int blocks = narrow_blocks<DT>();
+  constexpr int blocks = narrow_blocks<DT, NT>();
   auto running = [&](int64_t v) {   // sums of lanes 0..lane
 #pragma unroll
     for (int off = 1; off < 64; off *= 2) {
@@ -1022,7 +1030,7 @@ void attend_narrow_kernel(AttendArgs a, float* parts, Cut* cuts) {
     float* slot = parts + (blockIdx.x + (c0 == 0 ? (int64_t)gridDim.x : 0)) * slot_floats<DT>(kRows);
     constexpr int kPitch = 36;   // floats of 32 values and room against bank conflicts
     constexpr int kAll = DT / 32, kSlice = 4 * kRows * kPitch;
-    constexpr int kFit = (int)(narrow_bytes<DT>() / (4 * kSlice));
+    constexpr int kFit = (int)(narrow_bytes<DT, NT>() / (4 * kSlice));
     // (Two tiles of rows have no registers left for more than one slice.)
     constexpr int kSlices = NT > 1 ? 1 : kFit >= kAll ? kAll : kFit >= 2 && kAll % 2 == 0 ? 2 : 1;
     static_assert(kFit >= kSlices, "");
@@ -1183,8 +1191,8 @@ hipError_t launch_wide(const AttendArgs& a, float* parts, hipStream_t s) {
 
 template <int DT, int NT>
 hipError_t launch_narrow(const AttendArgs& a, float* parts, hipStream_t s) {
-  constexpr int blocks = narrow_blocks<DT>();
-  constexpr size_t shm = narrow_bytes<DT>();
+  constexpr int blocks = narrow_blocks<DT, NT>();
+  constexpr size_t shm = narrow_bytes<DT, NT>();
   Cut* cuts = reinterpret_cast<Cut*>(parts + 2 * blocks * slot_floats<DT>(32 * NT));
   static LdsAllowance seen, seen_runs;
   const bool runs = in_runs<DT>(a.cache, 32);
@@ -1206,8 +1214,9 @@ int64_t attend_workspace_bytes(int64_t m, int64_t sequences, int32_t hq, int32_t
     constexpr int DT = decltype(dim)::value;
     const Form form = form_of(m, sequences, hq / hk, DT);
     if (form != kWide) {
-      const int64_t blocks = narrow_blocks<DT>();
-      return blocks * (2 * 4 * slot_floats<DT>(form == kNarrow32 ? 32 : 64) + (int64_t)sizeof(Cut));
+      const bool one = form == kNarrow32;
+      const int64_t blocks = one ? narrow_blocks<DT, 1>() : narrow_blocks<DT, 2>();
+      return blocks * (2 * 4 * slot_floats<DT>(one ? 32 : 64) + (int64_t)sizeof(Cut));
     }
     const int64_t units = tiles_of(m, sequences, hq / hk, kWideRows) * hk;
     const int splits = wide_splits(units, DT);

@@ -87,7 +87,7 @@ def test_scales(q3, scale, new):
     _check(p, q, out, lse, scale, 0)
 
 
-FORMS = [(1, 4, 1), (6, 4, 1), (6, 16, 1), (50, 8, 2), (130, 2, 1), (70, 6, 2)]   # new, hq, hk: rows of each kernel form
+FORMS = [(1, 4, 1), (6, 4, 1), (6, 16, 1), (12, 4, 1), (20, 4, 1), (50, 8, 2), (130, 2, 1), (70, 6, 2)]   # new, hq, hk: rows of each kernel form
 
 
 @pytest.mark.parametrize("d", [64, 128, 240, 256])
