@@ -586,6 +586,12 @@ __device__ __forceinline__ int steps_of(const Span& span) {
   return (span.hi - (span.lo & ~(kStep - 1)) + kStep - 1) / kStep;
 }
 
+// Blocks of a launch for each part: those of (head, tile), and some that find nothing
+// where heads are shared by XCDs.
+__host__ __device__ __forceinline__ uint32_t wide_units(int64_t tiles, int hk) {
+  return (uint32_t)(hk < 8 && 8 % hk == 0 ? (tiles + 8 / hk - 1) / (8 / hk) * 8 : tiles * hk);
+}
+
 // Four waves with 32 rows each share 64 keys at a time through a ring of LDS
 // buffers.  The loads of a step are asked for beside the products of scores, up to
 // three steps ahead.  kRuns: 16 keys are in one page, whole rows.
@@ -600,14 +606,27 @@ void attend_wide_kernel(AttendArgs a, int splits, float* parts) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int hk = a.cache.heads, group = a.hq / hk;
 
-  // Contiguous runs of (head, tile) to each XCD: tiles that read the same keys share an L2.
+  // An XCD takes whole heads, or every so manieth tile of one: tiles that read the same
+  // keys share an L2, and the XCDs have as much to do (4 kv heads of 256, 2048 tokens of
+  // 16 heads over 16000: 670 us, with a run of tiles for each XCD, of which one had a
+  // block more than CUs, 1282; 4096 over 4096: 218 and 406).
   const uint32_t tiles = (uint32_t)tiles_of(a.m, a.batch.sequences, group, kWideRows);
-  const uint32_t total = tiles * hk;   // below 2^24
+  const uint32_t total = wide_units(tiles, hk);   // below 2^24
   const int z = __builtin_amdgcn_readfirstlane(blockIdx.x / total);
-  const uint32_t id = blockIdx.x - z * total, per = total >> 3, rem = total & 7, xcd = id & 7;
-  const uint32_t unit = xcd * per + (xcd < rem ? xcd : rem) + (id >> 3);
-  const int head = __builtin_amdgcn_readfirstlane(unit / tiles);
-  const int64_t tile = tiles - 1 - (unit - head * tiles);     // the long ones of a chunk first
+  const uint32_t id = blockIdx.x - z * total, xcd = id & 7;
+  uint32_t unit, place;
+  if (hk < 8 && 8 % hk == 0) {
+    const uint32_t each = 8 / hk;   // XCDs of a head
+    unit = xcd / each;
+    place = (id >> 3) * each + xcd % each;
+  } else {
+    const uint32_t per = total >> 3, rem = total & 7, at = xcd * per + (xcd < rem ? xcd : rem) + (id >> 3);
+    unit = at / tiles;
+    place = at - unit * tiles;
+  }
+  if (place >= tiles) return;
+  const int head = __builtin_amdgcn_readfirstlane(unit);
+  const int64_t tile = tiles - 1 - __builtin_amdgcn_readfirstlane(place);     // the long ones of a chunk first
   const Tile t = find_tile(a, tile, group, kWideRows, lane);
   if (t.sequence == a.batch.sequences) return;
   const int live = t.rows - t.first < kWideRows ? t.rows - t.first : kWideRows;
@@ -1177,7 +1196,8 @@ hipError_t launch_wide(const AttendArgs& a, float* parts, hipStream_t s) {
   auto* kernel = runs ? attend_wide_kernel<DT, true> : attend_wide_kernel<DT, false>;
   const hipError_t ok = allow_dynamic_lds(reinterpret_cast<const void*>(kernel), shm, runs ? seen_runs : seen);
   if (ok != hipSuccess) return ok;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)(units * splits)), dim3(kThreads), shm, s, a, splits, parts);
+  hipLaunchKernelGGL(kernel, dim3(wide_units(units / a.cache.heads, a.cache.heads) * splits), dim3(kThreads), shm, s, a,
+                     splits, parts);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
   if (splits <= kFewSplits)
