@@ -6,6 +6,10 @@
 // rows of a sequence and kv head are its (token, head of the group) pairs, token
 // by token, so that one decoded token, a few drafted ones and a long chunk are the
 // same product with more or fewer rows, and keys are read once for a whole group.
+//
+// Few rows are bound by the cache's bytes (64 tokens over up to 16384, 8 kv heads of
+// 128: 437 us, 5.6 TB/s), many by the products, the reads of their fragments and the
+// exponentials (2048 over 32000, 32 heads of 128: 1.02 ms, 1.02 PFLOP/s).
 #include <type_traits>
 
 #include "q3_device.h"
@@ -595,6 +599,15 @@ __host__ __device__ __forceinline__ uint32_t wide_units(int64_t tiles, int hk) {
 // Four waves with 32 rows each share 64 keys at a time through a ring of LDS
 // buffers.  The loads of a step are asked for beside the products of scores, up to
 // three steps ahead.  kRuns: 16 keys are in one page, whole rows.
+//
+// Heads of 128, two waves a SIMD: for each pair of steps there the products take 2048
+// cycles, the CU's reads of fragments from LDS 2048 and its writes 512, and the vector
+// work about 2000, of which 1024 are the exponentials.  A step of 32000 keys' worth took
+// 4500 cycles a pair, so that these still stand behind one another more than beside.
+// Measured and not kept: 64 rows a wave, which halves the reads (its sums move between
+// the register files: 2450 us for 1021), eight waves and 256 rows (1060 to 1110), the
+// two waves' halves of a step apart (1110 to 1191), 32 keys a step for heads of 256
+// (907 for 670).
 template <int DT, bool kRuns>
 __global__ __launch_bounds__(kThreads, wide_blocks(DT))
 void attend_wide_kernel(AttendArgs a, int splits, float* parts) {
@@ -790,7 +803,10 @@ __global__ __launch_bounds__(kThreads) void attend_wide_join_kernel(AttendArgs a
   }
 }
 
-// Splits of the keys of a tile: until every CU has the blocks that it takes, twice over.
+// Splits of the keys of a tile: until every CU has the blocks that it takes, twice over,
+// where three quarters of them are not there without (32 heads of 128 over 32000: 800
+// tokens, 208 units, 513 us, until once over 578; 1300 tokens, 336 units, 714 and in
+// one part 865; 1700 tokens, 432 units, 946 in one part and 987 in two).
 int wide_splits(int64_t units, int dim) {
   const int64_t want = 256 * wide_blocks(dim);
   if (4 * units >= 3 * want) return 1;

@@ -20,6 +20,13 @@
 // not full yet, the top-th largest of the 64 lanes' maxima is a bound that at least
 // that many entries reach (found bit by bit, 18 of 32 bits: a lower bound is one
 // too).  What passes is packed behind one another and ranked by counting.
+//
+// Measured: 2048 rows of 151936 214 us (5.8 TB/s), 2047 of 50257 74 us.  64 rows of
+// 151936 take 13 us without top alternatives, 20 with the best one and 26 with 20: 21
+// in the parts and 6 in the join, a chain of lists rather than memory; one row of 32000
+// 6.5, 11.5 and 13.  One list for a block, with a barrier for each chunk, took 29 for the
+// 26 and 13.7 for the 13; packed bounds over the waves' lists instead of merges 26.6
+// and 13.1.
 #include "q3_device.h"
 #include "../../include/q3_block.h"
 #include "q3_internal.h"
@@ -381,7 +388,9 @@ __global__ __launch_bounds__(256) void logprobs_back_kernel(LogprobBackArgs a, i
   }
 }
 
-// Parts of a row: blocks for the whole chip where rows are few, whole chunks each.
+// Parts of a row: blocks for the whole chip where rows are few, whole chunks each (64
+// rows of 151936, best 20: 28 us a call with about 512 blocks, 28 with 1024, 30 with 2048,
+// whose lists cost more to join; one row of 32000 22 with any).
 int parts_of(int64_t m, int64_t n) {
   const int64_t chunks = (n + kChunk - 1) / kChunk, want = (1024 + m - 1) / m;
   const int64_t each = (chunks + want - 1) / want;
