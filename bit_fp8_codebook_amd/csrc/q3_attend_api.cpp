@@ -144,7 +144,7 @@ Q3_API q3_status q3_qk_norm_rope(const q3_head_norms* heads, const float* qkv, i
 
 Q3_API int64_t q3_qk_norm_rope_backward_workspace_bytes(int64_t m, int32_t head_dim) {
   if (m < 1 || m >= kMaxM || bad_head_dim(head_dim)) return 0;
-  return align256(q3::rope_back_groups(m) * 2 * head_dim * 4);
+  return align256(q3::rope_back_rows(m) * 2 * head_dim * 4);
 }
 
 Q3_API q3_status q3_qk_norm_rope_backward(const q3_head_norms* heads, const float* qkv, int64_t ld,
@@ -194,7 +194,6 @@ Q3_API q3_status q3_qk_norm_rope_backward(const q3_head_norms* heads, const floa
   a.dwk = g.dk_weight;
   a.part = g.dq_weight || g.dk_weight ? static_cast<float*>(workspace) : nullptr;
   a.m = m;
-  a.groups = q3::rope_back_groups(m);
   return from_hip(q3::launch_qk_norm_rope_back(a, g.d_type, static_cast<hipStream_t>(stream)));
 }
 

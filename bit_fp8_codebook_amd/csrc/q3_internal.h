@@ -261,13 +261,13 @@ struct RopeBackArgs {
   int64_t ld_dv;
   uint16_t* dqkv;
   int64_t ld_out;
-  float* part;      // [groups][2][d]; null: no weight gradients
+  float* part;      // [rope_back_rows][2][d]; null: no weight gradients
   float* dwq;
   float* dwk;
   int64_t m;
   int64_t groups;
 };
-int64_t rope_back_groups(int64_t m);
+int64_t rope_back_rows(int64_t m);   // rows of partial sums
 hipError_t launch_qk_norm_rope_back(const RopeBackArgs& a, int32_t d_type, hipStream_t s);
 
 // Attention over a paged cache (q3_attend.hip).

@@ -18,8 +18,8 @@
 //
 // Measured: 4 prompts' 6054 tokens of 32 + 2 x 8 heads of 128 40 us, 5.6 TB/s (with a
 // kernel for all pairings 46, with halves through LDS and angles by the library's sine
-// 70); one token 4.3 us.  Backward, 4095 tokens of 80 heads of 128, 77 us and 4.6 for the
-// weights' sums (92 and 4.6).
+// 70); one token 4.3 us.  Backward, 4095 tokens of 80 heads of 128, 56 us, 6.0 TB/s, and 4.7 for the
+// weights' sums (with a kernel for all pairings 92).
 #include <type_traits>
 
 #include "q3_device.h"
@@ -97,11 +97,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const bf16x2 v = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
   return __builtin_bit_cast(uint32_t, v);
 }
+template <bool kPast = false>   // past the caches
 __device__ __forceinline__ void store8(uint16_t* p, const Places& at, const Vec8& x) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-    *reinterpret_cast<u32x2*>(p + at.e[h]) =
-        u32x2{pack_bf16(x.v[4 * h], x.v[4 * h + 1]), pack_bf16(x.v[4 * h + 2], x.v[4 * h + 3])};
+  for (int h = 0; h < 2; ++h) {
+    const u32x2 u = {pack_bf16(x.v[4 * h], x.v[4 * h + 1]), pack_bf16(x.v[4 * h + 2], x.v[4 * h + 3])};
+    u32x2* to = reinterpret_cast<u32x2*>(p + at.e[h]);
+    if constexpr (kPast) __builtin_nontemporal_store(u, to);
+    else *to = u;
+  }
 }
 // A weight's values (4-byte aligned); ones without one.
 __device__ __forceinline__ Vec8 weight8(const float* w, const Places& at) {
@@ -246,8 +250,10 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(RopeArgs a) {
   }
 }
 
-// Blocks walk the tokens; a thread adds up the weight gradients of its eight
-// values over its heads, the block's groups are added in order at the end.
+// Blocks walk the tokens (blockIdx.y takes every gridDim.y-th run of heads); a thread
+// adds up the weight gradients of its eight values over its heads, the block's groups are
+// added in order at the end.  The gradients go past the caches, which the rows of the
+// tokens on their way fill (4095 tokens of 80 heads of 128, both launches: 76 us, without 84).
 template <int L, int P, typename E>
 __global__ __launch_bounds__(kThreads, 4) void qk_norm_rope_back_kernel(RopeBackArgs a) {
   __shared__ __align__(16) Turn turn[2];
@@ -274,19 +280,21 @@ __global__ __launch_bounds__(kThreads, 4) void qk_norm_rope_back_kernel(RopeBack
     return o;
   };
   int parity = 0;
-  Head next = load(blockIdx.x, threadIdx.x / L);
+  const int first = blockIdx.y * kHeads, stride = gridDim.y * kHeads;
+  Head next = load(blockIdx.x, first + threadIdx.x / L);
   for (int64_t row = blockIdx.x; row < a.m; row += a.groups, parity ^= 1) {
     // The other buffer's readers are a barrier behind.
     for (int t = threadIdx.x; t < a.rot / 2; t += kThreads)
       angle_of((double)a.positions[row], a.freq[t], turn[parity][0][t], turn[parity][1][t]);
     __syncthreads();
-    for (int h0 = 0; h0 < heads; h0 += kHeads) {
+    for (int h0 = first; h0 < heads; h0 += stride) {
       const int h = h0 + threadIdx.x / L;
       const bool query = h < a.hq, value = h >= a.hq + a.hk;
       Head cur = next;
       // The next heads', or the next token's first, while these are worked on.
-      const bool more = h0 + kHeads < heads;
-      if (more || row + a.groups < a.m) next = load(more ? row : row + a.groups, (more ? h0 + kHeads : 0) + threadIdx.x / L);
+      const bool more = h0 + stride < heads;
+      if (more || row + a.groups < a.m)
+        next = load(more ? row : row + a.groups, (more ? h0 + stride : first) + threadIdx.x / L);
       const bool norm = !value && (query ? a.wq : a.wk);
       Vec8 x = cur.x, g = cur.g, dn = g;
       rotate<L, P>(dn, at, a.rot, turn[parity], -1.f, swap[P == kOddHalves ? wave : 0], lane);
@@ -315,11 +323,12 @@ __global__ __launch_bounds__(kThreads, 4) void qk_norm_rope_back_kernel(RopeBack
       } else if (!value) {
         g = dn;
       }
-      store8(a.dqkv + row * a.ld_out + h * a.d, at, g);
+      store8<true>(a.dqkv + row * a.ld_out + h * a.d, at, g);
     }
   }
   if (!a.part) return;
   __shared__ float all[kThreads][9];   // 9: no two lanes of a step on one bank
+#pragma unroll
   for (int k = 0; k < 2; ++k) {
     __syncthreads();
 #pragma unroll
@@ -331,7 +340,11 @@ __global__ __launch_bounds__(kThreads, 4) void qk_norm_rope_back_kernel(RopeBack
       if (l >= a.d / 8) continue;
       float v = 0.f;
       for (int g = 0; g < kHeads; ++g) v += all[g * L + l][i];
-      a.part[((int64_t)blockIdx.x * 2 + k) * a.d + places<P>(l, a.d, a.rot).e[i / 4] + i % 4] = v;
+      // (An array's element at i / 4 would go through LDS, and its address through the
+      // block's size, read from host memory: 14 us of a call of 70 tokens.)
+      const Places of = places<P>(l, a.d, a.rot);
+      const int column = (i < 4 ? of.e[0] : of.e[1]) + i % 4;
+      a.part[(((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 2 + k) * a.d + column] = v;
     }
   }
 }
@@ -376,8 +389,9 @@ hipError_t launch_qk_norm_rope(const RopeArgs& args, hipStream_t s) {
   return by_lanes(args.d, pairing_of(args.rot, args.interleaved), [&](auto lanes, auto pairing) {
     constexpr int L = decltype(lanes)::value, P = decltype(pairing)::value;
     const int runs = (args.hq + 2 * args.hk + kThreads / L - 1) / (kThreads / L);
-    // Few tokens: a block per run of heads, so that one token's heads load at once.
-    const unsigned split = args.m >= 1024 ? 1u : (unsigned)runs;
+    // Few tokens: a block per run of heads, so that one token's heads load at once (48
+    // heads of 128: 64 tokens 4.4 us, without 5.1; 256 tokens 7.1 and 6.1; 1000 17.4 and 11.8).
+    const unsigned split = args.m >= 128 ? 1u : (unsigned)runs;
     RopeArgs a = args;
     constexpr int64_t most = int64_t(1) << 22;   // a launch takes less than 2^32 threads
     for (a.first = 0; a.first < a.m; a.first += most) {
@@ -390,21 +404,30 @@ hipError_t launch_qk_norm_rope(const RopeArgs& args, hipStream_t s) {
   });
 }
 
-// Blocks of the backward pass: four a CU, each leaves one row of partial sums.
-int64_t rope_back_groups(int64_t m) { return m < 1024 ? m : 1024; }
+// Blocks of the backward pass: four a CU, each leaves one row of partial sums (4095
+// tokens: 75 us, with 768 blocks 85, with 2048 80).
+constexpr int64_t kBackBlocks = 1024;
+int64_t rope_back_rows(int64_t m) { return m > 0 ? kBackBlocks : 0; }
 
-hipError_t launch_qk_norm_rope_back(const RopeBackArgs& a, int32_t d_type, hipStream_t s) {
+hipError_t launch_qk_norm_rope_back(const RopeBackArgs& args, int32_t d_type, hipStream_t s) {
+  RopeBackArgs a = args;
+  a.groups = a.m < kBackBlocks ? a.m : kBackBlocks;
+  int64_t rows = 0;   // of partial sums
   const hipError_t err = by_lanes(a.d, pairing_of(a.rot, a.interleaved), [&](auto lanes, auto pairing) {
     constexpr int L = decltype(lanes)::value, P = decltype(pairing)::value;
+    // Few tokens: their heads in runs, as in the forward pass (48 heads of 128: 70 tokens 9.0
+    // us with the sums' launch, in one run 10.9; 300 tokens 14.4 and 13.4).
+    const int64_t runs = (a.hq + 2 * a.hk + kThreads / L - 1) / (kThreads / L), most = a.m < 128 ? kBackBlocks / a.groups : 1;
+    const dim3 grid((unsigned)a.groups, (unsigned)(runs < most ? runs : most));
+    rows = (int64_t)grid.x * grid.y;
     if (d_type == Q3_BF16)
-      hipLaunchKernelGGL((qk_norm_rope_back_kernel<L, P, uint16_t>), dim3((unsigned)a.groups), dim3(kThreads), 0, s,
-                         a);
+      hipLaunchKernelGGL((qk_norm_rope_back_kernel<L, P, uint16_t>), grid, dim3(kThreads), 0, s, a);
     else
-      hipLaunchKernelGGL((qk_norm_rope_back_kernel<L, P, float>), dim3((unsigned)a.groups), dim3(kThreads), 0, s, a);
+      hipLaunchKernelGGL((qk_norm_rope_back_kernel<L, P, float>), grid, dim3(kThreads), 0, s, a);
     return hipGetLastError();
   });
   if (err != hipSuccess || !a.part) return err;
-  hipLaunchKernelGGL(rope_reduce_kernel, dim3((unsigned)(2 * a.d / 16)), dim3(1024), 0, s, a.part, a.groups, a.d,
+  hipLaunchKernelGGL(rope_reduce_kernel, dim3((unsigned)(2 * a.d / 16)), dim3(1024), 0, s, a.part, rows, a.d,
                      a.dwq, a.dwk);
   return hipGetLastError();
 }
