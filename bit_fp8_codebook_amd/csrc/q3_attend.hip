@@ -571,6 +571,49 @@ struct Joined {
   }
 };
 
+// The rows of a tile from its parts: a wave a row, or, of more parts than a wave reads in
+// two turns, a block a row, whose waves take every fourth turn and whose first adds the
+// four up in order (3 sequences of 19 tokens over up to 92000, one kv head of 192
+// values, 85 parts: 12.3 us, with a wave a row 38.6; 21 parts of 64 values: 13.5 with a
+// block a row, 5.8 with a wave).  Blocks of four waves, blockIdx.y takes every
+// gridDim.y-th of the rows, or of the fours of them.
+template <int DT, typename Slot>
+__device__ __forceinline__ void join_rows(const AttendArgs& a, const Tile& t, int head, int group, Slot&& slot, int count,
+                                          int rows, int live) {
+  constexpr int L = Joined<DT>::L, G = 64 / L;
+  __shared__ f32x4 sums[3][L];
+  __shared__ float marks[3][2];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (count <= 16 * G) {
+    for (int row = blockIdx.y * 4 + wave; row < live; row += 4 * gridDim.y) {
+      Joined<DT> j;
+      j.template gather<8>(slot, lane / L, G, count, rows, row, lane);
+      j.add_groups();
+      if (lane < L) j.write(a, t, head, group, row, lane);
+    }
+    return;
+  }
+  for (int row = blockIdx.y; row < live; row += gridDim.y) {
+    Joined<DT> j;
+    j.template gather<8>(slot, wave * G + lane / L, 4 * G, count, rows, row, lane);
+    j.add_groups();
+    if (wave && lane < L) {
+      sums[wave - 1][lane] = j.o;
+      if (lane == 0) {
+        marks[wave - 1][0] = j.top;
+        marks[wave - 1][1] = j.sum;
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x < L) {
+#pragma unroll
+      for (int w = 0; w < 3; ++w) j.add(marks[w][0], marks[w][1], sums[w][lane]);
+      j.write(a, t, head, group, row, lane);
+    }
+    __syncthreads();
+  }
+}
+
 // ---- many rows: tiles of 128 -----------------------------------------------------------
 
 constexpr int kStep = 64, kWideRows = 128, kThreads = 256;   // keys of a step, rows of a tile
@@ -579,21 +622,26 @@ constexpr int kStep = 64, kWideRows = 128, kThreads = 256;   // keys of a step, 
 __host__ __device__ constexpr int wide_blocks(int dim) { return dim > 128 ? 1 : 2; }
 __host__ __device__ constexpr int wide_ring(int dim) { return dim > 192 ? 2 : dim > 128 ? 3 : dim > 64 ? 2 : 4; }
 
-// Parts that a tile's steps go to: at most `splits`, of six steps at least (a call of a
-// prompt of 500 and 8 single tokens with a window: 35 us, with four steps 41, with
-// twelve 37).
+// Parts that a tile's steps go to: at most `splits`, of three steps at least (2 x 208
+// tokens over 1233, 4 kv heads of 256: 40 us, with six 45, with one 58; 4 x 387 over up
+// to 402, one head of 192: 26, 30 and 23).
 __device__ __forceinline__ int parts_of(int steps, int splits) {
-  const int most = (steps + 5) / 6;
+  const int most = (steps + 2) / 3;
   return most < splits ? (most > 0 ? most : 1) : splits;
 }
 __device__ __forceinline__ int steps_of(const Span& span) {
   return (span.hi - (span.lo & ~(kStep - 1)) + kStep - 1) / kStep;
 }
 
+// Whether XCDs share heads.  Not with a few tiles, whose parts have to go round (89 tokens
+// over 16464, 2 heads of 192: 41 us, 62 with both heads' parts on an XCD each).
+__host__ __device__ __forceinline__ bool heads_share(int64_t tiles, int hk) {
+  return hk < 8 && 8 % hk == 0 && tiles * hk >= 64;
+}
 // Blocks of a launch for each part: those of (head, tile), and some that find nothing
-// where heads are shared by XCDs.
+// where XCDs share heads.
 __host__ __device__ __forceinline__ uint32_t wide_units(int64_t tiles, int hk) {
-  return (uint32_t)(hk < 8 && 8 % hk == 0 ? (tiles + 8 / hk - 1) / (8 / hk) * 8 : tiles * hk);
+  return (uint32_t)(heads_share(tiles, hk) ? (tiles + 8 / hk - 1) / (8 / hk) * 8 : tiles * hk);
 }
 
 // Four waves with 32 rows each share 64 keys at a time through a ring of LDS
@@ -628,7 +676,7 @@ void attend_wide_kernel(AttendArgs a, int splits, float* parts) {
   const int z = __builtin_amdgcn_readfirstlane(blockIdx.x / total);
   const uint32_t id = blockIdx.x - z * total, xcd = id & 7;
   uint32_t unit, place;
-  if (hk < 8 && 8 % hk == 0) {
+  if (heads_share(tiles, hk)) {
     const uint32_t each = 8 / hk;   // XCDs of a head
     unit = xcd / each;
     place = (id >> 3) * each + xcd % each;
@@ -774,7 +822,7 @@ void attend_wide_kernel(AttendArgs a, int splits, float* parts) {
 }
 
 // The parts of a tile's rows.  With few splits a wave has several rows (a chunk of 500
-// and 8 tokens, heads of 64, up to 6 parts: 5.3 us, with a wave for each row 12.3).
+// and 8 tokens, heads of 64, three parts: 5.3 us, with a wave for each row 12.3).
 constexpr int kFewSplits = 8;
 template <int DT, bool kFew>
 __global__ __launch_bounds__(kThreads) void attend_wide_join_kernel(AttendArgs a, int splits, const float* parts) {
@@ -786,31 +834,29 @@ __global__ __launch_bounds__(kThreads) void attend_wide_join_kernel(AttendArgs a
   const int count = parts_of(steps_of(span_of(a, t, t.first, t.first + live, group)), splits);
   if (count == 1) return;
   const float* first = parts + ((int64_t)tile * hk + head) * splits * slot_floats<DT>(kWideRows);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   auto slot = [&](int z) { return first + z * slot_floats<DT>(kWideRows); };
-  constexpr int L = Joined<DT>::L, G = 64 / L;
-  for (int row0 = (blockIdx.y * 4 + wave) * (kFew ? G : 1); row0 < live; row0 += 4 * gridDim.y * (kFew ? G : 1)) {
-    const int row = kFew ? row0 + lane / L : row0;
-    if (row >= live) break;
-    Joined<DT> x;
-    if (kFew) {
+  if constexpr (!kFew) {
+    join_rows<DT>(a, t, head, group, slot, count, kWideRows, live);
+  } else {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    constexpr int L = Joined<DT>::L, G = 64 / L;
+    for (int row = (blockIdx.y * 4 + wave) * G + lane / L; row < live; row += 4 * gridDim.y * G) {
+      Joined<DT> x;
       x.template gather<4>(slot, 0, 1, count, kWideRows, row, lane);
-    } else {
-      x.template gather<8>(slot, lane / L, G, count, kWideRows, row, lane);
-      x.add_groups();
+      x.write(a, t, head, group, row, lane);
     }
-    if (kFew || lane < L) x.write(a, t, head, group, row, lane);
   }
 }
 
-// Splits of the keys of a tile: until every CU has the blocks that it takes, twice over,
-// where three quarters of them are not there without (32 heads of 128 over 32000: 800
-// tokens, 208 units, 513 us, until once over 578; 1300 tokens, 336 units, 714 and in
-// one part 865; 1700 tokens, 432 units, 946 in one part and 987 in two).
+// Splits of the keys of a tile: as many as there are blocks for at a time, if that is two
+// or more (3 x 440 tokens over 3011, 8 heads of 64: 30 us, twice as many 40; 32 heads of
+// 128 over 32000, 800 tokens, 208 units: 493 and 513); else as many as for twice over
+// (1300 tokens, 336 units: 714, in one part 865), but in one part from three quarters on
+// (1700 tokens, 432 units: 946, in two parts 987).
 int wide_splits(int64_t units, int dim) {
   const int64_t want = 256 * wide_blocks(dim);
   if (4 * units >= 3 * want) return 1;
-  const int64_t s = 2 * want / units;
+  const int64_t s = want / units > 1 ? want / units : 2 * want / units;
   return (int)(s < 64 ? s : 64);
 }
 
@@ -1128,54 +1174,20 @@ void attend_narrow_kernel(AttendArgs a, float* parts, Cut* cuts) {
 }
 
 // Blocks (x, y) join the tile that block x of the kernel above began and others went on
-// with: a wave a row, or, of more parts than a wave reads in two turns, a block a row,
-// whose waves take every fourth turn and whose first adds the four up in order (3
-// sequences of 19 tokens over up to 92000, one kv head of 192 values, 85 parts: 12.3
-// us, with a wave a row 38.6; 21 parts of 64 values: 13.5 with a block a row, 5.8 with a
-// wave).
+// with.
 template <int DT, int NT>
 __global__ __launch_bounds__(kThreads) void attend_narrow_join_kernel(AttendArgs a, const float* parts, const Cut* cuts) {
-  constexpr int kRows = 32 * NT, L = Joined<DT>::L, G = 64 / L;
-  __shared__ f32x4 sums[3][L];
-  __shared__ float marks[3][2];
+  constexpr int kRows = 32 * NT;
   const Cut cut = cuts[blockIdx.x];
-  const int group = a.hq / a.cache.heads;
   Tile t{};
   t.start = cut.start;
   t.rows = cut.rows;
   t.first = cut.first;
   const int live = t.rows - t.first < kRows ? t.rows - t.first : kRows;   // 0: no tile
   const int64_t x = blockIdx.x, blocks = gridDim.x;
-  const int count = cut.last - (int)x + 1, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  auto slot = [&](int z) { return parts + (z ? x + z : blocks + x) * slot_floats<DT>(kRows); };
-  if (count <= 16 * G) {
-    const int row = blockIdx.y * 4 + wave;   // there is a wave for each
-    if (row >= live) return;
-    Joined<DT> j;
-    j.template gather<8>(slot, lane / L, G, count, kRows, row, lane);
-    j.add_groups();
-    if (lane < L) j.write(a, t, cut.head, group, row, lane);
-    return;
-  }
-  for (int row = blockIdx.y; row < live; row += gridDim.y) {
-    Joined<DT> j;
-    j.template gather<8>(slot, wave * G + lane / L, 4 * G, count, kRows, row, lane);
-    j.add_groups();
-    if (wave && lane < L) {
-      sums[wave - 1][lane] = j.o;
-      if (lane == 0) {
-        marks[wave - 1][0] = j.top;
-        marks[wave - 1][1] = j.sum;
-      }
-    }
-    __syncthreads();
-    if (threadIdx.x < L) {
-#pragma unroll
-      for (int w = 0; w < 3; ++w) j.add(marks[w][0], marks[w][1], sums[w][lane]);
-      j.write(a, t, cut.head, group, row, lane);
-    }
-    __syncthreads();
-  }
+  join_rows<DT>(a, t, cut.head, a.hq / a.cache.heads,
+                [&](int z) { return parts + (z ? x + z : blocks + x) * slot_floats<DT>(kRows); }, cut.last - (int)x + 1,
+                kRows, live);
 }
 
 // ---- which of them -----------------------------------------------------------------------
@@ -1238,7 +1250,6 @@ hipError_t launch_narrow(const AttendArgs& a, float* parts, hipStream_t s) {
   hipLaunchKernelGGL(kernel, dim3(blocks), dim3(kThreads), shm, s, a, parts, cuts);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  static_assert(8192 / blocks * 4 >= 32 * NT, "a wave for each row");
   hipLaunchKernelGGL((attend_narrow_join_kernel<DT, NT>), dim3(blocks, 8192 / blocks), dim3(kThreads), 0, s, a, parts, cuts);
   return hipGetLastError();
 }
