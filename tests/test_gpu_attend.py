@@ -281,3 +281,15 @@ def test_many_and_few_parts(q3, new, length, hq, hk, d):
     _check(p, q, out, lse, d ** -0.5, 0)
     out2, lse2 = _run(q3, p, q, d ** -0.5, 700)
     _check(p, q, out2, lse2, d ** -0.5, 700)
+
+
+@pytest.mark.parametrize("d", [64, 112, 256])
+@pytest.mark.parametrize("new,length", [([300], [500]), ([150, 1, 0, 151], [460, 77, 30, 151])])
+@pytest.mark.parametrize("hk", [1, 2, 4])
+def test_heads_that_xcds_share(q3, hk, new, length, d):
+    # fewer kv heads than XCDs and many tiles, in parts
+    rng = np.random.default_rng(18)
+    p = Paged(rng, new, length, hk, d, 32)
+    q = _q(rng, p.m, 32, d)
+    out, lse = _run(q3, p, q, d ** -0.5, 0)
+    _check(p, q, out, lse, d ** -0.5, 0)
