@@ -15,6 +15,7 @@
 #include "q3_device.h"
 #include "q3_internal.h"
 #include "q3_paged.h"
+#include "q3_span.h"
 
 namespace q3 {
 namespace {
@@ -23,7 +24,6 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kMaxKey = 0x7FFFF000;   // positions stay below it, so sums with a step do not pass 2^31
 
 // A tile of `size` rows of one sequence.  Tiles of sequence s are numbered from
 // q_start[s] * group / size + s on: a sequence of n rows has at most n / size + 1
@@ -78,22 +78,9 @@ __device__ __forceinline__ Tile find_tile(const AttendArgs& a, int64_t tile, int
 __device__ __forceinline__ int position_of(const Tile& t, int row, int group) {
   return t.length - (t.end - (t.start + row / group));
 }
-// One below the first position that a token at `position` sees.
-__device__ __forceinline__ int below_window(const AttendArgs& a, int position) {
-  const int64_t low = a.window ? (int64_t)position - a.window : -1;
-  return low > -1 ? (int)low : -1;
-}
-struct Span {
-  int lo, hi;   // hi == lo: nothing
-};
 __device__ __forceinline__ Span span_of(const AttendArgs& a, const Tile& t, int r0, int r1, int group) {
-  const int64_t held = a.batch.table_pages << a.cache.shift;
-  int64_t hi = (int64_t)position_of(t, r1 - 1, group) + 1;
-  if (hi > held) hi = held;
-  if (hi > kMaxKey) hi = kMaxKey;
-  const int64_t lo = below_window(a, position_of(t, r0, group)) + 1;
-  if (hi < lo) hi = lo;
-  return {(int)lo, (int)hi};
+  return span_between(position_of(t, r0, group), position_of(t, r1 - 1, group), a.window, a.batch.table_pages,
+                      a.cache.shift);
 }
 
 // ---- keys and values on their way to LDS ------------------------------------------
@@ -307,7 +294,7 @@ struct Wave {
       const int64_t token = t.start + r / group;
       const int qhead = head * group + r % group;
       position[n] = position_of(t, r, group);
-      low[n] = below_window(a, position[n]);
+      low[n] = below_window(a.window, position[n]);
 #pragma unroll
       for (int k = 0; k < DT / 16; ++k) {
         u32x4 u = {0u, 0u, 0u, 0u};
@@ -629,9 +616,6 @@ __device__ __forceinline__ int parts_of(int steps, int splits) {
   const int most = (steps + 2) / 3;
   return most < splits ? (most > 0 ? most : 1) : splits;
 }
-__device__ __forceinline__ int steps_of(const Span& span) {
-  return (span.hi - (span.lo & ~(kStep - 1)) + kStep - 1) / kStep;
-}
 
 // Whether XCDs share heads.  Not with a few tiles, whose parts have to go round (89 tokens
 // over 16464, 2 heads of 192: 41 us, 62 with both heads' parts on an XCD each).
@@ -692,7 +676,7 @@ void attend_wide_kernel(AttendArgs a, int splits, float* parts) {
   if (t.sequence == a.batch.sequences) return;
   const int live = t.rows - t.first < kWideRows ? t.rows - t.first : kWideRows;
   const Span span = span_of(a, t, t.first, t.first + live, group);
-  const int begin = span.lo & ~(kStep - 1), steps = steps_of(span);
+  const int begin = first_of(span, kStep), steps = steps_of(span, kStep);
   const int count = parts_of(steps, splits);
   if (z >= count) return;
   const int s0 = (int)((int64_t)steps * z / count), s1 = (int)((int64_t)steps * (z + 1) / count);
@@ -700,7 +684,7 @@ void attend_wide_kernel(AttendArgs a, int splits, float* parts) {
   Wave<DT, 1> w;
   w.init(a, t, head, group, 32 * wave, live, lane);
   const int first_position = position_of(t, t.first, group);   // of the tile's rows
-  const int last_low = below_window(a, position_of(t, t.first + live - 1, group));
+  const int last_low = below_window(a.window, position_of(t, t.first + live - 1, group));
   const bool mine = 32 * wave < live;
   // A wave brings 16 keys of a step, and their values.
   const int keys16 = 16 * wave;
@@ -831,7 +815,7 @@ __global__ __launch_bounds__(kThreads) void attend_wide_join_kernel(AttendArgs a
   const Tile t = find_tile(a, tile, group, kWideRows, threadIdx.x & 63);
   if (t.sequence == a.batch.sequences) return;
   const int live = t.rows - t.first < kWideRows ? t.rows - t.first : kWideRows;
-  const int count = parts_of(steps_of(span_of(a, t, t.first, t.first + live, group)), splits);
+  const int count = parts_of(steps_of(span_of(a, t, t.first, t.first + live, group), kStep), splits);
   if (count == 1) return;
   const float* first = parts + ((int64_t)tile * hk + head) * splits * slot_floats<DT>(kWideRows);
   auto slot = [&](int z) { return first + z * slot_floats<DT>(kWideRows); };
@@ -916,8 +900,7 @@ __device__ __forceinline__ Share share_of(const AttendArgs& a, int s, int group,
   w.t.length = length > 0 ? length : 0;
   w.span = span_of(a, w.t, 0, w.t.rows, group);
   w.tiles = (w.t.rows + size - 1) / size;
-  const int begin = w.span.lo & ~(kNarrowStep - 1);
-  w.steps = (w.span.hi - begin + kNarrowStep - 1) / kNarrowStep;
+  w.steps = steps_of(w.span, kNarrowStep);
   if (w.steps < 1) w.steps = 1;   // rows that see nothing are written too
   return w;
 }
@@ -1003,10 +986,10 @@ void attend_narrow_kernel(AttendArgs a, float* parts, Cut* cuts) {
     Tile t = sh.t;
     t.first = (unit - head * sh.tiles) * kRows;
     const int live = t.rows - t.first < kRows ? t.rows - t.first : kRows;
-    const int begin = sh.span.lo & ~(kNarrowStep - 1);
+    const int begin = first_of(sh.span, kNarrowStep);
     const int first_position = position_of(t, t.first, group);
     const int last_position = position_of(t, t.first + live - 1, group);
-    const int last_low = below_window(a, last_position);
+    const int last_low = below_window(a.window, last_position);
     const bool complete = c0 == 0 && n == sh.steps;
     if (c0 == 0 && !complete) {
       const int64_t last = at + sh.steps - 1;   // the tile's last step

@@ -190,7 +190,7 @@ typedef struct q3_paged_cache {
  * table row names.
  * Entries are checked on the device: a position that is negative or past the
  * table, or whose page is outside [0, pages), is not there -- it is not written,
- * and attention does not see it. */
+ * and attention does not see it.  Attention sees positions below 2^31 - 4096. */
 typedef struct q3_paged_batch {
   int64_t sequences;
   const int32_t* q_start;

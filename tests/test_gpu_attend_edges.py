@@ -1,0 +1,51 @@
+"""q3_paged_attention at the ends of its tables, lengths and windows."""
+import numpy as np
+import pytest
+import torch
+
+from paged_util import Paged, cuda
+from test_gpu_attend import FORMS, _q
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def q3():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import bit_fp8_codebook_amd as q3
+    q3.lib()
+    return q3
+
+
+BIG = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("window", [1, 63, 64, 127, 4096])
+@pytest.mark.parametrize("length", [BIG, BIG - 63, BIG - 127, BIG - 4095, BIG - 4200, 2 ** 30])
+@pytest.mark.parametrize("form", FORMS)
+def test_windows_far_behind_the_table_see_nothing(q3, form, length, window):
+    new, hq, hk = form
+    p = Paged(np.random.default_rng(21), [new, 1], [new + 30, 20], hk, 64, 16, stale=float("nan"))
+    cache, _ = p.on_device(q3)
+    q = _q(np.random.default_rng(22), p.m, hq, 64)
+    out, lse = torch.full_like(q, 2.0), torch.full((p.m, hq), 2.0, device="cuda")
+    far = cuda(np.array([length, length], np.int32))
+    q3.q3_paged_attention(q, cache, q3.PagedBatch(cuda(p.start), far, cuda(p.table)), window=window, out=out, lse=lse)
+    assert not out.any() and (lse == -np.inf).all()
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_far_tokens_without_a_window_see_the_whole_table(q3, form):
+    new, hq, hk = form
+    p = Paged(np.random.default_rng(23), [new, 1], [160, 160], hk, 64, 16)
+    cache, _ = p.on_device(q3)
+    q = _q(np.random.default_rng(24), p.m, hq, 64)
+
+    def run(length, window):
+        batch = q3.PagedBatch(cuda(p.start), cuda(np.array([length, length], np.int32)), cuda(p.table))
+        return q3.q3_paged_attention(q, cache, batch, window=window, want_lse=True)
+    near = run(160 + new, 0)     # the table ends in front of every new token
+    for length, window in ((2 ** 30, 0), (BIG, 0), (BIG, BIG), (BIG - 4200, BIG - 4200)):
+        far = run(length, window)
+        assert torch.equal(near[0], far[0]) and torch.equal(near[1], far[1]), (length, window)
