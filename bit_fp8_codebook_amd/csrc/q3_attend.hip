@@ -1127,11 +1127,11 @@ void attend_narrow_kernel(AttendArgs a, float* parts, Cut* cuts) {
               v += *reinterpret_cast<const f32x4*>(buf + (k * kRows + row) * kPitch + e);
               top = fmaxf(top, marks[k][row][0]);
             }
+            // (A wave whose scores are all NaN has the lowest maximum and a sum that counts.)
+            const float floor_ = top == -INFINITY ? 0.f : top;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float m = marks[k][row][0];
-              sum += m == -INFINITY ? 0.f : marks[k][row][1] * __builtin_amdgcn_exp2f(m - top);
-            }
+            for (int k = 0; k < 4; ++k)
+              sum += marks[k][row][1] * __builtin_amdgcn_exp2f(marks[k][row][0] - floor_);
             if (complete) {
               const int r = t.first + row;
               const int64_t token = t.start + r / group;

@@ -49,3 +49,37 @@ def test_far_tokens_without_a_window_see_the_whole_table(q3, form):
     for length, window in ((2 ** 30, 0), (BIG, 0), (BIG, BIG), (BIG - 4200, BIG - 4200)):
         far = run(length, window)
         assert torch.equal(near[0], far[0]) and torch.equal(near[1], far[1]), (length, window)
+
+
+@pytest.mark.parametrize("d", [64, 128, 192])
+@pytest.mark.parametrize("extra", [32, 200])
+@pytest.mark.parametrize("form", FORMS)
+def test_nan_reaches_the_lse_of_the_rows_that_see_it(q3, form, extra, d):
+    # a NaN score makes the sum NaN; -inf is the lse of rows that see nothing, and no other
+    new, hq, hk = form
+    length = new + extra
+    p = Paged(np.random.default_rng(25), [new, 1], [length, 40], hk, d, 16)
+    q = _q(np.random.default_rng(26), p.m, hq, d)
+
+    def run(q):
+        cache, batch = p.on_device(q3)
+        return q3.q3_paged_attention(q, cache, batch, want_lse=True)
+    x = run(q)
+    dirty = q.clone()
+    dirty[new - 1, d * (hq - 1) + 3] = float("nan")
+    y = run(dirty)
+    keep = torch.ones(p.m, hq, dtype=torch.bool, device="cuda")
+    keep[new - 1, hq - 1] = False
+    assert torch.equal(x[1][keep], y[1][keep]) and torch.isnan(y[1][~keep]).all()
+    assert torch.isnan(y[0].view(p.m, hq, d)[~keep]).all()
+    # one position's key: alone in its wave's tiles at 32 of 33, first, and last of all
+    for at in {0, min(32, length - 1), length - 1}:
+        page, place = int(p.table[0, at // 16]), at % 16
+        was = p.k[page, :, place, 5].clone()
+        p.k[page, :, place, 5] = float("nan")
+        y = run(q)
+        p.k[page, :, place, 5] = was
+        sees = torch.zeros(p.m, dtype=torch.bool, device="cuda")
+        sees[:new] = torch.arange(length - new, length, device="cuda") >= at
+        assert torch.isnan(y[1][sees]).all() and torch.isnan(y[0][sees]).all(), at
+        assert torch.equal(x[1][~sees], y[1][~sees]) and torch.equal(x[0][~sees], y[0][~sees]), at
