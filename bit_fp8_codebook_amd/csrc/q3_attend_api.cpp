@@ -16,9 +16,11 @@ namespace {
 constexpr int32_t kMaxHeads = 1024;
 constexpr int64_t kMaxRows = int64_t(1) << 24;   // attention and scored rows, exclusive
 constexpr int64_t kMaxVocabulary = int64_t(1) << 19;
+constexpr float kLog2e = 1.4426950408889634f;
 
 bool bad_head_dim(int64_t d) { return d < 16 || d > 256 || d % 16; }
-bool bad_temperature(float t) { return !(t > 0.f) || !std::isfinite(t) || !std::isfinite(1.f / t); }
+// The kernels take 1 / t, and 1 / t as a power of two.
+bool bad_temperature(float t) { return !(t > 0.f) || !std::isfinite(t) || !std::isfinite(1.f / t * kLog2e); }
 bool bad_heads(int64_t h) { return h < 1 || h > kMaxHeads; }
 
 q3_status check_cache(const q3_paged_cache* c) {

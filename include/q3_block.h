@@ -320,8 +320,8 @@ Q3_API q3_status q3_sample(const float* logits, int64_t m, int64_t n, int64_t ld
  * top), if some logits are +inf only those count; a row with nothing else gives
  * logprob -inf (0 without a target) and entropy 0.  Unfilled places of top hold -1 and -inf.
  * logits fp32 [m][ld], 1 <= n <= 2^19, 1 <= m < 2^24; targets int32 [m], device;
- * temperature > 0, it and its reciprocal finite.  workspace: 256-byte aligned,
- * q3_logprobs_workspace_bytes(m, n, top) bytes. */
+ * temperature > 0, it and log2(e) / temperature finite (from 4.24e-39 on).
+ * workspace: 256-byte aligned, q3_logprobs_workspace_bytes(m, n, top) bytes. */
 Q3_API int64_t q3_logprobs_workspace_bytes(int64_t m, int64_t n, int32_t top);
 Q3_API q3_status q3_logprobs(const float* logits, int64_t m, int64_t n, int64_t ld, const int32_t* targets,
                              float temperature, int32_t top, float* logprobs, float* entropy, int32_t* top_ids,

@@ -1,0 +1,12 @@
+"""Where the arguments of the attention sublayer's and the log probabilities' entry
+points end, without a GPU: refusals before any HIP call."""
+import pytest
+
+from test_block_abi import FAKE, L  # noqa: F401
+
+
+@pytest.mark.parametrize("t", [4.23e-39, 3e-39, 2.95e-39, 1e-45])
+def test_temperatures_too_cold(L, t):  # noqa: F811
+    # 1 / t is still finite in fp32 down to 2.94e-39, log2(e) / t only to 4.24e-39
+    assert L.q3_logprobs(FAKE, 2, 100, 100, FAKE, t, 0, FAKE, None, None, None, None, None, 0, None) == 1
+    assert L.q3_logprobs_backward(FAKE, 2, 100, 100, FAKE, t, FAKE, FAKE, None, FAKE + 4096, 100, 1, None) == 1
