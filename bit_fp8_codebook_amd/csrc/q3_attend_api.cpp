@@ -21,6 +21,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 bool bad_head_dim(int64_t d) { return d < 16 || d > 256 || d % 16; }
 // The kernels take 1 / t, and 1 / t as a power of two.
 bool bad_temperature(float t) { return !(t > 0.f) || !std::isfinite(t) || !std::isfinite(1.f / t * kLog2e); }
+// The kernels take |scale| as a power of two.
+bool bad_scale(float s) { return !std::isnormal(s) || !std::isfinite(s * kLog2e); }
 bool bad_heads(int64_t h) { return h < 1 || h > kMaxHeads; }
 
 q3_status check_cache(const q3_paged_cache* c) {
@@ -213,7 +215,7 @@ Q3_API q3_status q3_paged_attention(const uint16_t* q, int64_t ldq, int32_t head
   if (st != Q3_OK) return st;
   if ((st = check_batch(batch)) != Q3_OK) return st;
   if (bad_attention(m, batch->sequences, heads_q, cache->heads)) return Q3_ERR_UNSUPPORTED_SHAPE;
-  if (window < 0 || !std::isnormal(scale)) return Q3_ERR_INVALID_ARG;
+  if (window < 0 || bad_scale(scale)) return Q3_ERR_INVALID_ARG;
   const int64_t n = int64_t(heads_q) * cache->head_dim;
   if ((st = check_rows(q, ldq, n, 2)) != Q3_OK) return st;
   if ((st = check_rows(out, ldo, n, 2)) != Q3_OK) return st;

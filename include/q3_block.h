@@ -267,10 +267,10 @@ Q3_API q3_status q3_qk_norm_rope_backward(const q3_head_norms* heads, const floa
  * zeros and lse -inf; rows that belong to no sequence are left as they are.
  * What a token does not see cannot reach its row, whatever it holds (infinities
  * and NaN too).  Scores, sums and products are fp32; the weights e^(S - max)
- * enter the second product as bf16.  scale: finite, normal (its size at least
- * 2^-126).  1 <= m < 2^24, m * heads_q < 2^30, sequences * heads < 2^23.
- * workspace: 256-byte aligned, q3_paged_attention_workspace_bytes(m, sequences,
- * heads_q, heads, head_dim) bytes. */
+ * enter the second product as bf16.  scale: normal (its size at least 2^-126),
+ * scale log2(e) finite (its size up to 2.35e38).  1 <= m < 2^24,
+ * m * heads_q < 2^30, sequences * heads < 2^23.  workspace: 256-byte aligned,
+ * q3_paged_attention_workspace_bytes(m, sequences, heads_q, heads, head_dim) bytes. */
 Q3_API int64_t q3_paged_attention_workspace_bytes(int64_t m, int64_t sequences, int32_t heads_q, int32_t heads,
                                                   int32_t head_dim);
 Q3_API q3_status q3_paged_attention(const uint16_t* q, int64_t ldq, int32_t heads_q, const q3_paged_cache* cache,

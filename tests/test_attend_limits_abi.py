@@ -2,6 +2,7 @@
 points end, without a GPU: refusals before any HIP call."""
 import pytest
 
+from test_attend_abi import _batch, _cache, _ref
 from test_block_abi import FAKE, L  # noqa: F401
 
 
@@ -10,3 +11,10 @@ def test_temperatures_too_cold(L, t):  # noqa: F811
     # 1 / t is still finite in fp32 down to 2.94e-39, log2(e) / t only to 4.24e-39
     assert L.q3_logprobs(FAKE, 2, 100, 100, FAKE, t, 0, FAKE, None, None, None, None, None, 0, None) == 1
     assert L.q3_logprobs_backward(FAKE, 2, 100, 100, FAKE, t, FAKE, FAKE, None, FAKE + 4096, 100, 1, None) == 1
+
+
+@pytest.mark.parametrize("scale", [2.36e38, -2.36e38, 3.4e38])
+def test_scales_too_large(L, scale):  # noqa: F811
+    # scale is finite in fp32 up to 3.4e38, scale log2(e) only to 2.35e38
+    assert L.q3_paged_attention(FAKE, 256, 4, _ref(_cache()), _ref(_batch()), scale, 0, FAKE, 256, FAKE, 3, FAKE,
+                                1 << 40, None) == 1

@@ -83,3 +83,27 @@ def test_nan_reaches_the_lse_of_the_rows_that_see_it(q3, form, extra, d):
         sees[:new] = torch.arange(length - new, length, device="cuda") >= at
         assert torch.isnan(y[1][sees]).all() and torch.isnan(y[0][sees]).all(), at
         assert torch.equal(x[1][~sees], y[1][~sees]) and torch.equal(x[0][~sees], y[0][~sees]), at
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_scales_up_to_the_largest(q3, form):
+    # scale log2(e) has to be finite: the largest such scale gives zero scores their mean, the next is refused
+    new, hq, hk = form
+    p = Paged(np.random.default_rng(27), [new], [new + 40], hk, 64, 16)
+    cache, batch = p.on_device(q3)
+    q = torch.zeros(new, hq * 64, dtype=torch.bfloat16, device="cuda")
+    log2e = np.float32(1.4426950408889634)
+    scale = np.finfo(np.float32).max / log2e
+    with np.errstate(over="ignore"):
+        while np.isfinite(np.nextafter(scale, np.float32(np.inf)) * log2e):
+            scale = np.nextafter(scale, np.float32(np.inf))
+        while not np.isfinite(scale * log2e):
+            scale = np.nextafter(scale, np.float32(0))
+    want = q3.q3_paged_attention(q, cache, batch, 1.0, want_lse=True)
+    for s in (float(scale), -float(scale)):
+        got = q3.q3_paged_attention(q, cache, batch, s, want_lse=True)
+        assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1]), s
+    above = float(np.nextafter(scale, np.float32(np.inf)))
+    for s in (above, -above, float(np.finfo(np.float32).max)):
+        with pytest.raises(q3.Q3Error):
+            q3.q3_paged_attention(q, cache, batch, s)
