@@ -201,13 +201,16 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(RopeArgs a) {
     }
   };
   const int first = blockIdx.y * kHeads;
-  load(first);
   const Vec8 wq = weight8(a.wq, at), wk = weight8(a.wk, at);
 
+  int s = 0;
+  if (a.batch.sequences) {
+    s = find_sequence(a.batch, (int)row, lane);
+    if (s == a.batch.sequences) return;   // the whole block; its row need not be there
+  }
+  load(first);   // beside what the tables say of the row
   int64_t position = 0, page = -1;
   if (a.batch.sequences) {
-    const int s = find_sequence(a.batch, (int)row, lane);
-    if (s == a.batch.sequences) return;   // the whole block
     position = (int64_t)a.batch.kv_len[s] - (a.batch.q_start[s + 1] - row);
     page = find_page(a.batch, a.cache, s, position);
   }
