@@ -63,7 +63,7 @@ q3::BatchView view_of(const q3_paged_batch* b) {
   v.kv_len = b->kv_len;
   v.table = b->page_table;
   v.ld_table = b->ld_table;
-  v.table_pages = b->table_pages;
+  v.table_pages = b->table_pages < kMaxM ? b->table_pages : kMaxM;   // no position is past 2^31
   v.sequences = static_cast<int32_t>(b->sequences);
   return v;
 }

@@ -24,10 +24,11 @@ struct Span {
 // of 1 << shift positions.  Where they see nothing the span is [0, 0): a window may
 // begin far behind the table's end, up to 2^31, where no step can be added.
 __host__ __device__ __forceinline__ Span span_between(int first, int last, int32_t window, int64_t pages, int shift) {
-  const int64_t held = pages > (kMaxKey >> shift) ? kMaxKey : pages << shift;
-  const int64_t lo = (int64_t)below_window(window, first) + 1;
+  const int64_t held = pages << shift;   // the host keeps `pages` to 2^31
   int64_t hi = (int64_t)last + 1;
   if (hi > held) hi = held;
+  if (hi > kMaxKey) hi = kMaxKey;
+  const int64_t lo = below_window(window, first) + 1;
   if (hi <= lo) return {0, 0};
   return {(int)lo, (int)hi};
 }

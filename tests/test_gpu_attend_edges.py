@@ -107,3 +107,18 @@ def test_scales_up_to_the_largest(q3, form):
     for s in (above, -above, float(np.finfo(np.float32).max)):
         with pytest.raises(q3.Q3Error):
             q3.q3_paged_attention(q, cache, batch, s)
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_a_table_that_claims_more_pages_than_positions(q3, form):
+    # table_pages up to ld_table, whatever that is: 2^60 pages of 16 are more positions than 64 bits hold
+    from bit_fp8_codebook_amd import _block
+    new, hq, hk = form
+    p = Paged(np.random.default_rng(28), [new], [new + 70], hk, 64, 16)
+    cache, batch = p.on_device(q3)
+    q = _q(np.random.default_rng(29), new, hq, 64)
+    want = q3.q3_paged_attention(q, cache, batch, want_lse=True)
+    batch._desc = _block.Q3PagedBatch(1, batch.q_start.data_ptr(), batch.kv_len.data_ptr(), batch.page_table.data_ptr(),
+                                      1 << 60, 1 << 60)
+    got = q3.q3_paged_attention(q, cache, batch, want_lse=True)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
