@@ -590,6 +590,8 @@ def q3_paged_attention(q: torch.Tensor, cache: PagedCache, batch: PagedBatch, sc
     want_lse (or lse given) -> (out, lse), lse float32 [m][heads_q].  Tokens that see
     nothing get zeros and -inf; rows that belong to no sequence are not written.
     For inference: not recorded by autograd."""
+    if not 0 <= window < 1 << 31:   # the C call's 32 bits would take another one
+        raise ValueError(f"window must be 0..2^31 - 1, got {window}")
     if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 2:
         raise ValueError("q must be a device tensor bfloat16 [m][heads_q * head_dim]")
     (m, n), dev = q.shape, q.device

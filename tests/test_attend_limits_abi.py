@@ -18,3 +18,12 @@ def test_scales_too_large(L, scale):  # noqa: F811
     # scale is finite in fp32 up to 3.4e38, scale log2(e) only to 2.35e38
     assert L.q3_paged_attention(FAKE, 256, 4, _ref(_cache()), _ref(_batch()), scale, 0, FAKE, 256, FAKE, 3, FAKE,
                                 1 << 40, None) == 1
+
+
+@pytest.mark.parametrize("window", [-1, 1 << 31, (1 << 32) + 5, 1 << 40])
+def test_the_binding_takes_no_window_past_32_bits(window):
+    # as an int32 the last two would be windows of 5 and of 0, which is none at all
+    import torch
+    from bit_fp8_codebook_amd import _block as b
+    with pytest.raises(ValueError, match="window"):
+        b.q3_paged_attention(torch.zeros(3, 256, dtype=torch.bfloat16), None, None, window=window)
