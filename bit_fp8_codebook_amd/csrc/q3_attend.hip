@@ -111,15 +111,17 @@ __device__ const u32x4 kZeros = {0u, 0u, 0u, 0u};   // what stands behind a head
 
 // One wave's 1 KB from memory to LDS: lane l's 16 bytes land at dst + 16 l.  As
 // assembly, because the compiler would make every transposing LDS read wait for
-// all of them; the kernels wait for the ones they need.
+// all of them; the kernels wait for the ones they need.  The target stands in m0,
+// which the compiler sets (written here and named as such, heads of 256 in chunks
+// lose 3%); the first instruction behind that has to wait a cycle.
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {
   return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)p);   // the low half of a generic address
 }
 __device__ __forceinline__ void load_lds(const void* base, uint32_t offset, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst), "v"(offset), "s"(base) : "memory", "m0");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(dst), "v"(offset), "s"(base) : "memory");
 }
 __device__ __forceinline__ void load_lds(const void* p, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(dst), "v"(p) : "memory", "m0");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"{m0}"(dst), "v"(p) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void wait_loads() {   // until at most N are under way

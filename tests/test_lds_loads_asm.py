@@ -44,7 +44,7 @@ def test_the_compiler_knows_what_the_loads_write(tmp_path):
     for name in ("probe_any", "probe_run"):
         body = text[text.index(f"\n{name}:"):]
         lines = [x.strip() for x in body[:body.index("s_endpgm")].split("\n")]
-        seen = [x for x in lines if re.match(r"s_mov_b32 m0|global_load_lds", x)]
+        seen = [x for x in lines if re.match(r"s_\w+ m0,|global_load_lds", x)]
         loads = [i for i, x in enumerate(seen) if x.startswith("global_load_lds")]
         assert len(loads) == 3, seen
-        assert all(i > 0 and seen[i - 1].startswith("s_mov_b32 m0") for i in loads), seen
+        assert all(i > 0 and " m0," in seen[i - 1] for i in loads), seen
