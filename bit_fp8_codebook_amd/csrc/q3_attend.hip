@@ -9,7 +9,8 @@
 //
 // Few rows are bound by the cache's bytes (64 tokens over up to 16384, 8 kv heads of
 // 128: 437 us, 5.6 TB/s), many by the products, the reads of their fragments and the
-// exponentials (2048 over 32000, 32 heads of 128: 1.02 ms, 1.02 PFLOP/s).
+// exponentials (2048 over 32000, 32 heads of 128: 1.01 to 1.12 ms on several cards, 0.93
+// to 1.03 PFLOP/s).
 #include <type_traits>
 
 #include "q3_device.h"
@@ -655,7 +656,7 @@ void attend_wide_kernel(AttendArgs a, int splits, float* parts) {
 
   // An XCD takes whole heads, or every so manieth tile of one: tiles that read the same
   // keys share an L2, and the XCDs have as much to do (4 kv heads of 256, 2048 tokens of
-  // 16 heads over 16000: 670 us, with a run of tiles for each XCD, of which one had a
+  // 16 heads over 16000: 674 us, with a run of tiles for each XCD, of which one had a
   // block more than CUs, 1282; 4096 over 4096: 218 and 406).
   const uint32_t tiles = (uint32_t)tiles_of(a.m, a.batch.sequences, group, kWideRows);
   const uint32_t total = wide_units(tiles, hk);   // below 2^24
@@ -863,10 +864,9 @@ int wide_splits(int64_t units, int dim) {
 constexpr int kNarrowStep = 128;
 // Blocks of a CU, as many as registers allow, so that some stream while another begins
 // or ends a tile, and how many tiles of keys, and of values, a wave's part of LDS holds.
-// Heads of 128, two blocks with one tile each against one block with two: 64 single
-// tokens over up to 500 positions 36 and 55 us, over up to 16384 359 and 372.  Heads of
-// 64, three with one tile against two with two: 22 and 26, 200 and 199 (four: 37 and
-// 281, spilled).
+// 8 kv heads of 128, two blocks with one tile each against one block with two: 64 single
+// tokens over up to 500 positions 35 and 58 us, over up to 16384 436 and 455.  Heads of
+// 64, three with one tile against two with two: 24 and 28, 230 and 234 (four spill).
 template <int DT, int NT>
 constexpr int per_cu() { return NT == 1 ? (DT <= 64 ? 3 : DT <= 128 ? 2 : 1) : DT <= 64 ? 2 : 1; }
 template <int DT, int NT>
@@ -1183,7 +1183,7 @@ enum Form { kNarrow32, kNarrow64, kWide };
 // (narrow, 64) and 164, at 72 rows 230 (narrow, 64) and 166; of 256 values at 32 rows
 // 247 and 299, at 48 (narrow, 32: two tiles) 556 and 388 (two tiles at a time do not fit
 // a wave's registers there).  Unlike lengths are a reason for the narrow ones besides:
-// 64 single tokens over up to 16384, heads of 192, 533 us and 829.
+// 64 single tokens over up to 16384, 8 kv heads of 192, 660 us and 940.
 Form form_of(int64_t m, int64_t sequences, int group, int dim) {
   const int64_t rows = m * group;
   if (rows <= 32 * sequences) return kNarrow32;

@@ -389,8 +389,8 @@ __global__ __launch_bounds__(256) void logprobs_back_kernel(LogprobBackArgs a, i
 }
 
 // Parts of a row: blocks for the whole chip where rows are few, whole chunks each (64
-// rows of 151936, best 20: 28 us a call with about 512 blocks, 28 with 1024, 30 with 2048,
-// whose lists cost more to join; one row of 32000 22 with any).
+// rows of 151936, best 20: 27 us a call with about 512 blocks or 1024, 29 with 2048,
+// whose lists cost more to join; one row of 32000 20 to 22 with any).
 int parts_of(int64_t m, int64_t n) {
   const int64_t chunks = (n + kChunk - 1) / kChunk, want = (1024 + m - 1) / m;
   const int64_t each = (chunks + want - 1) / want;

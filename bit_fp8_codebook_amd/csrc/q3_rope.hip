@@ -16,10 +16,11 @@
 // token's angles are formed once by the block while the first heads' loads are
 // under way.
 //
-// Measured: 4 prompts' 6054 tokens of 32 + 2 x 8 heads of 128 40 us, 5.6 TB/s (with a
+// Measured: 4 prompts' 6054 tokens of 32 + 2 x 8 heads of 128 39 us, 5.7 TB/s (with a
 // kernel for all pairings 46, with halves through LDS and angles by the library's sine
-// 70); one token 4.3 us.  Backward, 4095 tokens of 80 heads of 128, 56 us, 6.0 TB/s, and 4.7 for the
-// weights' sums (with a kernel for all pairings 92).
+// 70); one token 4.3 us.  Backward, 4095 tokens of 80 heads of 128: 74 us on fresh rows,
+// 4.5 TB/s (83 with fp32 gradients, 5.0), 56 where a third of them is in the memory-side
+// cache, and 4 for the weights' sums (a call 77, with a kernel for all pairings 92).
 #include <type_traits>
 
 #include "q3_device.h"

@@ -317,8 +317,9 @@ Q3_API q3_status q3_sample(const float* logits, int64_t m, int64_t n, int64_t ld
  *   stats fp32 [m][4]: the largest logit, ln sum e^(z - max z), entropy, 0 (may be
  *     NULL): what the backward pass takes; 16-byte aligned
  * Masks as in q3_sample: -inf and NaN have no weight (logprob -inf, never in
- * top), if some logits are +inf only those count; a row with nothing else gives
- * logprob -inf (0 without a target) and entropy 0.  Unfilled places of top hold -1 and -inf.
+ * top), if some logits are +inf only those have any (finite ones follow them in top,
+ * with logprob -inf); a row with nothing else gives logprob -inf (0 without a target)
+ * and entropy 0.  Unfilled places of top hold -1 and -inf.
  * logits fp32 [m][ld], 1 <= n <= 2^19, 1 <= m < 2^24; targets int32 [m], device;
  * temperature > 0, it and log2(e) / temperature finite (from 4.24e-39 on).
  * workspace: 256-byte aligned, q3_logprobs_workspace_bytes(m, n, top) bytes. */
